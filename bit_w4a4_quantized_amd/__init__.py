@@ -8,4 +8,5 @@ from . import binding  # noqa: F401
 from .binding import (  # noqa: F401
     svdq_quantize_down, svdq_gemm_w4a4_up, svdq_linear, svdq_quantize_weight,
     svdq_linear_unfused, svdq_gemm_w4a16, svdq_gelu_tanh_smooth, SvdqError,
+    svdq_add_rmsnorm, svdq_gemm_act_residual, svdq_rope_axes,
 )

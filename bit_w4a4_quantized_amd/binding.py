@@ -24,6 +24,15 @@ FMT_NAMES = {v: k for k, v in FORMATS.items()}
 _lib = None
 
 _c_int, _c_size, _vp = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+_c_i64, _c_float = ctypes.c_int64, ctypes.c_float
+
+
+class RopeOperand(ctypes.Structure):
+    """svdq_rope_operand."""
+    _fields_ = [("inp", _vp), ("out", _vp), ("weight", _vp), ("heads", _c_int), ("in_batch", _c_i64),
+                ("in_token", _c_i64), ("in_head", _c_i64), ("out_batch", _c_i64), ("out_token", _c_i64),
+                ("out_head", _c_i64)]
+
 
 _SIGS = {
     "svdq_code_row_bytes": (_c_size, [_c_int, _c_int]),
@@ -47,6 +56,12 @@ _SIGS = {
                                     _vp, _c_size, _vp, _vp]),
     "svdq_relayout": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "svdq_linear_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp]),
+    "svdq_add_rmsnorm": (_c_int, [_vp, _c_i64, _c_int, _vp, _c_i64, _c_int, _vp, _c_int, _c_float, _c_int, _c_int,
+                                  _c_int, _vp, _vp, _vp, _c_i64, _vp]),
+    "svdq_gemm_act_residual": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_int, _c_int, _c_int, _c_int,
+                                        _c_int, _c_int, _vp, _c_i64, _vp]),
+    "svdq_rope_axes": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _c_i64, _vp, _c_int, _vp,
+                                _c_int, _c_float, _c_int, _vp]),
     "svdq_status_string": (ctypes.c_char_p, [_c_int]),
     "svdq_version": (ctypes.c_char_p, []),
 }
@@ -508,6 +523,252 @@ def svdq_relayout(codes, scales, K, fmt, to_canonical, codes_out=None, scales_ou
     _check("svdq_relayout", lib().svdq_relayout(_p(codes), _p(scales), rows, K, _fmt(fmt), 1 if to_canonical else 0,
                                                 _p(codes_out), _p(scales_out), _stream(stream)))
     return codes_out, scales_out
+
+
+# ------------------------------------------------------------------ a block's operators between its linears
+ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}
+
+
+@functools.lru_cache(maxsize=None)
+def _types():
+    """torch dtype -> svdq_type."""
+    import torch
+    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.int8: 3, torch.float8_e4m3fn: 4}
+
+
+def _rows(t, dtypes, shape, what):
+    """The row stride of a 2-D device tensor whose rows are contiguous (any row stride that keeps
+    them apart); else ValueError.  dtypes: the dtype or dtypes it may have."""
+    if t is None:
+        raise ValueError(f"{what} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} must be one of {dtypes}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{what} must have shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    step, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what}'s rows must be contiguous")
+    if rows <= 1 or cols == 0:
+        return cols
+    if step < cols:
+        raise ValueError(f"{what}'s rows must not overlap")
+    return step
+
+
+def _vector(t, dtypes, n, what):
+    if not t.is_cuda or t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous device tensor of shape ({n},) and one of {dtypes}, "
+                         f"got {tuple(t.shape)} {t.dtype}")
+
+
+def _launch(fn, args, tensors, made, stream):
+    """One C call on the tensors' device: on `stream` when given, else on that device's current
+    stream.  `made`: tensors allocated for this call; the allocator learns that another stream
+    than theirs uses them."""
+    import torch
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = getattr(lib(), fn)(*args, _current(dev.index) if stream is None else stream)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib(), fn)(*args, _current(dev.index) if stream is None else stream)
+    if st != 0:
+        raise SvdqError(fn, st)
+    if stream is not None:
+        for t in made:
+            t.record_stream(torch.cuda.ExternalStream(stream, device=dev))
+
+
+_raw_stream = None
+
+
+def _current(dev_index):
+    global _raw_stream
+    if _raw_stream is None:
+        _raw_stream = _raw_stream_fn()
+    return _raw_stream(dev_index or 0)
+
+
+def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=None, scales=None,
+                     residual_out=None, stream=None):
+    """RMS norm of x [M, K] (fp16 or bf16, rows any stride apart) plus a residual (x's type or
+    fp32), weight [K] (x's type or fp32).  out_format "int8" or "e4m3": codes [M, K] and fp32
+    scales [M], code * scale being the normed value; "same": [M, K] in x's type, no scales.
+    Returns (out, scales, stream): stream = x + residual in the residual's type, None without one.
+    residual_out may be residual, or x where the types agree."""
+    import torch
+    types = _types()
+    xs = _rows(x, (torch.float16, torch.bfloat16), None, "x")
+    M, K = x.shape
+    xd = x.dtype
+    _vector(weight, (xd, torch.float32), K, "weight")
+    if out_format not in ("int8", "e4m3", "same"):
+        raise ValueError(f"out_format must be 'int8', 'e4m3' or 'same', got {out_format!r}")
+    od = torch.int8 if out_format == "int8" else torch.float8_e4m3fn if out_format == "e4m3" else xd
+    made = []
+    rs = ros = rt = 0
+    if residual is not None:
+        rs, rt = _rows(residual, (xd, torch.float32), (M, K), "residual"), types[residual.dtype]
+        if residual_out is not None:
+            ros = _rows(residual_out, (residual.dtype,), (M, K), "residual_out")
+    else:
+        _absent(residual_out, "residual_out", "without a residual")
+    if out is not None:
+        _need(out, od, (M, K), "out")
+    if out_format == "same":
+        _absent(scales, "scales", "for a 16-bit output")
+    elif scales is not None:
+        _need(scales, torch.float32, (M,), "scales")
+    if out is None:
+        out = torch.empty((M, K), dtype=od, device=x.device)
+        made.append(out)
+    if scales is None and od is not xd:
+        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+        made.append(scales)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty((M, K), dtype=residual.dtype, device=x.device)
+        ros = K
+        made.append(residual_out)
+    _launch("svdq_add_rmsnorm",
+            (x.data_ptr(), xs, types[xd], _p(residual), rs, rt, weight.data_ptr(), types[weight.dtype], eps, M, K,
+             types[od], out.data_ptr(), _p(scales), _p(residual_out), ros),
+            (x, weight, residual, out, scales, residual_out), made, stream)
+    return out, scales, residual_out
+
+
+def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none", residual=None, out_dtype=None,
+                           y=None, stream=None):
+    """y = act((x w^T) * xs[:, None] * ws + bias) + residual, rounded once.  x [M, K] and w [N, K]
+    int8, float8_e4m3fn, fp16 or bf16 (x's rows any stride apart); xs [M], ws [N] fp32; bias [N],
+    residual and y [M, N] of out_dtype (fp16 or bf16; x's type, or fp16 for 8-bit x, when None);
+    activation "none", "gelu" (tanh) or "silu".  y may be residual."""
+    import torch
+    types = _types()
+    xt = _rows(x, (torch.int8, torch.float8_e4m3fn, torch.float16, torch.bfloat16), None, "x")
+    M, K = x.shape
+    if w is None or w.dim() != 2:
+        raise ValueError("w must be a device tensor [N, K]")
+    N = int(w.shape[0])
+    _need(w, x.dtype, (N, K), "w")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}, got {activation!r}")
+    if out_dtype is None:
+        out_dtype = x.dtype if x.dtype in (torch.float16, torch.bfloat16) else torch.float16
+    if out_dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"out_dtype must be float16 or bfloat16, got {out_dtype}")
+    if xs is not None:
+        _vector(xs, (torch.float32,), M, "xs")
+    if ws is not None:
+        _vector(ws, (torch.float32,), N, "ws")
+    if bias is not None:
+        _vector(bias, (out_dtype,), N, "bias")
+    rs = 0 if residual is None else _rows(residual, (out_dtype,), (M, N), "residual")
+    made = ()
+    if y is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        made, yt = (y,), N
+    else:
+        yt = _rows(y, (out_dtype,), (M, N), "y")
+    _launch("svdq_gemm_act_residual",
+            (x.data_ptr(), xt, _p(xs), w.data_ptr(), _p(ws), _p(bias), _p(residual), rs, M, N, K, types[x.dtype],
+             ACTIVATIONS[activation], types[out_dtype], y.data_ptr(), yt),
+            (x, w, xs, ws, bias, residual, y), made, stream)
+    return y
+
+
+@functools.lru_cache(maxsize=256)
+def _axis_array(axis_pairs):
+    return (_c_int * len(axis_pairs))(*axis_pairs)
+
+
+def _heads_layout(t, heads_first, what):
+    """(batch, token, head) strides of [batch, tokens, heads, dim] (heads_first: [batch, heads,
+    tokens, dim]), or without the batch; sizes likewise."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{what} must have 3 or 4 dimensions, got {t.dim()}")
+    size, step = tuple(t.shape), t.stride()
+    if step[-1] != 1 and size[-1] > 1:
+        raise ValueError(f"{what}'s heads must be contiguous")
+    if len(size) == 3:
+        size, step = (1, *size), (0, *step)
+    if heads_first:
+        size, step = (size[0], size[2], size[1], size[3]), (step[0], step[2], step[1])
+    return size, step[:3]
+
+
+def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_weight=None, k_weight=None, eps=1e-6,
+                   inverse=False, heads_first=False, q_out=None, k_out=None, stream=None):
+    """Rotary positions with several axes on q [batch, tokens, heads, dim] and k (the same with its
+    own number of heads; None for q alone), fp16 or bf16, or both without the batch; any strides
+    with contiguous heads.  positions [tokens, axes] or [batch, tokens, axes] int32 or fp32;
+    inv_freq fp32 [P]; axis_pairs: pairs that turn by each axis, P in all, 2 P <= dim.  pairs:
+    "adjacent" (2p, 2p + 1) or "halves" (p, p + P).  q_weight, k_weight fp32 [dim]: the heads' RMS
+    norm in front.  inverse: turn back (the gradient).  Outputs [batch, tokens, heads, dim], or
+    [batch, heads, tokens, dim] with heads_first; q_out may be q, k_out k, with heads_first False.
+    Returns (q_out, k_out)."""
+    import torch
+    if pairs not in ("adjacent", "halves"):
+        raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
+    axis_pairs = tuple(axis_pairs)
+    P = sum(axis_pairs)
+    _vector(inv_freq, (torch.float32,), P, "inv_freq")
+    if not positions.is_cuda or positions.dtype not in (torch.int32, torch.float32) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 or float32 device tensor")
+    ops = (RopeOperand * 2)()
+    outs, made, sizes, count = [None, None], [], None, 0
+    for i, (name, x, w, out) in enumerate((("q", q, q_weight, q_out), ("k", k, k_weight, k_out))):
+        if x is None:
+            if name == "q":
+                raise ValueError("q is required")
+            _absent(w, "k_weight", "without k")
+            _absent(out, "k_out", "without k")
+            continue
+        if not x.is_cuda or x.dtype not in (torch.float16, torch.bfloat16) or x.dtype != q.dtype:
+            raise ValueError(f"{name} must be a float16 or bfloat16 device tensor of q's type, got {x.dtype}")
+        size, step = _heads_layout(x, False, name)
+        if sizes is None:
+            sizes = size
+        elif (size[0], size[1], size[3]) != (sizes[0], sizes[1], sizes[3]) or x.dim() != q.dim():
+            raise ValueError(f"k must have q's batch, tokens and dim, got {tuple(x.shape)} and {tuple(q.shape)}")
+        if w is not None:
+            _vector(w, (torch.float32,), size[3], name + "_weight")
+        if out is None:
+            shape = tuple(x.shape)
+            if heads_first:
+                shape = (*shape[:-3], shape[-2], shape[-3], shape[-1])
+            out = torch.empty(shape, dtype=x.dtype, device=x.device)
+            made.append(out)
+        else:
+            if not out.is_cuda or out.dtype != x.dtype or out.dim() != x.dim():
+                raise ValueError(f"{name}_out must be a {x.dtype} device tensor of {x.dim()} dimensions")
+        osize, ostep = _heads_layout(out, heads_first, name + "_out")
+        if osize != size:
+            raise ValueError(f"{name}_out must have {name}'s sizes in the output's layout, got {tuple(out.shape)}")
+        if any(n > 1 and s < 1 for n, s in zip(osize, ostep)):
+            raise ValueError(f"{name}_out must not overlap itself")
+        ops[i] = RopeOperand(x.data_ptr(), out.data_ptr(), _p(w), size[2], *step, *ostep)
+        outs[i] = out
+        count += 1
+    B, T, _, D = sizes
+    axes = len(axis_pairs)
+    if tuple(positions.shape) == (T, axes):
+        pos_batch = 0
+    elif q.dim() == 4 and tuple(positions.shape) == (B, T, axes):
+        pos_batch = T * axes
+    else:
+        raise ValueError(f"positions must have shape ({T}, {axes}) or ({B}, {T}, {axes}), got {tuple(positions.shape)}")
+    _launch("svdq_rope_axes",
+            (ctypes.addressof(ops), count, B, T, D, _types()[q.dtype], positions.data_ptr(),
+             int(positions.dtype == torch.float32), pos_batch, inv_freq.data_ptr(), axes, _axis_array(axis_pairs),
+             int(pairs == "halves"), eps, int(bool(inverse)), ),
+            (q, k, positions, inv_freq, q_weight, k_weight, *outs), made, stream)
+    return outs[0], outs[1]
 
 
 # svdq_linear_noalloc's static device scratch (SVDQ_STATIC_SCRATCH_BYTES in include/svdq.h)

@@ -17,7 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsvdq.so")
 SOURCES = ["svdq_api.hip", "k_quant_down.hip", "k_quant_weight.hip", "k_gemm.hip", "k_gemm2.hip",
-           "k_gemm3.hip", "k_gemm_i8.hip", "k_gemm_f4.hip", "k_gemm_mx.hip", "k_w4a16.hip", "k_misc.hip", "k_relayout.hip"]
+           "k_gemm3.hip", "k_gemm_i8.hip", "k_gemm_f4.hip", "k_gemm_mx.hip", "k_w4a16.hip", "k_misc.hip", "k_relayout.hip",
+           "block_api.hip", "k_rmsnorm.hip", "k_rope.hip", "k_gemm_act.hip"]
 # -amdgpu-mfma-vgpr-form: MFMA results in VGPRs, so the per-group rescale reads
 # them without v_accvgpr_read copies.  Not for the MXFP4 GEMM, whose four-wave kernel keeps
 # 256 accumulators per lane in the accumulation registers (its other kernels come out the same
@@ -78,24 +79,26 @@ def build(verbose: bool = False) -> str:
 # The C ABI's host code (argument validation, workspace carving) built with AddressSanitizer
 # and UndefinedBehaviorSanitizer for the host pass only (each -fsanitize after -Xarch_host), linked
 # with tests/abi_check.cpp: a program that drives every validation path without a GPU.
+API_SOURCES = ("svdq_api.hip", "block_api.hip")
 SANITIZE = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
             "-Xarch_host", "-fno-sanitize-recover=undefined", "-Xarch_host", "-fno-omit-frame-pointer", "-g"]
 HOST_CHECK = os.path.join(BUILD_DIR, "svdq_abi_check")
 
 
-def build_host_check(verbose: bool = False) -> str:
-    """Compile svdq_api.hip with the sanitizers (the other objects come from build()) and link
-    the ABI check program; returns its path."""
+def build_host_check(verbose: bool = False, check: str = "abi_check.cpp", exe: str = HOST_CHECK) -> str:
+    """Compile the C-ABI sources with the sanitizers (the other objects come from build()) and link
+    an ABI check program of tests/; returns its path."""
     if not all(os.path.exists(os.path.join(BUILD_DIR, s.replace(".hip", ".o"))) for s in SOURCES):
         build(verbose)
     cc = hipcc()
-    api = os.path.join(BUILD_DIR, "svdq_api_sanitized.o")
-    _run([cc, *FLAGS, *SANITIZE, "-c", os.path.join(CSRC, "svdq_api.hip"), "-o", api], verbose)
-    objs = [api] + [os.path.join(BUILD_DIR, s.replace(".hip", ".o")) for s in SOURCES if s != "svdq_api.hip"]
-    check = os.path.join(os.path.dirname(HERE), "tests", "abi_check.cpp")
-    _run([cc, "--offload-arch=gfx950", *SANITIZE, "-x", "c++", check, "-x", "none", *objs, "-o", HOST_CHECK],
-         verbose)
-    return HOST_CHECK
+    objs = [os.path.join(BUILD_DIR, s.replace(".hip", ".o")) for s in SOURCES if s not in API_SOURCES]
+    for src in API_SOURCES:
+        api = os.path.join(BUILD_DIR, src.replace(".hip", "_sanitized.o"))
+        _run([cc, *FLAGS, *SANITIZE, "-c", os.path.join(CSRC, src), "-o", api], verbose)
+        objs.append(api)
+    check = os.path.join(os.path.dirname(HERE), "tests", check)
+    _run([cc, "--offload-arch=gfx950", *SANITIZE, "-x", "c++", check, "-x", "none", *objs, "-o", exe], verbose)
+    return exe
 
 
 MICROBENCH = os.path.join(BUILD_DIR, "mfma_valu")

@@ -1,0 +1,331 @@
+// Root-mean-square norm with the residual's addition in front and an 8-bit (or 16-bit) output:
+//
+//   h = rnd(x + r)  (the stream, kept in r's type)        rstd = 1 / sqrt(mean_k h^2 + eps)
+//   v = h w,  a = max(max_k |v|, 2^-100)
+//   8 bits : code = rnd(v (qmax / a)),  scale = a rstd / qmax       16 bits : y = rnd(v rstd)
+//
+// rstd is one factor of the whole row, so it cancels in the codes: they depend on exact maxima
+// and elementwise fp32 operations only, not on the order of the row sum.
+//
+// One pass: a row's values stay in registers between the sums and the codes, so each input byte
+// is read and each output byte written once.  HBM bounds it for many rows, latency for few.
+#include "block_ops.h"
+
+namespace svdq {
+
+namespace {
+
+constexpr float kTiny = 0x1p-100f;           // floor of a row's maximum: a row of zeros gets codes 0, a finite scale
+
+enum Res { RES_NONE = 0, RES_16 = 1, RES_32 = 2 };
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+
+// Sum of squares and maximum over the row's WPR waves.  red: [2][waves of the block].
+template <int WPR>
+__device__ __forceinline__ void row_reduce(float& ss, float& mx, float (*red)[16]) {
+  ss = wave_sum(ss);
+  mx = wave_max(mx);
+  if (WPR > 1) {
+    const int wave = threadIdx.x >> 6, first = wave / WPR * WPR;
+    if ((threadIdx.x & 63) == 0) {
+      red[0][wave] = ss;
+      red[1][wave] = mx;
+    }
+    __syncthreads();
+    ss = 0.f;
+    mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < WPR; i++) {
+      ss += red[0][first + i];
+      mx = fmaxf(mx, red[1][first + i]);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t code_i8(float v) { return (uint32_t)(int)__builtin_rintf(v) & 0xFFu; }
+
+// n <= 8 16-bit values at p (any element alignment) as a 16-byte piece, zeros behind them.
+__device__ __forceinline__ uint4 load_piece(const uint16_t* p, int n) {
+  uint4 u = make_uint4(0, 0, 0, 0);
+  if (n >= 8) {
+    __builtin_memcpy(&u, p, 16);
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 7; i++) e[i] = i < n ? p[i] : 0u;
+    u = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6]);
+  }
+  return u;
+}
+__device__ __forceinline__ void store_piece(uint16_t* p, const uint4& u, int n) {
+  if (n >= 8) {
+    __builtin_memcpy(p, &u, 16);
+  } else {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+      if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+struct F8 {
+  float4 a, b;
+};
+__device__ __forceinline__ F8 load_piece(const float* p, int n) {
+  F8 u{};
+  if (n >= 8) {
+    __builtin_memcpy(&u, p, 32);
+  } else {
+    float e[8];
+#pragma unroll
+    for (int i = 0; i < 7; i++) e[i] = i < n ? p[i] : 0.f;
+    u = F8{make_float4(e[0], e[1], e[2], e[3]), make_float4(e[4], e[5], e[6], 0.f)};
+  }
+  return u;
+}
+__device__ __forceinline__ void store_piece(float* p, const float* f, int n) {
+  if (n >= 8) {
+    __builtin_memcpy(p, f, 32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; i++)
+      if (i < n) p[i] = f[i];
+  }
+}
+template <bool BF>
+__device__ __forceinline__ void unpack(const uint4& u, float* f) { unpack8(u, BF, f); }
+template <bool BF>
+__device__ __forceinline__ void unpack(const F8& u, float* f) {
+  f[0] = u.a.x; f[1] = u.a.y; f[2] = u.a.z; f[3] = u.a.w;
+  f[4] = u.b.x; f[5] = u.b.y; f[6] = u.b.z; f[7] = u.b.w;
+}
+
+// The weighted values v of n <= 8 elements from element o of the output, as codes or 16-bit values.
+template <bool BF>
+__device__ __forceinline__ void store_out(const NormArgs& a, int64_t o, const float* v, float mul, int n) {
+  if (a.out_type == T_INT8 || a.out_type == T_E4M3) {
+    uint32_t c[2];
+    if (a.out_type == T_INT8) {
+#pragma unroll
+      for (int w = 0; w < 2; w++)
+        c[w] = code_i8(v[4 * w] * mul) | (code_i8(v[4 * w + 1] * mul) << 8) | (code_i8(v[4 * w + 2] * mul) << 16) |
+               (code_i8(v[4 * w + 3] * mul) << 24);
+    } else {
+#pragma unroll
+      for (int w = 0; w < 2; w++) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w] * mul, v[4 * w + 1] * mul, 0, false);
+        c[w] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * w + 2] * mul, v[4 * w + 3] * mul, lo, true);
+      }
+    }
+    uint8_t* q = static_cast<uint8_t*>(a.out) + o;
+    if (n >= 8) {
+      __builtin_memcpy(q, c, 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; i++)
+        if (i < n) q[i] = (uint8_t)(c[i >> 2] >> (8 * (i & 3)));
+    }
+  } else {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) y[e] = v[e] * mul;
+    store_piece(static_cast<uint16_t*>(a.out) + o, pack8(y, BF), n);
+  }
+}
+
+// The factor of the weighted values, and the row's scale.
+__device__ __forceinline__ float row_factor(const NormArgs& a, int64_t r, float ss, float mx, bool first) {
+  const float rstd = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  if (a.out_type != T_INT8 && a.out_type != T_E4M3) return rstd;
+  mx = fmaxf(mx, kTiny);
+  const float qmax = a.out_type == T_INT8 ? 127.f : 448.f;
+  if (first) a.scales[r] = mx * rstd / qmax;
+  return qmax / mx;
+}
+
+template <int RES>
+struct ResOf {
+  typedef uint16_t T;
+  typedef uint4 P;
+};
+template <>
+struct ResOf<RES_32> {
+  typedef float T;
+  typedef F8 P;
+};
+
+// A row in registers: WPR waves, V pieces of 8 elements per lane.  All loads go out first.
+template <int RES, bool BF, int WPR, int V>
+__global__ void __launch_bounds__(WPR > 4 ? WPR * 64 : 256)
+k_rmsnorm(NormArgs a) {
+  constexpr int LANES = WPR * 64;
+  constexpr int ROWS = WPR > 4 ? 1 : 4 / WPR;
+  typedef typename ResOf<RES>::T RT;
+  typedef typename ResOf<RES>::P RP;
+  __shared__ float red[2][16];
+  const int row = blockIdx.x * ROWS + (threadIdx.x / LANES), lane = threadIdx.x % LANES;
+  const bool live = row < a.M;
+  const int64_t r = live ? row : a.M - 1;    // rows past the end repeat the last one and store nothing
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.x_stride;
+  const RT* res = RES ? static_cast<const RT*>(a.res) + r * a.res_stride : nullptr;
+  RT* res_out = RES ? static_cast<RT*>(a.res_out) + r * a.res_out_stride : nullptr;
+  uint4 xr[V];
+  RP rr[V];
+  float v[V][8], w[V][8];
+#pragma unroll
+  for (int p = 0; p < V; p++) {
+    const int i = (p * LANES + lane) * 8;
+    xr[p] = make_uint4(0, 0, 0, 0);
+    rr[p] = RP{};
+    if (i < a.K) {
+      xr[p] = load_piece(x + i, a.K - i);
+      if (RES) rr[p] = load_piece(res + i, a.K - i);
+    }
+  }
+  if (a.weight_type == T_F32) {
+    F8 wr[V];
+#pragma unroll
+    for (int p = 0; p < V; p++) {
+      const int i = (p * LANES + lane) * 8;
+      wr[p] = F8{};
+      if (i < a.K) wr[p] = load_piece(static_cast<const float*>(a.weight) + i, a.K - i);
+    }
+#pragma unroll
+    for (int p = 0; p < V; p++) unpack<BF>(wr[p], w[p]);
+  } else {
+    uint4 wr[V];
+#pragma unroll
+    for (int p = 0; p < V; p++) {
+      const int i = (p * LANES + lane) * 8;
+      wr[p] = make_uint4(0, 0, 0, 0);
+      if (i < a.K) wr[p] = load_piece(static_cast<const uint16_t*>(a.weight) + i, a.K - i);
+    }
+#pragma unroll
+    for (int p = 0; p < V; p++) unpack<BF>(wr[p], w[p]);
+  }
+  float ss = 0.f, mx = 0.f;
+#pragma unroll
+  for (int p = 0; p < V; p++) {
+    const int i = (p * LANES + lane) * 8;
+    unpack<BF>(xr[p], v[p]);
+    if (RES) {
+      float g[8];
+      unpack<BF>(rr[p], g);
+#pragma unroll
+      for (int e = 0; e < 8; e++) v[p][e] += g[e];
+      if constexpr (RES == RES_16) {
+        const uint4 u = pack8(v[p], BF);
+        unpack<BF>(u, v[p]);
+        if (live && i < a.K) store_piece(res_out + i, u, a.K - i);
+      } else if constexpr (RES == RES_32) {
+        if (live && i < a.K) store_piece(res_out + i, v[p], a.K - i);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      ss += v[p][e] * v[p][e];
+      v[p][e] *= w[p][e];
+      mx = fmaxf(mx, fabsf(v[p][e]));
+    }
+  }
+  row_reduce<WPR>(ss, mx, red);
+  if (!live) return;
+  const float mul = row_factor(a, r, ss, mx, lane == 0);
+#pragma unroll
+  for (int p = 0; p < V; p++) {
+    const int i = (p * LANES + lane) * 8;
+    if (i < a.K) store_out<BF>(a, r * a.K + i, v[p], mul, a.K - i);
+  }
+}
+
+// A row too long for registers: one workgroup reads it twice (the second time mostly from the
+// caches).  With a residual the second read is of the stream just written by the same thread.
+template <int RES, bool BF>
+__global__ void __launch_bounds__(1024)
+k_rmsnorm_long(NormArgs a) {
+  typedef typename ResOf<RES>::T RT;
+  __shared__ float red[2][16];
+  const int64_t r = blockIdx.x;
+  const uint16_t* x = static_cast<const uint16_t*>(a.x) + r * a.x_stride;
+  const RT* res = RES ? static_cast<const RT*>(a.res) + r * a.res_stride : nullptr;
+  RT* res_out = RES ? static_cast<RT*>(a.res_out) + r * a.res_out_stride : nullptr;
+  auto weigh = [&](float* v, int i) {
+    float w[8];
+    if (a.weight_type == T_F32) unpack<BF>(load_piece(static_cast<const float*>(a.weight) + i, a.K - i), w);
+    else unpack<BF>(load_piece(static_cast<const uint16_t*>(a.weight) + i, a.K - i), w);
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] *= w[e];
+  };
+  float ss = 0.f, mx = 0.f;
+  for (int i = threadIdx.x * 8; i < a.K; i += 8192) {
+    float v[8];
+    unpack<BF>(load_piece(x + i, a.K - i), v);
+    if (RES) {
+      float g[8];
+      unpack<BF>(load_piece(res + i, a.K - i), g);
+#pragma unroll
+      for (int e = 0; e < 8; e++) v[e] += g[e];
+      if constexpr (RES == RES_16) {
+        const uint4 u = pack8(v, BF);
+        unpack<BF>(u, v);
+        store_piece(res_out + i, u, a.K - i);
+      } else if constexpr (RES == RES_32) {
+        store_piece(res_out + i, v, a.K - i);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e++) ss += v[e] * v[e];
+    weigh(v, i);
+#pragma unroll
+    for (int e = 0; e < 8; e++) mx = fmaxf(mx, fabsf(v[e]));
+  }
+  row_reduce<16>(ss, mx, red);
+  const float mul = row_factor(a, r, ss, mx, threadIdx.x == 0);
+  for (int i = threadIdx.x * 8; i < a.K; i += 8192) {
+    float v[8];
+    if (RES) unpack<BF>(load_piece(res_out + i, a.K - i), v);
+    else unpack<BF>(load_piece(x + i, a.K - i), v);
+    weigh(v, i);
+    store_out<BF>(a, r * a.K + i, v, mul, a.K - i);
+  }
+}
+
+template <int RES, bool BF, int WPR, int V>
+hipError_t go(const NormArgs& a, hipStream_t s) {
+  constexpr int ROWS = WPR > 4 ? 1 : 4 / WPR;
+  hipLaunchKernelGGL((k_rmsnorm<RES, BF, WPR, V>), dim3((a.M + ROWS - 1) / ROWS), dim3(WPR > 4 ? WPR * 64 : 256), 0, s,
+                     a);
+  return hipGetLastError();
+}
+
+template <int RES, bool BF>
+hipError_t launch_res(const NormArgs& a, hipStream_t s) {
+  if (a.K <= 1024) return go<RES, BF, 1, 2>(a, s);
+  if (a.K <= 4096) return go<RES, BF, 4, 2>(a, s);
+  if (a.K <= 16384) return go<RES, BF, 8, 4>(a, s);
+  hipLaunchKernelGGL((k_rmsnorm_long<RES, BF>), dim3(a.M), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+template <bool BF>
+hipError_t launch_type(const NormArgs& a, hipStream_t s) {
+  if (!a.res) return launch_res<RES_NONE, BF>(a, s);
+  return a.res_type == T_F32 ? launch_res<RES_32, BF>(a, s) : launch_res<RES_16, BF>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t s) {
+  return a.x_type == T_BF16 ? launch_type<true>(a, s) : launch_type<false>(a, s);
+}
+
+}  // namespace svdq

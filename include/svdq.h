@@ -363,6 +363,112 @@ svdq_status svdq_linear_folded(const void* x, const float* lambda_in, const void
                                int M, int N, int K, int r, svdq_format fmt, void* workspace,
                                size_t workspace_bytes, void* y, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The operators of a transformer block between its quantized linears: the norm in front of a
+ * linear, a matrix product with its neighbours in the epilogue, and the rotary positions of
+ * queries and keys.  Beyond the conventions above:
+ *  - sizes and strides have their own rules, stated at each operator; strides count elements of
+ *    their tensor and the innermost dimension is contiguous;
+ *  - a pointer needs its element's alignment only, unless the operator says 16 bytes;
+ *  - an output may overlap an input only where the operator says so;
+ *  - all arithmetic is fp32 (int32 for INT8 sums) and every output is rounded once, to nearest
+ *    even; the library adds in a fixed order, so equal calls give equal bits.
+ */
+typedef enum {
+  SVDQ_TYPE_F16 = 0,
+  SVDQ_TYPE_BF16 = 1,
+  SVDQ_TYPE_F32 = 2,
+  SVDQ_TYPE_INT8 = 3,  /* codes in [-127, 127] */
+  SVDQ_TYPE_E4M3 = 4,  /* OCP FP8 E4M3 (finite, largest value 448) */
+  SVDQ_TYPE_INT_MIN_ = -2147483647 - 1,   /* not types: see svdq_format */
+  SVDQ_TYPE_INT_MAX_ = 2147483647
+} svdq_type;
+
+typedef enum {
+  SVDQ_ACT_NONE = 0,
+  SVDQ_ACT_GELU_TANH = 1,  /* gelu_tanh of svdq_gelu_tanh_smooth, the same fp32 form */
+  SVDQ_ACT_SILU = 2,       /* v / (1 + exp(-v)) */
+  SVDQ_ACT_INT_MIN_ = -2147483647 - 1,
+  SVDQ_ACT_INT_MAX_ = 2147483647
+} svdq_activation;
+
+/*
+ * Root-mean-square norm of x plus a residual, with an 8-bit output and its scales.  Per row:
+ *   h = rnd(x + residual) in the residual's type (h = x without one), written to residual_out;
+ *   rstd = 1 / sqrt(mean_k h^2 + eps);  v = h weight;
+ *   8-bit out_type: a = max(max_k |v|, 2^-100), code = rnd(v * (qmax / a)) with qmax 127 (INT8,
+ *     ties to even) or 448 (E4M3), scale = a * rstd / qmax, so code * scale is the normed value.
+ *     rstd is a factor of the whole row and cancels in the codes: they are exact functions of h.
+ *   out_type == x_type: out = rnd(v * rstd), scales unused.  With weight / lambda in place of
+ *     weight this is the smoothed input of svdq_linear.
+ *   x        : [M, K], x_type SVDQ_TYPE_F16 or _BF16, rows x_stride apart.
+ *   residual : [M, K] of residual_type (x_type or SVDQ_TYPE_F32), or NULL for none (residual_out
+ *              is then unused and the strides and type are ignored).
+ *   weight   : [K] of weight_type (x_type or SVDQ_TYPE_F32).
+ *   eps      : finite, > 0.
+ *   out      : out, [M, K] contiguous, out_type (SVDQ_TYPE_INT8, _E4M3 or x_type).
+ *   scales   : out, fp32 [M]; required for an 8-bit out_type.
+ *   residual_out : out, rows residual_out_stride apart; may be residual, or x where the types agree.
+ * 1 <= K <= 2^24, M >= 0 (0 = nothing to do), strides >= K.
+ */
+svdq_status svdq_add_rmsnorm(const void* x, int64_t x_stride, svdq_type x_type, const void* residual,
+                             int64_t residual_stride, svdq_type residual_type, const void* weight,
+                             svdq_type weight_type, float eps, int M, int K, svdq_type out_type, void* out,
+                             float* scales, void* residual_out, int64_t residual_out_stride, void* stream);
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue:
+ *   y[m, n] = rnd( act( (sum_k x[m, k] w[n, k]) * xs[m] * ws[n] + bias[n] ) + residual[m, n] )
+ *   x  : [M, K] of `type` (SVDQ_TYPE_INT8, _E4M3, _F16 or _BF16), rows x_stride apart.
+ *   xs : fp32 [M], or NULL for ones (svdq_add_rmsnorm writes x and xs).
+ *   w  : [N, K] contiguous, of `type` (rows = output columns).
+ *   ws : fp32 [N], or NULL for ones.
+ *   bias     : [N] of out_type, or NULL.
+ *   residual : [M, N] of out_type, rows residual_stride apart, or NULL.
+ *   y        : out, [M, N] of out_type (SVDQ_TYPE_F16 or _BF16), rows y_stride apart; may be residual.
+ * INT8 sums are exact in int32 (K <= 2^17 for INT8: 2^17 * 127^2 < 2^31).  x and w are 16-byte
+ * aligned, K and x_stride multiples of 16 bytes, and a row of either (x_stride for x) takes at
+ * most 4 MiB.  Any M >= 0 and N >= 0 up to 2^24; strides >= the row's length.
+ */
+svdq_status svdq_gemm_act_residual(const void* x, int64_t x_stride, const float* xs, const void* w,
+                                   const float* ws, const void* bias, const void* residual,
+                                   int64_t residual_stride, int M, int N, int K, svdq_type type,
+                                   svdq_activation act, svdq_type out_type, void* y, int64_t y_stride,
+                                   void* stream);
+
+/*
+ * Rotary positions with several axes on queries and keys, with the heads' root-mean-square norm
+ * in front where a weight is given.  For each (batch, token, head) and its `dim` values x:
+ *   u = x * weight / sqrt(mean_d x^2 + eps), or u = x without a weight;
+ *   pair p of the first 2 P values turns by angle = positions[b, t, axis(p)] * inv_freq[p]:
+ *     (u_i, u_j) -> (u_i cos - u_j sin, u_i sin + u_j cos),
+ *   (i, j) = (2p, 2p + 1) or, with halves != 0, (p, p + P); axis_pairs[a] consecutive pairs turn
+ *   by axis a, P = sum of axis_pairs; the values from 2 P on are u unturned.
+ *   inverse != 0 turns by -angle: the inverse map, and the gradient of the output with respect
+ *   to x; it takes no weights.
+ * The product of position and frequency is carried to about 48 bits into the sine and cosine.
+ */
+typedef struct {
+  const void* in;        /* [batch, tokens, heads, dim], strides below, innermost contiguous */
+  void* out;             /* same shape; may be `in` with the same strides */
+  const float* weight;   /* fp32 [dim], or NULL: no norm */
+  int heads;             /* >= 1 */
+  int64_t in_batch, in_token, in_head, out_batch, out_token, out_head;   /* strides >= 0, in elements */
+} svdq_rope_operand;
+
+#define SVDQ_ROPE_MAX_AXES 4
+/*   operands : 1 or 2 operands (queries, keys), `count` of them; host memory, read in the call.
+ *   type     : SVDQ_TYPE_F16 or _BF16, of all inputs and outputs.
+ *   positions : [batch, tokens, axes] int32, or fp32 with positions_fp32 != 0; token stride
+ *              `axes`, batch stride position_batch (0: shared by the batch).
+ *   inv_freq : fp32 [P].  axis_pairs : host memory, `axes` (1 ... SVDQ_ROPE_MAX_AXES) counts >= 0.
+ * batch, tokens >= 0 (0 = nothing to do); 1 <= dim <= 1024; 1 <= P, 2 P <= dim; eps finite, > 0
+ * where a weight is given. */
+svdq_status svdq_rope_axes(const svdq_rope_operand* operands, int count, int batch, int tokens, int dim,
+                           svdq_type type, const void* positions, int positions_fp32, int64_t position_batch,
+                           const float* inv_freq, int axes, const int* axis_pairs, int halves, float eps,
+                           int inverse, void* stream);
+
 /* Static description of a status code. */
 const char* svdq_status_string(svdq_status s);
 
