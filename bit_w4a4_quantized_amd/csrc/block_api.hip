@@ -89,6 +89,7 @@ svdq_status svdq_rope_axes(const svdq_rope_operand* operands, int count, int bat
     a.pairs += axis_pairs[i];
     a.end[i] = a.pairs;
   }
+  for (int i = axes; i < kMaxRopeAxes; i++) a.end[i] = a.pairs;
   if (a.pairs < 1 || 2 * a.pairs > dim) return SVDQ_ERR_SHAPE;
   int64_t heads = 0;
   for (int i = 0; i < count; i++) {
@@ -101,7 +102,7 @@ svdq_status svdq_rope_axes(const svdq_rope_operand* operands, int count, int bat
     heads += o.heads;
   }
   // one workgroup takes at least one head of one token
-  if ((int64_t)batch * tokens > (int64_t)1 << 30 || (int64_t)batch * tokens * heads > (int64_t)1 << 31)
+  if ((int64_t)batch * tokens > (int64_t)1 << 30 || (int64_t)batch * tokens * heads >= (int64_t)1 << 31)
     return SVDQ_ERR_SHAPE;
   if (batch == 0 || tokens == 0) return SVDQ_OK;
   if (!positions || !inv_freq) return SVDQ_ERR_NULL;
