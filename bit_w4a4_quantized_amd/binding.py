@@ -59,7 +59,8 @@ _SIGS = {
     "svdq_add_rmsnorm": (_c_int, [_vp, _c_i64, _c_int, _vp, _c_i64, _c_int, _vp, _c_int, _c_float, _c_int, _c_int,
                                   _c_int, _vp, _vp, _vp, _c_i64, _vp]),
     "svdq_gemm_act_residual": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_int, _c_int, _c_int, _c_int,
-                                        _c_int, _c_int, _vp, _c_i64, _vp]),
+                                        _c_int, _c_int, _vp, _c_i64, _vp, _c_size, _vp]),
+    "svdq_gemm_act_residual_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
     "svdq_rope_axes": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _c_i64, _vp, _c_int, _vp,
                                 _c_int, _c_float, _c_int, _vp]),
     "svdq_status_string": (ctypes.c_char_p, [_c_int]),
@@ -642,12 +643,18 @@ def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=
     return out, scales, residual_out
 
 
+@functools.lru_cache(maxsize=4096)
+def gemm_act_residual_workspace_bytes(M: int, N: int, K: int, type_code: int) -> int:
+    return int(lib().svdq_gemm_act_residual_workspace_bytes(M, N, K, type_code))
+
+
 def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none", residual=None, out_dtype=None,
-                           y=None, stream=None):
+                           y=None, workspace=None, stream=None):
     """y = act((x w^T) * xs[:, None] * ws + bias) + residual, rounded once.  x [M, K] and w [N, K]
     int8, float8_e4m3fn, fp16 or bf16 (x's rows any stride apart); xs [M], ws [N] fp32; bias [N],
     residual and y [M, N] of out_dtype (fp16 or bf16; x's type, or fp16 for 8-bit x, when None);
-    activation "none", "gelu" (tanh) or "silu".  y may be residual."""
+    activation "none", "gelu" (tanh) or "silu".  y may be residual.  workspace: device bytes for
+    the sums of K's splits (gemm_act_residual_workspace_bytes; allocated here when None)."""
     import torch
     types = _types()
     xt = _rows(x, (torch.int8, torch.float8_e4m3fn, torch.float16, torch.bfloat16), None, "x")
@@ -669,16 +676,25 @@ def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none",
     if bias is not None:
         _vector(bias, (out_dtype,), N, "bias")
     rs = 0 if residual is None else _rows(residual, (out_dtype,), (M, N), "residual")
-    made = ()
+    made = []
+    if workspace is None:
+        need = gemm_act_residual_workspace_bytes(M, N, K, types[x.dtype])
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+            made.append(workspace)
+    else:
+        _need(workspace, None, None, "workspace")
     if y is None:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
-        made, yt = (y,), N
+        yt = N
+        made.append(y)
     else:
         yt = _rows(y, (out_dtype,), (M, N), "y")
     _launch("svdq_gemm_act_residual",
             (x.data_ptr(), xt, _p(xs), w.data_ptr(), _p(ws), _p(bias), _p(residual), rs, M, N, K, types[x.dtype],
-             ACTIVATIONS[activation], types[out_dtype], y.data_ptr(), yt),
-            (x, w, xs, ws, bias, residual, y), made, stream)
+             ACTIVATIONS[activation], types[out_dtype], y.data_ptr(), yt, _p(workspace),
+             0 if workspace is None else workspace.numel() * workspace.element_size()),
+            (x, w, xs, ws, bias, residual, y, workspace), made, stream)
     return y
 
 

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsvdq.so")
 SOURCES = ["svdq_api.hip", "k_quant_down.hip", "k_quant_weight.hip", "k_gemm.hip", "k_gemm2.hip",
            "k_gemm3.hip", "k_gemm_i8.hip", "k_gemm_f4.hip", "k_gemm_mx.hip", "k_w4a16.hip", "k_misc.hip", "k_relayout.hip",
-           "block_api.hip", "k_rmsnorm.hip", "k_rope.hip", "k_gemm_act.hip"]
+           "block_api.hip", "k_rmsnorm.hip", "k_rope.hip", "k_gemm_act.hip", "k_gemm_few.hip"]
 # -amdgpu-mfma-vgpr-form: MFMA results in VGPRs, so the per-group rescale reads
 # them without v_accvgpr_read copies.  Not for the MXFP4 GEMM, whose four-wave kernel keeps
 # 256 accumulators per lane in the accumulation registers (its other kernels come out the same

@@ -21,6 +21,14 @@ inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintp
 inline bool stride_ok(int64_t s, int64_t least) { return s >= least && s <= kMaxStride; }
 inline bool eps_ok(float e) { return isfinite(e) && e > 0.f; }
 
+svdq_status check_product(int M, int N, int K, int type) {
+  if (M < 0 || N < 0 || K <= 0 || M > kMaxDim || N > kMaxDim || (int64_t)K * bytes_of(type) > kMaxRowBytes)
+    return SVDQ_ERR_SHAPE;
+  if (K * bytes_of(type) % 16 != 0 || (type == SVDQ_TYPE_INT8 && K > 1 << 17)) return SVDQ_ERR_SHAPE;
+  if (((int64_t)M + 63) / 64 * (((int64_t)N + 63) / 64) >= (int64_t)1 << 31) return SVDQ_ERR_SHAPE;
+  return SVDQ_OK;
+}
+
 svdq_status map_launch(hipError_t e) {
   if (e == hipSuccess) return SVDQ_OK;
   if (e == hipErrorNoBinaryForGpu || e == hipErrorInvalidDeviceFunction) return SVDQ_ERR_DEVICE;
@@ -58,21 +66,27 @@ svdq_status svdq_gemm_act_residual(const void* x, int64_t x_stride, const float*
                                    const float* ws, const void* bias, const void* residual,
                                    int64_t residual_stride, int M, int N, int K, svdq_type type,
                                    svdq_activation act, svdq_type out_type, void* y, int64_t y_stride,
-                                   void* stream) {
+                                   void* workspace, size_t workspace_bytes, void* stream) {
   if ((!is8(type) && !is16(type)) || !is16(out_type)) return SVDQ_ERR_FORMAT;
   if (act != SVDQ_ACT_NONE && act != SVDQ_ACT_GELU_TANH && act != SVDQ_ACT_SILU) return SVDQ_ERR_FORMAT;
   const int b = bytes_of(type);
-  if (M < 0 || N < 0 || K <= 0 || M > kMaxDim || N > kMaxDim || (int64_t)K * b > kMaxRowBytes) return SVDQ_ERR_SHAPE;
-  if (K * b % 16 != 0 || (type == SVDQ_TYPE_INT8 && K > 1 << 17)) return SVDQ_ERR_SHAPE;
+  const svdq_status st = check_product(M, N, K, type);
+  if (st != SVDQ_OK) return st;
   if (x_stride < K || x_stride > kMaxRowBytes / b || x_stride * b % 16 != 0) return SVDQ_ERR_SHAPE;
   if (!stride_ok(y_stride, N) || (residual && !stride_ok(residual_stride, N))) return SVDQ_ERR_SHAPE;
   if (M == 0 || N == 0) return SVDQ_OK;
   if (!x || !w || !y) return SVDQ_ERR_NULL;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 2) || !aligned(xs, 4) || !aligned(ws, 4) ||
-      !aligned(bias, 2) || !aligned(residual, 2))
+      !aligned(bias, 2) || !aligned(residual, 2) || !aligned(workspace, 16))
     return SVDQ_ERR_ALIGN;
-  const GemmActArgs a{x, x_stride, xs, w, ws, bias, residual, residual_stride, M, N, K, type, act, out_type, y, y_stride};
+  const GemmActArgs a{x, x_stride, xs, w, ws, bias, residual, residual_stride, M, N, K, type, act, out_type, y, y_stride,
+                      workspace, workspace ? workspace_bytes : 0};
   return map_launch(launch_gemm_act(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t svdq_gemm_act_residual_workspace_bytes(int M, int N, int K, svdq_type type) {
+  if ((!is8(type) && !is16(type)) || check_product(M, N, K, type) != SVDQ_OK || M == 0 || N == 0) return 0;
+  return gemm_act_plan(M, N, K, type, ~(size_t)0).bytes;
 }
 
 svdq_status svdq_rope_axes(const svdq_rope_operand* operands, int count, int batch, int tokens, int dim,

@@ -92,7 +92,16 @@ struct GemmActArgs {
   const void* bias; const void* res; int64_t res_stride;
   int M, N, K, type, act, out_type;
   void* y; int64_t y_stride;
+  void* part; size_t part_bytes;             // room for the sums of K's splits (may be null)
 };
+// The kernel a product takes, and the bytes its splits of K need (0: one split); with less room than
+// `part_bytes` K is split less or not at all.
+struct GemmActPlan {
+  enum Kind { FEW, T64, T64x128, T128x256, LARGE };
+  int kind, splits;
+  size_t bytes;
+};
+GemmActPlan gemm_act_plan(int M, int N, int K, int type, size_t part_bytes);
 hipError_t launch_gemm_act(const GemmActArgs& a, hipStream_t s);
 
 }  // namespace svdq

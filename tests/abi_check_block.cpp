@@ -37,7 +37,7 @@ int main() {
   expect("norm eps", norm(64, H, NAN, 4, 64, I), SVDQ_ERR_SHAPE);
   expect("norm empty", norm(64, H, 1e-6f, 0, 64, I), SVDQ_OK);
   auto gemm = [&](int64_t xs, int M, int N, int K, svdq_type t, svdq_activation act, int64_t ys) {
-    return svdq_gemm_act_residual(P, xs, PF, P, PF, P, P, ys, M, N, K, t, act, H, P, ys, nullptr);
+    return svdq_gemm_act_residual(P, xs, PF, P, PF, P, P, ys, M, N, K, t, act, H, P, ys, P, 0, nullptr);
   };
   expect("gemm type", gemm(64, 4, 32, 64, BAD, SVDQ_ACT_NONE, 32), SVDQ_ERR_FORMAT);
   expect("gemm act", gemm(64, 4, 32, 64, I, static_cast<svdq_activation>(LOW32), 32), SVDQ_ERR_FORMAT);

@@ -38,8 +38,8 @@ def test_norm_statuses(bad, status):
     assert norm(**bad) == status
 
 
-def gemm(x=P, xst=64, xs=P, w=P, ws=P, b=P, r=P, rst=32, M=4, N=32, K=64, t=I8, act=0, ot=T16, y=P, yst=32):
-    return binding.lib().svdq_gemm_act_residual(x, xst, xs, w, ws, b, r, rst, M, N, K, t, act, ot, y, yst, None)
+def gemm(x=P, xst=64, xs=P, w=P, ws=P, b=P, r=P, rst=32, M=4, N=32, K=64, t=I8, act=0, ot=T16, y=P, yst=32, wsp=P, wb=0):
+    return binding.lib().svdq_gemm_act_residual(x, xst, xs, w, ws, b, r, rst, M, N, K, t, act, ot, y, yst, wsp, wb, None)
 
 
 @pytest.mark.parametrize("bad,status", [
@@ -50,7 +50,7 @@ def gemm(x=P, xst=64, xs=P, w=P, ws=P, b=P, r=P, rst=32, M=4, N=32, K=64, t=I8, 
     (dict(xst=(1 << 22) + 16), SHAPE), (dict(yst=31), SHAPE), (dict(rst=31), SHAPE),
     (dict(x=None), NULL), (dict(w=None), NULL), (dict(y=None), NULL),
     (dict(x=EIGHT), ALIGN), (dict(w=EIGHT), ALIGN), (dict(y=ODD), ALIGN), (dict(xs=4098), ALIGN), (dict(ws=4098), ALIGN),
-    (dict(b=ODD), ALIGN), (dict(r=ODD), ALIGN),
+    (dict(b=ODD), ALIGN), (dict(r=ODD), ALIGN), (dict(wsp=EIGHT), ALIGN),
     (dict(M=0, x=None, w=None, y=None), OK), (dict(N=0, w=None, y=None, yst=0, rst=0), OK),
 ])
 def test_gemm_statuses(bad, status):
@@ -113,7 +113,8 @@ class Recorder:
 
     def __getattr__(self, name):
         def fn(*args):
-            self.calls.append((name, args))
+            if not name.endswith("_bytes"):          # size queries: nothing needed
+                self.calls.append((name, args))
             return 0
         return fn
 
@@ -124,7 +125,9 @@ def rec(monkeypatch):
     monkeypatch.setattr(binding, "lib", lambda: r)
     monkeypatch.setattr(binding, "_raw_stream", lambda dev: 7)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    return r
+    binding.gemm_act_residual_workspace_bytes.cache_clear()
+    yield r
+    binding.gemm_act_residual_workspace_bytes.cache_clear()
 
 
 F16, BF16, F32, I8T = torch.float16, torch.bfloat16, torch.float32, torch.int8
@@ -161,7 +164,7 @@ def gemm_args(**kw):
 def test_gemm_binding(rec):
     binding.svdq_gemm_act_residual(**gemm_args())
     (name, args), = rec.calls
-    assert name == "svdq_gemm_act_residual" and args == (P, 80, P, P, P, P, P, 40, 4, 32, 64, 3, 1, 0, P, 32, 7)
+    assert name == "svdq_gemm_act_residual" and args == (P, 80, P, P, P, P, P, 40, 4, 32, 64, 3, 1, 0, P, 32, None, 0, 7)
     for bad in (dict(x=None), dict(x=Dev((4, 64), F32)), dict(x=Dev((4, 64), I8T, (1, 4))), dict(w=None),
                 dict(w=Dev((32, 48), I8T)), dict(w=Dev((32, 64), F16)), dict(w=Dev((32, 64), I8T, (80, 1))),
                 dict(xs=Dev((5,), F32)), dict(xs=Dev((4,), F16)), dict(ws=Dev((31,), F32)), dict(ws=Dev((32, 1), F32)),

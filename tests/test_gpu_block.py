@@ -467,3 +467,27 @@ def test_operators_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+def test_gemm_workspace():
+    """Splits of K need the workspace they ask for; less is allowed and never written past; INT8
+    sums do not depend on it."""
+    g = gen(13)
+    M, N, K = 70, 200, 8192
+    need = binding.gemm_act_residual_workspace_bytes(M, N, K, 3)
+    assert need > 0
+    x = torch.randint(-127, 128, (M, K), generator=g).to(torch.int8).cuda()
+    w = torch.randint(-127, 128, (N, K), generator=g).to(torch.int8).cuda()
+    s = torch.full((M,), 2.0 ** -16).cuda()
+    want = (x.cpu().to(F64) @ w.cpu().to(F64).T * 2.0 ** -16).to(F16)
+    for room in (need, need // 2 // 16 * 16, 16, 0):
+        buf = torch.full((room + 64,), 77, dtype=torch.uint8, device="cuda")
+        y = binding.svdq_gemm_act_residual(x, w, xs=s, workspace=buf[:room])
+        assert torch.equal(y.cpu(), want) and bool((buf[room:] == 77).all())
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,N,K", [(65, 64, 8192), (100, 300, 5008), (130, 520, 4096), (70, 3072, 4096), (16, 48, 12288),
+                                   (64, 100, 8192)])
+def test_gemm_splits(t, M, N, K):
+    gemm_case(M, N, K, t, BF16, "gelu", scales=True)
