@@ -570,15 +570,15 @@ def _launch(fn, args, tensors, made, stream):
     stream.  `made`: tensors allocated for this call; the allocator learns that another stream
     than theirs uses them."""
     import torch
-    dev = tensors[0].device
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = getattr(lib(), fn)(*args, _current(dev.index) if stream is None else stream)
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on one device, got {tensors[0].device} and {t.device}")
+    if dev == torch._C._cuda_getDevice():
+        st = getattr(lib(), fn)(*args, _current(dev) if stream is None else stream)
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib(), fn)(*args, _current(dev.index) if stream is None else stream)
+            st = getattr(lib(), fn)(*args, _current(dev) if stream is None else stream)
     if st != 0:
         raise SvdqError(fn, st)
     if stream is not None:
@@ -593,7 +593,7 @@ def _current(dev_index):
     global _raw_stream
     if _raw_stream is None:
         _raw_stream = _raw_stream_fn()
-    return _raw_stream(dev_index or 0)
+    return _raw_stream(dev_index)
 
 
 def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=None, scales=None,
@@ -633,7 +633,8 @@ def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=
         scales = torch.empty((M,), dtype=torch.float32, device=x.device)
         made.append(scales)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty((M, K), dtype=residual.dtype, device=x.device)
+        residual_out = torch.empty_like(residual) if rs == K else \
+            torch.empty((M, K), dtype=residual.dtype, device=x.device)
         ros = K
         made.append(residual_out)
     _launch("svdq_add_rmsnorm",
@@ -698,24 +699,58 @@ def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none",
     return y
 
 
-@functools.lru_cache(maxsize=256)
-def _axis_array(axis_pairs):
-    return (_c_int * len(axis_pairs))(*axis_pairs)
-
-
-def _heads_layout(t, heads_first, what):
-    """(batch, token, head) strides of [batch, tokens, heads, dim] (heads_first: [batch, heads,
-    tokens, dim]), or without the batch; sizes likewise."""
-    if t.dim() not in (3, 4):
-        raise ValueError(f"{what} must have 3 or 4 dimensions, got {t.dim()}")
-    size, step = tuple(t.shape), t.stride()
+def _heads_layout(size, step, heads_first, what):
+    """Sizes and (batch, token, head) strides of [batch, tokens, heads, dim] (heads_first: [batch,
+    heads, tokens, dim]), or of the same without the batch."""
+    if len(size) not in (3, 4):
+        raise ValueError(f"{what} must have 3 or 4 dimensions, got {len(size)}")
     if step[-1] != 1 and size[-1] > 1:
         raise ValueError(f"{what}'s heads must be contiguous")
     if len(size) == 3:
         size, step = (1, *size), (0, *step)
     if heads_first:
         size, step = (size[0], size[2], size[1], size[3]), (step[0], step[2], step[1])
-    return size, step[:3]
+    return tuple(size), tuple(step[:3])
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_plan(q, k, q_out, k_out, positions, axis_pairs, heads_first):
+    """What svdq_rope_axes checks and works out from sizes alone.  Operands as (shape, strides) or
+    None; returns the operands without their pointers, (B, T, D), P, the axes' array, the positions'
+    batch stride and the shapes of outputs to allocate."""
+    ops, shapes, sizes = (RopeOperand * 2)(), [None, None], None
+    for i, (name, x, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
+        if x is None:
+            continue
+        size, step = _heads_layout(*x, False, name)
+        if sizes is None:
+            sizes = size
+        elif (size[0], size[1], size[3]) != (sizes[0], sizes[1], sizes[3]) or len(x[0]) != len(q[0]):
+            raise ValueError(f"k must have q's batch, tokens and dim, got {tuple(x[0])} and {tuple(q[0])}")
+        if out is None:
+            s = tuple(x[0])
+            shapes[i] = (*s[:-3], s[-2], s[-3], s[-1]) if heads_first else s
+            steps = [1]
+            for n in reversed(shapes[i][1:]):
+                steps.insert(0, steps[0] * n)
+            out = (shapes[i], tuple(steps))
+        if len(out[0]) != len(x[0]):
+            raise ValueError(f"{name}_out must have {len(x[0])} dimensions")
+        osize, ostep = _heads_layout(*out, heads_first, name + "_out")
+        if osize != size:
+            raise ValueError(f"{name}_out must have {name}'s sizes in the output's layout, got {tuple(out[0])}")
+        if any(n > 1 and s < 1 for n, s in zip(osize, ostep)):
+            raise ValueError(f"{name}_out must not overlap itself")
+        ops[i] = RopeOperand(0, 0, 0, size[2], *step, *ostep)
+    B, T, _, D = sizes
+    axes = len(axis_pairs)
+    if tuple(positions) == (T, axes):
+        pos_batch = 0
+    elif len(q[0]) == 4 and tuple(positions) == (B, T, axes):
+        pos_batch = T * axes
+    else:
+        raise ValueError(f"positions must have shape ({T}, {axes}) or ({B}, {T}, {axes}), got {tuple(positions)}")
+    return bytes(ops), (B, T, D), sum(axis_pairs), (_c_int * axes)(*axis_pairs), pos_batch, shapes
 
 
 def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_weight=None, k_weight=None, eps=1e-6,
@@ -729,62 +764,49 @@ def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_we
     [batch, heads, tokens, dim] with heads_first; q_out may be q, k_out k, with heads_first False.
     Returns (q_out, k_out)."""
     import torch
+    if q is None:
+        raise ValueError("q is required")
     if pairs not in ("adjacent", "halves"):
         raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
-    axis_pairs = tuple(axis_pairs)
-    P = sum(axis_pairs)
-    _vector(inv_freq, (torch.float32,), P, "inv_freq")
+    dtype = q.dtype
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"q must be float16 or bfloat16, got {dtype}")
+    if k is None:
+        _absent(k_weight, "k_weight", "without k")
+        _absent(k_out, "k_out", "without k")
+    for name, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
+        if t is not None and not (t.is_cuda and t.dtype == dtype):
+            raise ValueError(f"{name} must be a {dtype} device tensor")
     if not positions.is_cuda or positions.dtype not in (torch.int32, torch.float32) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or float32 device tensor")
-    ops = (RopeOperand * 2)()
-    outs, made, sizes, count = [None, None], [], None, 0
-    for i, (name, x, w, out) in enumerate((("q", q, q_weight, q_out), ("k", k, k_weight, k_out))):
-        if x is None:
-            if name == "q":
-                raise ValueError("q is required")
-            _absent(w, "k_weight", "without k")
-            _absent(out, "k_out", "without k")
-            continue
-        if not x.is_cuda or x.dtype not in (torch.float16, torch.bfloat16) or x.dtype != q.dtype:
-            raise ValueError(f"{name} must be a float16 or bfloat16 device tensor of q's type, got {x.dtype}")
-        size, step = _heads_layout(x, False, name)
-        if sizes is None:
-            sizes = size
-        elif (size[0], size[1], size[3]) != (sizes[0], sizes[1], sizes[3]) or x.dim() != q.dim():
-            raise ValueError(f"k must have q's batch, tokens and dim, got {tuple(x.shape)} and {tuple(q.shape)}")
-        if w is not None:
-            _vector(w, (torch.float32,), size[3], name + "_weight")
-        if out is None:
-            shape = tuple(x.shape)
-            if heads_first:
-                shape = (*shape[:-3], shape[-2], shape[-3], shape[-1])
-            out = torch.empty(shape, dtype=x.dtype, device=x.device)
-            made.append(out)
-        else:
-            if not out.is_cuda or out.dtype != x.dtype or out.dim() != x.dim():
-                raise ValueError(f"{name}_out must be a {x.dtype} device tensor of {x.dim()} dimensions")
-        osize, ostep = _heads_layout(out, heads_first, name + "_out")
-        if osize != size:
-            raise ValueError(f"{name}_out must have {name}'s sizes in the output's layout, got {tuple(out.shape)}")
-        if any(n > 1 and s < 1 for n, s in zip(osize, ostep)):
-            raise ValueError(f"{name}_out must not overlap itself")
-        ops[i] = RopeOperand(x.data_ptr(), out.data_ptr(), _p(w), size[2], *step, *ostep)
-        outs[i] = out
-        count += 1
-    B, T, _, D = sizes
-    axes = len(axis_pairs)
-    if tuple(positions.shape) == (T, axes):
-        pos_batch = 0
-    elif q.dim() == 4 and tuple(positions.shape) == (B, T, axes):
-        pos_batch = T * axes
-    else:
-        raise ValueError(f"positions must have shape ({T}, {axes}) or ({B}, {T}, {axes}), got {tuple(positions.shape)}")
+    layout = lambda t: None if t is None else (t.shape, t.stride())  # noqa: E731
+    axis_pairs = tuple(axis_pairs)
+    blank, (B, T, D), P, axes, pos_batch, shapes = _rope_plan(
+        layout(q), layout(k), layout(q_out), layout(k_out), positions.shape, axis_pairs, bool(heads_first))
+    _vector(inv_freq, (torch.float32,), P, "inv_freq")
+    ops = (RopeOperand * 2).from_buffer_copy(blank)
+    made = []
+    if q_weight is not None:
+        _vector(q_weight, (torch.float32,), D, "q_weight")
+        ops[0].weight = q_weight.data_ptr()
+    if q_out is None:
+        q_out = torch.empty_like(q) if shapes[0] == q.shape and q.is_contiguous() else q.new_empty(shapes[0])
+        made.append(q_out)
+    ops[0].inp, ops[0].out = q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        if k_weight is not None:
+            _vector(k_weight, (torch.float32,), D, "k_weight")
+            ops[1].weight = k_weight.data_ptr()
+        if k_out is None:
+            k_out = torch.empty_like(k) if shapes[1] == k.shape and k.is_contiguous() else k.new_empty(shapes[1])
+            made.append(k_out)
+        ops[1].inp, ops[1].out = k.data_ptr(), k_out.data_ptr()
     _launch("svdq_rope_axes",
-            (ctypes.addressof(ops), count, B, T, D, _types()[q.dtype], positions.data_ptr(),
-             int(positions.dtype == torch.float32), pos_batch, inv_freq.data_ptr(), axes, _axis_array(axis_pairs),
-             int(pairs == "halves"), eps, int(bool(inverse)), ),
-            (q, k, positions, inv_freq, q_weight, k_weight, *outs), made, stream)
-    return outs[0], outs[1]
+            (ctypes.addressof(ops), 1 if k is None else 2, B, T, D, _types()[dtype], positions.data_ptr(),
+             1 if positions.dtype == torch.float32 else 0, pos_batch, inv_freq.data_ptr(), len(axis_pairs), axes,
+             1 if pairs == "halves" else 0, eps, 1 if inverse else 0),
+            (q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out), made, stream)
+    return q_out, k_out
 
 
 # svdq_linear_noalloc's static device scratch (SVDQ_STATIC_SCRATCH_BYTES in include/svdq.h)

@@ -106,6 +106,9 @@ class Dev:
     def data_ptr(self):
         return P
 
+    def get_device(self):
+        return self.device.index
+
 
 class Recorder:
     def __init__(self):
@@ -124,7 +127,7 @@ def rec(monkeypatch):
     r = Recorder()
     monkeypatch.setattr(binding, "lib", lambda: r)
     monkeypatch.setattr(binding, "_raw_stream", lambda dev: 7)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     binding.gemm_act_residual_workspace_bytes.cache_clear()
     yield r
     binding.gemm_act_residual_workspace_bytes.cache_clear()
