@@ -180,3 +180,23 @@ def with_branch(d: DeviceLayer, h: HostLayer, device="cuda") -> DeviceLayer:
     l1t = torch.from_numpy(h.l1t).to(device) if r else None
     l2 = torch.from_numpy(h.l2).to(device) if r else None
     return DeviceLayer(d.fmt, d.K, d.N, r, l1t, l2, d.wq, d.ws, d.bias, d.lam)
+
+
+def quantize_rows(w, types: str):
+    """8-bit weights for svdq_gemm_act_residual, offline: w [N, K] (torch, any float type) to codes
+    ("int8" or "e4m3") and fp32 scales [N], one per output column, by svdq_add_rmsnorm's rule:
+    a = max|w| of the row (at least 2^-100), code = rnd(w (qmax / a)), scale = a / qmax."""
+    import torch
+    qmax = {"int8": 127.0, "e4m3": 448.0}[types]
+    w = w.float()
+    a = w.abs().amax(-1).clamp_min(2.0 ** -100)
+    codes = w * (torch.full_like(a, qmax) / a)[:, None]
+    codes = codes.round().to(torch.int8) if types == "int8" else codes.to(torch.float8_e4m3fn)
+    return codes.contiguous(), a / qmax
+
+
+def rope_frequencies(axis_pairs, theta: float = 10000.0):
+    """inv_freq for svdq_rope_axes, fp32 [P]: pair j of an axis with n pairs turns by theta^(-j / n)
+    per position."""
+    import torch
+    return torch.cat([theta ** (-torch.arange(n, dtype=torch.float64) / max(n, 1)) for n in axis_pairs]).float()
