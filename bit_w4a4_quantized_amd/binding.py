@@ -34,6 +34,8 @@ class RopeOperand(ctypes.Structure):
                 ("out_head", _c_i64)]
 
 
+_RopeOperands = RopeOperand * 2
+
 _SIGS = {
     "svdq_code_row_bytes": (_c_size, [_c_int, _c_int]),
     "svdq_scale_row_bytes": (_c_size, [_c_int, _c_int]),
@@ -527,26 +529,44 @@ def svdq_relayout(codes, scales, K, fmt, to_canonical, codes_out=None, scales_ou
 
 
 # ------------------------------------------------------------------ a block's operators between its linears
+# These calls are short next to their host work, so the checks of the usual case are few Python
+# operations and everything that depends on sizes alone is cached.
 ACTIVATIONS = {"none": 0, "gelu": 1, "silu": 2}
 
 
-@functools.lru_cache(maxsize=None)
-def _types():
-    """torch dtype -> svdq_type."""
-    import torch
-    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.int8: 3, torch.float8_e4m3fn: 4}
+class _Dtypes:
+    """torch and what the block operators ask of it, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.code = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.int8: 3, torch.float8_e4m3fn: 4}
+        self.half = (torch.float16, torch.bfloat16)
+        self.operand = (torch.int8, torch.float8_e4m3fn, torch.float16, torch.bfloat16)
+        self.f32 = (torch.float32,)
+        self.raw_stream = _raw_stream_fn()
+
+
+_dtypes = None
+
+
+def _d():
+    global _dtypes
+    if _dtypes is None:
+        _dtypes = _Dtypes()
+    return _dtypes
 
 
 def _rows(t, dtypes, shape, what):
     """The row stride of a 2-D device tensor whose rows are contiguous (any row stride that keeps
-    them apart); else ValueError.  dtypes: the dtype or dtypes it may have."""
+    them apart); else ValueError.  dtypes: those it may have."""
     if t is None:
         raise ValueError(f"{what} is required")
     if not t.is_cuda:
         raise ValueError(f"{what} must be a device tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{what} must be one of {dtypes}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{what} must have shape {shape or '[rows, columns]'}, got {tuple(t.shape)}")
     rows, cols = t.shape
     step, inner = t.stride()
@@ -567,33 +587,24 @@ def _vector(t, dtypes, n, what):
 
 def _launch(fn, args, tensors, made, stream):
     """One C call on the tensors' device: on `stream` when given, else on that device's current
-    stream.  `made`: tensors allocated for this call; the allocator learns that another stream
-    than theirs uses them."""
-    import torch
+    stream.  tensors: the caller's; made: those allocated for this call (the allocator learns that
+    another stream than theirs uses them)."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"all tensors must be on one device, got {tensors[0].device} and {t.device}")
+    d = _dtypes
+    torch = d.torch
     if dev == torch._C._cuda_getDevice():
-        st = getattr(lib(), fn)(*args, _current(dev) if stream is None else stream)
+        st = getattr(lib(), fn)(*args, d.raw_stream(dev) if stream is None else stream)
     else:
         with torch.cuda.device(dev):
-            st = getattr(lib(), fn)(*args, _current(dev) if stream is None else stream)
+            st = getattr(lib(), fn)(*args, d.raw_stream(dev) if stream is None else stream)
     if st != 0:
         raise SvdqError(fn, st)
     if stream is not None:
         for t in made:
             t.record_stream(torch.cuda.ExternalStream(stream, device=dev))
-
-
-_raw_stream = None
-
-
-def _current(dev_index):
-    global _raw_stream
-    if _raw_stream is None:
-        _raw_stream = _raw_stream_fn()
-    return _raw_stream(dev_index)
 
 
 def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=None, scales=None,
@@ -603,44 +614,48 @@ def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=
     scales [M], code * scale being the normed value; "same": [M, K] in x's type, no scales.
     Returns (out, scales, stream): stream = x + residual in the residual's type, None without one.
     residual_out may be residual, or x where the types agree."""
-    import torch
-    types = _types()
-    xs = _rows(x, (torch.float16, torch.bfloat16), None, "x")
-    M, K = x.shape
+    d = _dtypes or _d()
+    torch, code = d.torch, d.code
+    xs = _rows(x, d.half, None, "x")
+    shape = x.shape
+    M, K = shape
     xd = x.dtype
     _vector(weight, (xd, torch.float32), K, "weight")
-    if out_format not in ("int8", "e4m3", "same"):
+    if out_format == "int8":
+        od = torch.int8
+    elif out_format == "e4m3":
+        od = torch.float8_e4m3fn
+    elif out_format == "same":
+        od = xd
+        _absent(scales, "scales", "for a 16-bit output")
+    else:
         raise ValueError(f"out_format must be 'int8', 'e4m3' or 'same', got {out_format!r}")
-    od = torch.int8 if out_format == "int8" else torch.float8_e4m3fn if out_format == "e4m3" else xd
-    made = []
     rs = ros = rt = 0
     if residual is not None:
-        rs, rt = _rows(residual, (xd, torch.float32), (M, K), "residual"), types[residual.dtype]
+        rs, rt = _rows(residual, (xd, torch.float32), shape, "residual"), code[residual.dtype]
         if residual_out is not None:
-            ros = _rows(residual_out, (residual.dtype,), (M, K), "residual_out")
-    else:
+            ros = _rows(residual_out, (residual.dtype,), shape, "residual_out")
+    elif residual_out is not None:
         _absent(residual_out, "residual_out", "without a residual")
     if out is not None:
-        _need(out, od, (M, K), "out")
-    if out_format == "same":
-        _absent(scales, "scales", "for a 16-bit output")
-    elif scales is not None:
+        _need(out, od, shape, "out")
+    if scales is not None:
         _need(scales, torch.float32, (M,), "scales")
+    given = (x, weight, residual, out, scales, residual_out)
+    made = []
     if out is None:
-        out = torch.empty((M, K), dtype=od, device=x.device)
+        out = torch.empty(shape, dtype=od, device=x.device)
         made.append(out)
     if scales is None and od is not xd:
-        scales = torch.empty((M,), dtype=torch.float32, device=x.device)
+        scales = torch.empty(M, dtype=torch.float32, device=x.device)
         made.append(scales)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual) if rs == K else \
-            torch.empty((M, K), dtype=residual.dtype, device=x.device)
+        residual_out = torch.empty_like(residual) if rs == K else torch.empty(shape, dtype=residual.dtype, device=x.device)
         ros = K
         made.append(residual_out)
     _launch("svdq_add_rmsnorm",
-            (x.data_ptr(), xs, types[xd], _p(residual), rs, rt, weight.data_ptr(), types[weight.dtype], eps, M, K,
-             types[od], out.data_ptr(), _p(scales), _p(residual_out), ros),
-            (x, weight, residual, out, scales, residual_out), made, stream)
+            (x.data_ptr(), xs, code[xd], _p(residual), rs, rt, weight.data_ptr(), code[weight.dtype], eps, M, K,
+             code[od], out.data_ptr(), _p(scales), _p(residual_out), ros), given, made, stream)
     return out, scales, residual_out
 
 
@@ -656,46 +671,48 @@ def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none",
     residual and y [M, N] of out_dtype (fp16 or bf16; x's type, or fp16 for 8-bit x, when None);
     activation "none", "gelu" (tanh) or "silu".  y may be residual.  workspace: device bytes for
     the sums of K's splits (gemm_act_residual_workspace_bytes; allocated here when None)."""
-    import torch
-    types = _types()
-    xt = _rows(x, (torch.int8, torch.float8_e4m3fn, torch.float16, torch.bfloat16), None, "x")
+    d = _dtypes or _d()
+    torch, code = d.torch, d.code
+    xt = _rows(x, d.operand, None, "x")
     M, K = x.shape
+    dtype = x.dtype
     if w is None or w.dim() != 2:
         raise ValueError("w must be a device tensor [N, K]")
-    N = int(w.shape[0])
-    _need(w, x.dtype, (N, K), "w")
-    if activation not in ACTIVATIONS:
+    N = w.shape[0]
+    _need(w, dtype, (N, K), "w")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}, got {activation!r}")
     if out_dtype is None:
-        out_dtype = x.dtype if x.dtype in (torch.float16, torch.bfloat16) else torch.float16
-    if out_dtype not in (torch.float16, torch.bfloat16):
+        out_dtype = dtype if dtype in d.half else torch.float16
+    elif out_dtype not in d.half:
         raise ValueError(f"out_dtype must be float16 or bfloat16, got {out_dtype}")
     if xs is not None:
-        _vector(xs, (torch.float32,), M, "xs")
+        _vector(xs, d.f32, M, "xs")
     if ws is not None:
-        _vector(ws, (torch.float32,), N, "ws")
+        _vector(ws, d.f32, N, "ws")
     if bias is not None:
         _vector(bias, (out_dtype,), N, "bias")
     rs = 0 if residual is None else _rows(residual, (out_dtype,), (M, N), "residual")
+    given = (x, w, xs, ws, bias, residual, y, workspace)
     made = []
-    if workspace is None:
-        need = gemm_act_residual_workspace_bytes(M, N, K, types[x.dtype])
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-            made.append(workspace)
-    else:
+    if workspace is not None:
         _need(workspace, None, None, "workspace")
-    if y is None:
+        room = workspace.numel() * workspace.element_size()
+    else:
+        room = gemm_act_residual_workspace_bytes(M, N, K, code[dtype])
+        if room:
+            workspace = torch.empty(room, dtype=torch.uint8, device=x.device)
+            made.append(workspace)
+    if y is not None:
+        yt = _rows(y, (out_dtype,), (M, N), "y")
+    else:
         y = torch.empty((M, N), dtype=out_dtype, device=x.device)
         yt = N
         made.append(y)
-    else:
-        yt = _rows(y, (out_dtype,), (M, N), "y")
     _launch("svdq_gemm_act_residual",
-            (x.data_ptr(), xt, _p(xs), w.data_ptr(), _p(ws), _p(bias), _p(residual), rs, M, N, K, types[x.dtype],
-             ACTIVATIONS[activation], types[out_dtype], y.data_ptr(), yt, _p(workspace),
-             0 if workspace is None else workspace.numel() * workspace.element_size()),
-            (x, w, xs, ws, bias, residual, y, workspace), made, stream)
+            (x.data_ptr(), xt, _p(xs), w.data_ptr(), _p(ws), _p(bias), _p(residual), rs, M, N, K, code[dtype], act,
+             code[out_dtype], y.data_ptr(), yt, _p(workspace), room), given, made, stream)
     return y
 
 
@@ -718,7 +735,7 @@ def _rope_plan(q, k, q_out, k_out, positions, axis_pairs, heads_first):
     """What svdq_rope_axes checks and works out from sizes alone.  Operands as (shape, strides) or
     None; returns the operands without their pointers, (B, T, D), P, the axes' array, the positions'
     batch stride and the shapes of outputs to allocate."""
-    ops, shapes, sizes = (RopeOperand * 2)(), [None, None], None
+    ops, shapes, sizes = _RopeOperands(), [None, None], None
     for i, (name, x, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
         if x is None:
             continue
@@ -763,13 +780,14 @@ def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_we
     norm in front.  inverse: turn back (the gradient).  Outputs [batch, tokens, heads, dim], or
     [batch, heads, tokens, dim] with heads_first; q_out may be q, k_out k, with heads_first False.
     Returns (q_out, k_out)."""
-    import torch
+    d = _dtypes or _d()
+    torch = d.torch
     if q is None:
         raise ValueError("q is required")
     if pairs not in ("adjacent", "halves"):
         raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
     dtype = q.dtype
-    if dtype not in (torch.float16, torch.bfloat16):
+    if dtype not in d.half:
         raise ValueError(f"q must be float16 or bfloat16, got {dtype}")
     if k is None:
         _absent(k_weight, "k_weight", "without k")
@@ -783,11 +801,12 @@ def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_we
     axis_pairs = tuple(axis_pairs)
     blank, (B, T, D), P, axes, pos_batch, shapes = _rope_plan(
         layout(q), layout(k), layout(q_out), layout(k_out), positions.shape, axis_pairs, bool(heads_first))
-    _vector(inv_freq, (torch.float32,), P, "inv_freq")
-    ops = (RopeOperand * 2).from_buffer_copy(blank)
+    _vector(inv_freq, d.f32, P, "inv_freq")
+    ops = _RopeOperands.from_buffer_copy(blank)
+    given = (q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     made = []
     if q_weight is not None:
-        _vector(q_weight, (torch.float32,), D, "q_weight")
+        _vector(q_weight, d.f32, D, "q_weight")
         ops[0].weight = q_weight.data_ptr()
     if q_out is None:
         q_out = torch.empty_like(q) if shapes[0] == q.shape and q.is_contiguous() else q.new_empty(shapes[0])
@@ -795,17 +814,17 @@ def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_we
     ops[0].inp, ops[0].out = q.data_ptr(), q_out.data_ptr()
     if k is not None:
         if k_weight is not None:
-            _vector(k_weight, (torch.float32,), D, "k_weight")
+            _vector(k_weight, d.f32, D, "k_weight")
             ops[1].weight = k_weight.data_ptr()
         if k_out is None:
             k_out = torch.empty_like(k) if shapes[1] == k.shape and k.is_contiguous() else k.new_empty(shapes[1])
             made.append(k_out)
         ops[1].inp, ops[1].out = k.data_ptr(), k_out.data_ptr()
     _launch("svdq_rope_axes",
-            (ctypes.addressof(ops), 1 if k is None else 2, B, T, D, _types()[dtype], positions.data_ptr(),
+            (ctypes.addressof(ops), 1 if k is None else 2, B, T, D, d.code[dtype], positions.data_ptr(),
              1 if positions.dtype == torch.float32 else 0, pos_batch, inv_freq.data_ptr(), len(axis_pairs), axes,
              1 if pairs == "halves" else 0, eps, 1 if inverse else 0),
-            (q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out), made, stream)
+            given, made, stream)
     return q_out, k_out
 
 

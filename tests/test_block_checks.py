@@ -126,7 +126,7 @@ class Recorder:
 def rec(monkeypatch):
     r = Recorder()
     monkeypatch.setattr(binding, "lib", lambda: r)
-    monkeypatch.setattr(binding, "_raw_stream", lambda dev: 7)
+    monkeypatch.setattr(binding._d(), "raw_stream", lambda dev: 7)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     binding.gemm_act_residual_workspace_bytes.cache_clear()
     yield r
