@@ -76,7 +76,7 @@ __device__ __forceinline__ void pair_cos_sin(const RopeArgs& a, int64_t pos, int
 struct Split {
   int tw, batches;
   int waves;                                 // of the operand
-  uint32_t magic;                            // ceil(2^32 / heads): unit / heads for units below 2^16
+  uint32_t magic;                            // ceil(2^32 / heads): unit / heads for units below 2^16; 0 for one head
 };
 struct Splits {
   Split of[2];
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) 
     if (u < last) {
       int hd = u, b = b0, t = t0;
       if (w_.tw > 1) {
-        tl[i] = (int)__umulhi((uint32_t)u, w_.magic);
+        tl[i] = w_.magic ? (int)__umulhi((uint32_t)u, w_.magic) : u;
         hd = u - tl[i] * o.heads;
         t += tl[i];
         while (t >= a.tokens) {
@@ -277,7 +277,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
     tw = tw < tokens / 2048 ? tw : tokens / 2048;
     w.tw = tw < 1 ? 1 : (int)tw;
     w.waves = (int)((tokens + w.tw - 1) / w.tw) * w.batches;
-    w.magic = (uint32_t)(((1ull << 32) + heads - 1) / heads);
+    w.magic = heads == 1 ? 0u : (uint32_t)(((1ull << 32) + heads - 1) / heads);
     blocks[i] = (uint32_t)(w.waves + 3) / 4;
   }
   const uint32_t all = blocks[0] + blocks[1];

@@ -376,7 +376,7 @@ const char* svdq_status_string(svdq_status s) {
   switch (s) {
     case SVDQ_OK: return "ok";
     case SVDQ_ERR_NULL: return "a required pointer is NULL";
-    case SVDQ_ERR_SHAPE: return "shape outside the supported constraints (K % 64 == 0, N % 16 == 0, r in {0,16,32,48,64}, dims <= 2^24)";
+    case SVDQ_ERR_SHAPE: return "shape outside the supported constraints (K % 64 == 0, N % 16 == 0, r in {0,16,32,48,64}, dims <= 2^24; the block operators state their own)";
     case SVDQ_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case SVDQ_ERR_FORMAT: return "unknown or unsupported format";
     case SVDQ_ERR_WORKSPACE: return "workspace too small (for svdq_linear_noalloc: the shape needs more than its static scratch)";

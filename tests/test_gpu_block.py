@@ -381,6 +381,14 @@ def test_rope_many_tokens():
     rope_case(2, 9000, 8, 2, 64, (4, 14, 14), "adjacent", BF16, True, heads_first=True)
 
 
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("B,T,H,G,D", [(1, 5500, 2, 1, 256), (3, 3000, 1, 1, 64), (1, 4100, 3, 1, 128), (2, 2100, 5, 3, 8),
+                                       (2500, 3, 7, 1, 64), (1, 6150, 6, 2, 16)])
+def test_rope_tokens_of_few_heads(B, T, H, G, D, heads_first):
+    """A wave takes several tokens, across batches too: one head, odd heads, few tokens a batch."""
+    rope_case(B, T, H, G, D, (D // 2,), "adjacent", BF16, True, heads_first=heads_first)
+
+
 @pytest.mark.parametrize("pairs", ["adjacent", "halves"])
 @pytest.mark.parametrize("D", [128, 36])
 def test_rope_far_positions(D, pairs):
