@@ -29,6 +29,14 @@ template <>
 struct Mma<T_INT8> {
   using Acc = v16i;
 };
+template <int TYPE>
+struct Quarter {
+  using Sum = v4f;
+};
+template <>
+struct Quarter<T_INT8> {
+  using Sum = v4i;
+};
 
 // A workgroup barrier after waiting for the wave's LDS operations and all but its N most recent
 // vector-memory operations, with the builtins, so that the compiler's own waits know of it.
@@ -225,21 +233,6 @@ struct Tile {
           part_at(part, tj, ti)[q * 64] = v;
         }
   }
-  static __device__ __forceinline__ void add_part(const Acc* part, Acc (&acc)[TJ][TI]) {
-#pragma unroll
-    for (int tj = 0; tj < TJ; tj++)
-#pragma unroll
-      for (int ti = 0; ti < TI; ti++) {
-        Acc v;
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-          const uint4 u = part_at(const_cast<Acc*>(part), tj, ti)[q * 64];
-          __builtin_memcpy(reinterpret_cast<char*>(&v) + 16 * q, &u, 16);
-        }
-        acc[tj][ti] += v;
-      }
-  }
-
   // Epilogue: each wave stages its block in 16-bit row pieces, so that global accesses take whole
   // lines.  b0, b1: LDS that nobody else uses.
   static __device__ __forceinline__ void finish(const Args& a, int m0, int n0, uint8_t* b0, uint8_t* b1, const float* cs,
@@ -348,30 +341,52 @@ __global__ void __launch_bounds__(64 * WM * WN, OCC) k_gemm_tile(Args a, int spl
   T::run(a, tm * T::BM, tn * T::BN, b0, b1, b2, cs, first, last, to);
 }
 
-// The splits' sums of a tile added in order, and the epilogue.
-template <int TYPE, int WM, int WN, int TI, int TJ>
-__global__ void __launch_bounds__(64 * WM * WN) k_gemm_join(Args a, int splits, const void* part) {
-  using T = Tile<TYPE, WM, WN, TI, TJ, 2>;
-  constexpr int Y = T::NW / 2 * TI * 32 * TJ * 64;
-  __shared__ __attribute__((aligned(16))) uint8_t y0[Y];
-  __shared__ __attribute__((aligned(16))) uint8_t y1[Y];
-  __shared__ __attribute__((aligned(16))) float cs[2 * T::BN];
-  const int tiles_m = (a.M + T::BM - 1) / T::BM, tiles_n = (a.N + T::BN - 1) / T::BN, tiles = tiles_m * tiles_n;
+// The splits' sums added in order, and the epilogue, four columns a thread: workgroup j of a tile
+// takes quarter-tile pieces 4 j ... 4 j + 3 of its waves' 32 x 32 blocks.  Every load goes out
+// before the first sum (64 x 3072 in five splits: 4.0 us; with the tile kernel's staged
+// epilogue, one workgroup a tile, 7.6).
+template <int TYPE, int WM, int WN>
+__global__ void __launch_bounds__(256) k_gemm_join(Args a, int splits, const uint4* part) {
+  constexpr int BM = WM * 32, BN = WN * 32, GROUPS = WM * WN;
+  const int tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN, tiles = tiles_m * tiles_n;
+  const int id = blockIdx.x / GROUPS, wave = blockIdx.x - id * GROUPS;
   int tm, tn;
-  skel::tile_of(blockIdx.x, tiles, tiles_m, tiles_n, &tm, &tn);
-  T::load_columns(a, tn * T::BN, cs);
-  typename T::Acc acc[TJ][TI];
+  skel::tile_of(id, tiles, tiles_m, tiles_n, &tm, &tn);
+  const int q = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int m = tm * BM + wave / WN * 32 + (lane & 31), n = tn * BN + wave % WN * 32 + 8 * q + 4 * (lane >> 5);
+  if (m >= a.M || n >= a.N) return;
+  const uint4* from = part + ((int64_t)id * GROUPS + wave) * 256 + threadIdx.x;
+  const int64_t next = (int64_t)tiles * GROUPS * 256;
+  float sw[4], bv[4], rv[4];
 #pragma unroll
-  for (int tj = 0; tj < TJ; tj++)
+  for (int j = 0; j < 4; j++) {
+    const bool in = n + j < a.N;
+    sw[j] = in && a.ws ? a.ws[n + j] : 1.f;
+    bv[j] = in && a.bias ? load16(a.bias, n + j, a.bf) : 0.f;
+    rv[j] = in && a.res ? load16(a.res, m * a.res_stride + n + j, a.bf) : 0.f;
+  }
+  const float sx = a.xs ? a.xs[m] : 1.f;
+  using Sum = typename Quarter<TYPE>::Sum;
+  Sum v = {0, 0, 0, 0};
+  for (int s0 = 0; s0 < splits; s0 += 8) {
+    uint4 u[8];
 #pragma unroll
-    for (int ti = 0; ti < TI; ti++)
+    for (int s = 0; s < 8; s++)
+      u[s] = s0 + s < splits ? from[(s0 + s) * next] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 16; i++) acc[tj][ti][i] = 0;
-#pragma unroll 4
-  for (int sp = 0; sp < splits; sp++)
-    T::add_part(static_cast<const typename T::Acc*>(part) + ((int64_t)sp * tiles + blockIdx.x) * T::PART, acc);
-  __syncthreads();
-  T::finish(a, tm * T::BM, tn * T::BN, y0, y1, cs, acc);
+    for (int s = 0; s < 8; s++) v += __builtin_bit_cast(Sum, u[s]);
+  }
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; j++) y[j] = activate((float)v[j] * sx * sw[j] + bv[j], a.act) + rv[j];
+  uint16_t* out = static_cast<uint16_t*>(a.y) + m * a.y_stride + n;
+  if (a.wide >= 4) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack16(y[0], y[1], a.bf), pack16(y[2], y[3], a.bf));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+      if (n + j < a.N) store16(out, j, y[j], a.bf);
+  }
 }
 
 template <int TYPE, int WM, int WN, int TI, int TJ, int R, int OCC>
@@ -388,8 +403,10 @@ hipError_t go_split(const Args& a, int splits, void* part, hipStream_t s) {
   using T = Tile<TYPE, WM, WN, TI, TJ, R>;
   const hipError_t e = go<TYPE, WM, WN, TI, TJ, R, OCC>(a, splits, part, s);
   if (e != hipSuccess || splits == 1) return e;
+  static_assert(TI == 1 && TJ == 1, "k_gemm_join takes waves of one 32 x 32 block");
   const int64_t tiles = (int64_t)((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN);
-  hipLaunchKernelGGL((k_gemm_join<TYPE, WM, WN, TI, TJ>), dim3((unsigned)tiles), dim3(T::NT), 0, s, a, splits, part);
+  hipLaunchKernelGGL((k_gemm_join<TYPE, WM, WN>), dim3((unsigned)(tiles * T::NW)), dim3(256), 0, s, a, splits,
+                     static_cast<const uint4*>(part));
   return hipGetLastError();
 }
 
@@ -399,7 +416,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(512, 1) k_gemm_large(Args a, int whole, int parts) {
   using T = Tile<TYPE, 2, 4, 4, 2, 2>;
   using Half = Tile<TYPE, 2, 4, 2, 2, 2>;
-  using Quarter = Tile<TYPE, 2, 4, 2, 1, 2>;
+  using Fourth = Tile<TYPE, 2, 4, 2, 1, 2>;
   __shared__ __attribute__((aligned(16))) uint8_t b0[T::BUF];
   __shared__ __attribute__((aligned(16))) uint8_t b1[T::BUF];
   __shared__ __attribute__((aligned(16))) float cs[2 * T::BN];
@@ -413,7 +430,7 @@ __global__ void __launch_bounds__(512, 1) k_gemm_large(Args a, int whole, int pa
   const int stages = (a.KB + BK - 1) / BK;
   if (rest < 0 || parts == 1) T::run(a, m0, n0, b0, b1, nullptr, cs, 0, stages, nullptr);
   else if (parts == 2) Half::run(a, m0, n0, b0, b1, nullptr, cs, 0, stages, nullptr);
-  else Quarter::run(a, m0, n0, b0, b1, nullptr, cs, 0, stages, nullptr);
+  else Fourth::run(a, m0, n0, b0, b1, nullptr, cs, 0, stages, nullptr);
 }
 
 template <int TYPE>
@@ -446,7 +463,7 @@ int64_t tiles_of(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) /
 // stage of 128 bytes of K costs a CU its LDS-DMA (0.21 us for each 64 x 64 tile it holds, 0.29 for
 // 64 x 128) but no less than the ring's latency with one tile (0.25); 128 x 256 tiles take 0.95 a
 // stage and 256 x 256 1.72 with all CUs at work (power-bound) and less with few.  A split of K costs
-// the sums' round trip and a second launch: 64 x 3072 x 12288 26.5 us whole, 15.5 in four.
+// the sums' round trip and a second launch (2.8 us on the GPU, and 3 more that its host work counts): 64 x 12288 x 3072 26.5 us whole, 14.5 in five.
 GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
   const double cus = resident_workgroups() / 2;
   const double S = (KB + BK - 1) / BK;
@@ -466,7 +483,7 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
   for (int splits = 1; splits <= 16; splits++) {
     if (splits > 1 && S / splits < 4) break;
     const double st = ceil(S / splits);
-    auto join = [&](int64_t bytes) { return splits > 1 ? 3 + 0.32 * splits + (double)bytes * 2 / 4e6 : 0.0; };
+    auto join = [&](int64_t bytes) { return splits > 1 ? 5.8 + 0.1 * splits + (double)bytes * 2 / 4e6 : 0.0; };
     const int64_t t64 = tiles_of(M, N, 64, 64), t128 = tiles_of(M, N, 64, 128);
     const double c64 = (double)(t64 * splits) / cus, c128 = ceil((double)(t128 * splits) / cus);
     const int64_t b64 = splits > 1 ? t64 * splits * 64 * 64 * 4 : 0, b128 = splits > 1 ? t128 * splits * 64 * 128 * 4 : 0;
