@@ -250,15 +250,13 @@ struct Tile {
       __builtin_amdgcn_wave_barrier();
     };
     const int sr = lane / SL, ss = lane % SL;                // row and slot of this lane's line pieces
-    const bool wide = a.wide == 8, res = a.res != nullptr;
-    if (res && wide) {
+    if (a.res) {
 #pragma unroll
       for (int i = 0; i < TI * 32 / PASS; i++) {
         const int row = i * PASS + sr, m = mw + row, n = n0 + nw + ss * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (m < a.M && n < a.N)
-          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.res) + m * a.res_stride + n);
-        *at(row, ss) = v;
+        uint32_t v[4] = {0, 0, 0, 0};
+        if (m < a.M && n < a.N) load_piece<8>(a.res, m * a.res_stride + n, a.N - n, v);
+        *at(row, ss) = make_uint4(v[0], v[1], v[2], v[3]);
       }
       sync();
     }
@@ -289,15 +287,9 @@ struct Tile {
           }
 #pragma unroll
           for (int e = 0; e < 8; e++) v[e] = activate(v[e] * sx[ti] * sw[e] + bv[e], a.act);
-          if (res) {
+          if (a.res) {
             float r[8];
-            if (wide) {
-              unpack8(*at(row, slot), a.bf, r);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; e++)
-                r[e] = mw + row < a.M && n0 + c + e < a.N ? load16(a.res, (mw + row) * a.res_stride + n0 + c + e, a.bf) : 0.f;
-            }
+            unpack8(*at(row, slot), a.bf, r);
 #pragma unroll
             for (int e = 0; e < 8; e++) v[e] += r[e];
           }
@@ -308,17 +300,9 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < TI * 32 / PASS; i++) {
       const int row = i * PASS + sr, m = mw + row, n = n0 + nw + ss * 8;
-      const uint4 v = *at(row, ss);
-      if (m >= a.M || n >= a.N) continue;
-      uint16_t* y = static_cast<uint16_t*>(a.y) + m * a.y_stride + n;
-      if (wide) {
-        *reinterpret_cast<uint4*>(y) = v;
-      } else {
-        const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 8; e++)
-          if (n + e < a.N) y[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
-      }
+      const uint4 u = *at(row, ss);
+      const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+      if (m < a.M && n < a.N) store_piece<8>(a.y, m * a.y_stride + n, a.N - n, v);
     }
   }
 };
@@ -357,13 +341,14 @@ __global__ void __launch_bounds__(256) k_gemm_join(Args a, int splits, const uin
   if (m >= a.M || n >= a.N) return;
   const uint4* from = part + ((int64_t)id * GROUPS + wave) * 256 + threadIdx.x;
   const int64_t next = (int64_t)tiles * GROUPS * 256;
-  float sw[4], bv[4], rv[4];
+  float sw[4], bv[4];
+  uint32_t rr[2] = {0, 0};
+  if (a.res) load_piece<4>(a.res, m * a.res_stride + n, a.N - n, rr);
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     const bool in = n + j < a.N;
     sw[j] = in && a.ws ? a.ws[n + j] : 1.f;
     bv[j] = in && a.bias ? load16(a.bias, n + j, a.bf) : 0.f;
-    rv[j] = in && a.res ? load16(a.res, m * a.res_stride + n + j, a.bf) : 0.f;
   }
   const float sx = a.xs ? a.xs[m] : 1.f;
   using Sum = typename Quarter<TYPE>::Sum;
@@ -376,17 +361,12 @@ __global__ void __launch_bounds__(256) k_gemm_join(Args a, int splits, const uin
 #pragma unroll
     for (int s = 0; s < 8; s++) v += __builtin_bit_cast(Sum, u[s]);
   }
-  float y[4];
+  float y[4], rv[4];
+  unpack4(rr, a.bf, rv);
 #pragma unroll
   for (int j = 0; j < 4; j++) y[j] = activate((float)v[j] * sx * sw[j] + bv[j], a.act) + rv[j];
-  uint16_t* out = static_cast<uint16_t*>(a.y) + m * a.y_stride + n;
-  if (a.wide >= 4) {
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack16(y[0], y[1], a.bf), pack16(y[2], y[3], a.bf));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-      if (n + j < a.N) store16(out, j, y[j], a.bf);
-  }
+  const uint32_t o[2] = {pack16(y[0], y[1], a.bf), pack16(y[2], y[3], a.bf)};
+  store_piece<4>(a.y, m * a.y_stride + n, a.N - n, o);
 }
 
 template <int TYPE, int WM, int WN, int TI, int TJ, int R, int OCC>
@@ -458,12 +438,20 @@ int64_t tiles_of(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) /
 
 }  // namespace
 
-// The kernel that costs least, in microseconds fitted on M = 1 ... 4608 by N = 100 ... 12288 and K = 512 ...
-// 12288 bytes (int8 and bf16, one box; it is within 10% of the best kernel on 100 of 106 sizes).  A
-// stage of 128 bytes of K costs a CU its LDS-DMA (0.21 us for each 64 x 64 tile it holds, 0.29 for
-// 64 x 128) but no less than the ring's latency with one tile (0.25); 128 x 256 tiles take 0.95 a
-// stage and 256 x 256 1.72 with all CUs at work (power-bound) and less with few.  A split of K costs
-// the sums' round trip and a second launch (2.8 us on the GPU, and 3 more that its host work counts): 64 x 12288 x 3072 26.5 us whole, 14.5 in five.
+// The kernel that costs least, in microseconds fitted to every kernel's time over M = 1 ... 4608,
+// N = 1024 ... 12288 and K = 1024 ... 12288 in int8 and bf16: of 140 such sizes the choice is the
+// best kernel or within 10% of it at 136, and within 18% at the others (1024 x 12288 x 3072 in
+// bf16: 128 us, 112 in 128 x 256 tiles).  A stage of 128 bytes of K costs a CU its LDS-DMA (0.21 us
+// for each 64 x 64 tile it holds, 0.29 for 64 x 128) but no less than the ring's latency with one
+// tile (0.25); 128 x 256 tiles take 0.95 a stage and 256 x 256 1.72 with all CUs at work
+// (power-bound) and less with few.  A split of K costs the sums' round trip and a second launch
+// (2.8 us on the GPU, and 3 more that its host work counts).
+//
+// Both sides, in us, int8 (M x K x N): few rows / tiles 1 x 12288 x 3072 8.8 / 13.3, 1 x 3072 x 12288
+// 12.6 / 10.7, 33 x 3072 x 12288 17.4 / 10.9; 64 x 128 / 128 x 256 tiles 512 x 3072 x 12288
+// 28.4 / 26.2, 256 x 3072 x 12288 19.0 / 22.5; 128 x 256 / 256 x 256 2048 x 3072 x 3072 25.9 / 30.6,
+// 4608 x 3072 x 12288 183 / 170; 64 x 64 / 64 x 128 65 x 3072 x 3072 8.8 / 10.0,
+// 512 x 3072 x 3072 13.9 / 12.3; 64 x 12288 x 3072 26.5 whole, 14.5 in five splits.
 GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
   const double cus = resident_workgroups() / 2;
   const double S = (KB + BK - 1) / BK;
@@ -527,11 +515,6 @@ hipError_t launch_gemm_act(const GemmActArgs& g, hipStream_t s) {
   a.bf = g.out_type == T_BF16;
   a.y = g.y;
   a.y_stride = g.y_stride;
-  auto wide = [&](int n) {                   // whether n elements of y and res may be moved at once everywhere
-    auto ok = [&](const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % (2 * n) == 0 && stride % n == 0; };
-    return g.N % n == 0 && ok(g.y, g.y_stride) && (!g.res || ok(g.res, g.res_stride));
-  };
-  a.wide = wide(8) ? 8 : wide(4) ? 4 : 1;
   const GemmActPlan p = gact::plan(a.M, a.N, a.KB, (int64_t)g.part_bytes);
   if (p.kind == GemmActPlan::FEW) return gact::launch_few(a, g.type, s);
   switch (g.type) {
