@@ -439,19 +439,20 @@ int64_t tiles_of(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) /
 }  // namespace
 
 // The kernel that costs least, in microseconds fitted to every kernel's time over M = 1 ... 4608,
-// N = 1024 ... 12288 and K = 1024 ... 12288 in int8 and bf16: of 140 such sizes the choice is the
-// best kernel or within 10% of it at 136, and within 18% at the others (1024 x 12288 x 3072 in
-// bf16: 128 us, 112 in 128 x 256 tiles).  A stage of 128 bytes of K costs a CU its LDS-DMA (0.21 us
+// N = 1024 ... 12288 and K = 1024 ... 12288 in int8 and bf16: of 152 such sizes the choice is the
+// best kernel or within 10% of it at 149, and within 13% at the others (777 x 3072 x 12288 in bf16:
+// 78 us, 69 in 256 x 256 tiles).  A stage of 128 bytes of K costs a CU its LDS-DMA (0.21 us
 // for each 64 x 64 tile it holds, 0.29 for 64 x 128) but no less than the ring's latency with one
 // tile (0.25); 128 x 256 tiles take 0.95 a stage and 256 x 256 1.72 with all CUs at work
 // (power-bound) and less with few.  A split of K costs the sums' round trip and a second launch
 // (2.8 us on the GPU, and 3 more that its host work counts).
 //
-// Both sides, in us, int8 (M x K x N): few rows / tiles 1 x 12288 x 3072 8.8 / 13.3, 1 x 3072 x 12288
-// 12.6 / 10.7, 33 x 3072 x 12288 17.4 / 10.9; 64 x 128 / 128 x 256 tiles 512 x 3072 x 12288
-// 28.4 / 26.2, 256 x 3072 x 12288 19.0 / 22.5; 128 x 256 / 256 x 256 2048 x 3072 x 3072 25.9 / 30.6,
-// 4608 x 3072 x 12288 183 / 170; 64 x 64 / 64 x 128 65 x 3072 x 3072 8.8 / 10.0,
-// 512 x 3072 x 3072 13.9 / 12.3; 64 x 12288 x 3072 26.5 whole, 14.5 in five splits.
+// Both sides, in us, int8 (M x K x N): few rows / tiles 1 x 3072 x 12288 8.9 / 10.6, 17 x 3072 x 12288
+// 9.3 / 10.7, 33 x 3072 x 12288 13.7 / 10.9, 64 x 3072 x 3072 6.7 / 8.2; 64 x 64 / 64 x 128 tiles
+// 65 x 3072 x 3072 8.8 / 10.0, 512 x 3072 x 3072 13.9 / 12.3; 64 x 128 / 128 x 256
+// 256 x 3072 x 12288 19.0 / 22.5, 512 x 3072 x 12288 28.4 / 26.2; 128 x 256 / 256 x 256
+// 2048 x 3072 x 3072 25.9 / 30.6, 4608 x 3072 x 12288 183 / 170; 64 x 12288 x 3072 26.5 whole, 14.5
+// in five splits.
 GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
   const double cus = resident_workgroups() / 2;
   const double S = (KB + BK - 1) / BK;
@@ -465,8 +466,8 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
   };
   if (M <= kFewRows) {
     const int ti = (M + 15) / 16;
-    const double wgs = (N + 15) / 16, rounds = ceil(wgs / (cus * (ti == 1 ? 2 : 1)));
-    consider(GemmActPlan::FEW, 1, rounds * (ceil(S / 4) * (0.13 + 0.1 * ti) + 3.2) + 0.5 * (rounds - 1), 0);
+    const double c = (N + 15) / 16 / cus, rounds = ceil(c / (ti <= 2 ? 3 : 2));
+    consider(GemmActPlan::FEW, 1, ceil(S / 4) * ceil(c) * (0.19 + 0.055 * ti) + 3.2 + 0.25 * ti + 0.3 * c + 1.5 * (rounds - 1), 0);
   }
   for (int splits = 1; splits <= 16; splits++) {
     if (splits > 1 && S / splits < 4) break;
@@ -475,7 +476,7 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
     const int64_t t64 = tiles_of(M, N, 64, 64), t128 = tiles_of(M, N, 64, 128);
     const double c64 = (double)(t64 * splits) / cus, c128 = ceil((double)(t128 * splits) / cus);
     const int64_t b64 = splits > 1 ? t64 * splits * 64 * 64 * 4 : 0, b128 = splits > 1 ? t128 * splits * 64 * 128 * 4 : 0;
-    consider(GemmActPlan::T64, splits, (c64 > 1 ? 0.21 * ceil(c64) : 0.25) * st + 3 + 0.5 * c64 + join(b64), b64);
+    consider(GemmActPlan::T64, splits, (c64 > 1 ? 0.21 * ceil(c64) * st + 3 : 0.25 * st + 3.7) + 0.5 * c64 + join(b64), b64);
     consider(GemmActPlan::T64x128, splits, 0.29 * c128 * st + 4 + c128 + join(b128), b128);
   }
   // rounds of 256 workgroups, the last with its share of CUs at work

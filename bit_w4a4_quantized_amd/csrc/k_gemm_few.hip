@@ -10,10 +10,11 @@
 // reads of sixteen rows at one piece hit distinct banks.  v_mfma 16 x 16: lane (r16, q) holds
 // pieces q and 4 + q of its row, and gets columns 4 q ... 4 q + 3 of token row r16.
 //
-// 1 x 12288 x 3072 (M x K x N) takes 8.8 us in int8 (13.3 in split 64 x 64 tiles) and 13.8 in bf16:
-// 4.3 and 5.5 TB/s of weight; 17 rows 9.5, 64 rows 15.3, where the token rows' traffic (each workgroup reads them
-// all) has passed the weight's.  Wide and short products (1 x 3072 x 12288 in int8) are six stages
-// of K a wave, all latency, and go to the tiles.
+// The rings are short, so that two or three workgroups share a CU: with R = 4 and one or two of
+// them 16 x 3072 x 12288 (M x K x N) in int8 took 11.4 us, 9.2 with R = 3; 64 rows 20.9, 14.5 with R = 2.
+// 1 x 12288 x 3072 takes 9.1 us in int8 (13.3 in split 64 x 64 tiles) and 13.9 in bf16, 1 x 3072 x 12288
+// 8.9 and 13.8 (tiles 10.7 and 16.2): 4.1 ... 5.5 TB/s of weight.  With 33 rows and more the token
+// rows' traffic (each workgroup reads them all) passes the weight's, and wide products go to tiles.
 #include "gemm_act.h"
 
 namespace svdq {
@@ -55,14 +56,13 @@ __device__ __forceinline__ void wait_loads() {
 
 template <int TYPE, int TI>
 __global__ void __launch_bounds__(256) k_gemm_few(Args a) {
-  constexpr int R = 4;
+  constexpr int R = TI == 1 ? 3 : 2;
   constexpr int L = 2 + 2 * TI;              // LDS-DMA instructions (8 rows each) of a stage
   constexpr int BUF = 1024 * L;              // of one wave
   using Acc = typename Mma<TYPE>::Acc;
   __shared__ __attribute__((aligned(16))) uint8_t b0[4 * BUF];
   __shared__ __attribute__((aligned(16))) uint8_t b1[4 * BUF];
-  __shared__ __attribute__((aligned(16))) uint8_t b2[4 * BUF];
-  __shared__ __attribute__((aligned(16))) uint8_t b3[4 * BUF];
+  __shared__ __attribute__((aligned(16))) uint8_t b2[R > 2 ? 4 * BUF : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int q = lane >> 4, r16 = lane & 15;
   const int n0 = blockIdx.x * 16, nrows = min(16, a.N - n0);
@@ -111,8 +111,7 @@ __global__ void __launch_bounds__(256) k_gemm_few(Args a) {
   };
   load(0, b0);
   load(1, b1);
-  load(2, b2);
-  load(3, b3);
+  if (R > 2) load(2, b2);
   // the epilogue's operands: thread t < 64 TI ends up with columns n ... n + 3 of row m
   const int ot = threadIdx.x >> 6, m = ot * 16 + r16, n = n0 + 4 * q;
   const bool mine = ot < TI && m < a.M;
@@ -126,11 +125,10 @@ __global__ void __launch_bounds__(256) k_gemm_few(Args a) {
     sw[j] = in && a.ws ? a.ws[n + j] : 1.f;
     bv[j] = in && a.bias ? load16(a.bias, n + j, a.bf) : 0.f;
   }
-  for (int st = 0; st < stages; st += 4) {   // stages past the last are zeros
+  for (int st = 0; st < stages; st += R) {   // stages past the last are zeros
     step(st, b0);
     step(st + 1, b1);
-    step(st + 2, b2);
-    step(st + 3, b3);
+    if (R > 2) step(st + 2, b2);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // nothing of the rings may land in the partial sums
   __syncthreads();
