@@ -319,10 +319,21 @@ hipError_t go(const NormArgs& a, hipStream_t s) {
 
 template <int RES, bool BF>
 hipError_t launch_res(const NormArgs& a, hipStream_t s) {
-  // one piece per lane while 16 waves hold the row: the most loads in flight and the least
-  // registers (18432 x 3072 over an fp32 stream: 140 us, two pieces 150, six in one wave 166)
-  if (a.K <= 8192) return go<RES, BF, 1>(a, s);
-  if (a.K <= 16384) return go<RES, BF, 2>(a, s);
+  // Pieces a lane (16 bytes of x each, with 16 or 32 of the stream): 48 to 64 bytes in flight are
+  // enough, more waves cost their reductions and more pieces leave lanes idle in short rows.  In us,
+  // 4608 rows, one piece / two / four: no stream, K = 8192 40.5 / 26.5 / 23.3, 2048 11.3 / 10.0 / 10.8;
+  // 16-bit stream, 8192 55.2 / 52.5 / 53.2, 5120 40.0 / 33.8 / 34.3; fp32, 3072 29.1 / 30.5 / 31.0.
+  // At most 16 waves hold a row.
+  if constexpr (RES == RES_NONE) {
+    if (a.K <= 2048) return go<RES, BF, 2>(a, s);
+  }
+  if constexpr (RES == RES_16) {
+    if (a.K <= 16384) return go<RES, BF, 2>(a, s);
+  }
+  if constexpr (RES == RES_32) {
+    if (a.K <= 8192) return go<RES, BF, 1>(a, s);
+    if (a.K <= 16384) return go<RES, BF, 2>(a, s);
+  }
   if (a.K <= 32768) return go<RES, BF, 4>(a, s);
   hipLaunchKernelGGL((k_rmsnorm_long<RES, BF>), dim3(a.M), dim3(1024), 0, s, a);
   return hipGetLastError();

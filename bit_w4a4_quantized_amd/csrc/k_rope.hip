@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) 
   __shared__ __attribute__((aligned(16))) float table[4][2][512];   // cosines and sines of each wave's tokens
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   // workgroups of the two operands in even turns: a token's queries and keys are read at about the
-  // same time (2 x 16384 tokens of a packed projection 135 us, all queries first 141)
+  // same time (2 x 16384 tokens of a packed projection took 4% longer with all queries first)
   const uint32_t k1 = __umulhi(blockIdx.x, sp.share);
   const int which = __umulhi(blockIdx.x + 1, sp.share) > k1;
   const int id = __builtin_amdgcn_readfirstlane((int)(which ? k1 : blockIdx.x - k1) * 4 + wave);
@@ -256,8 +256,8 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
   int lanes = 1;
   while (lanes * 16 < a.dim) lanes *= 2;
   // Three units in flight per lane group for many tokens whose heads waste no more of three than
-  // of two (4608 tokens of 24 heads of 128: 27.3 us against 29.2), else two (one token 4.0 us
-  // against 4.6, four units 4.7; 512 tokens 5.5, 6.0 and 6.2)
+  // of two (4608 tokens of 24 heads of 128: 21.8 us against 23.6), else two (9000 tokens of 16 heads
+  // of 256 59.6 us against 63.0, one token 5.1 and 5.5, launch included)
   const int groups = 64 / lanes;
   auto wasted = [&](int u) {
     int n = 0;
