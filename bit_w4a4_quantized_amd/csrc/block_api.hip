@@ -31,6 +31,7 @@ svdq_status check_product(int M, int N, int K, int type) {
 
 svdq_status map_launch(hipError_t e) {
   if (e == hipSuccess) return SVDQ_OK;
+  if (e == hipErrorInvalidConfiguration) return SVDQ_ERR_SHAPE;   // !launchable
   if (e == hipErrorNoBinaryForGpu || e == hipErrorInvalidDeviceFunction) return SVDQ_ERR_DEVICE;
   return SVDQ_ERR_LAUNCH;
 }

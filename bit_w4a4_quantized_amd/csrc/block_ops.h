@@ -63,6 +63,9 @@ __device__ __forceinline__ uint4 pack8(const float* f, bool bf) {
   return u;
 }
 
+// A launch holds fewer than 2^32 threads.
+inline bool launchable(int64_t blocks, int threads) { return blocks * threads < (int64_t)1 << 32; }
+
 struct NormArgs {
   const void* x; int64_t x_stride; int x_type;                  // strides in elements
   const void* res; int64_t res_stride; int res_type;            // res may be null

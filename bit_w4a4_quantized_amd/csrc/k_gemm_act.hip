@@ -373,6 +373,7 @@ template <int TYPE, int WM, int WN, int TI, int TJ, int R, int OCC>
 hipError_t go(const Args& a, int splits, void* part, hipStream_t s) {
   using T = Tile<TYPE, WM, WN, TI, TJ, R>;
   const int64_t tiles = (int64_t)((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN);
+  if (!launchable(tiles * splits, T::NT)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_gemm_tile<TYPE, WM, WN, TI, TJ, R, OCC>), dim3((unsigned)(tiles * splits)), dim3(T::NT), 0, s, a,
                      splits, part);
   return hipGetLastError();
@@ -419,6 +420,7 @@ hipError_t go_large(const Args& a, hipStream_t s) {
   const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   const int rest = (int)(tiles % cus), whole = (int)(tiles - rest);
   const int parts = 4 * rest <= cus ? 4 : 2 * rest <= cus ? 2 : 1;
+  if (!launchable(whole + rest * parts, 512)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(k_gemm_large<TYPE>, dim3((unsigned)(whole + rest * parts)), dim3(512), 0, s, a, whole, parts);
   return hipGetLastError();
 }

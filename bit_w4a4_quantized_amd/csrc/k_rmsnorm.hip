@@ -313,6 +313,7 @@ k_rmsnorm_long(NormArgs a) {
 template <int RES, bool BF, int V>
 hipError_t go(const NormArgs& a, hipStream_t s) {
   const int wpr = (a.K + 512 * V - 1) / (512 * V), rows = wpr > 4 ? 1 : 4 / wpr;
+  if (!launchable((a.M + rows - 1) / rows, 64 * wpr * rows)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_rmsnorm<RES, BF, V>), dim3((a.M + rows - 1) / rows), dim3(64 * wpr * rows), 0, s, a, wpr);
   return hipGetLastError();
 }
@@ -335,6 +336,7 @@ hipError_t launch_res(const NormArgs& a, hipStream_t s) {
     if (a.K <= 16384) return go<RES, BF, 2>(a, s);
   }
   if (a.K <= 32768) return go<RES, BF, 4>(a, s);
+  if (!launchable(a.M, 1024)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_rmsnorm_long<RES, BF>), dim3(a.M), dim3(1024), 0, s, a);
   return hipGetLastError();
 }

@@ -250,6 +250,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
   const int64_t tokens = (int64_t)a.batch * a.tokens;
   if (!wide(a)) {
     const int64_t units = tokens * (a.op[0].heads + (a.nops > 1 ? a.op[1].heads : 0));
+    if (!launchable((units + 3) / 4, 256)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL(k_rope_any, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, s, a, units);
     return hipGetLastError();
   }
@@ -281,6 +282,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
     blocks[i] = (uint32_t)(w.waves + 3) / 4;
   }
   const uint32_t all = blocks[0] + blocks[1];
+  if (!launchable(all, 256)) return hipErrorInvalidConfiguration;
   sp.share = (uint32_t)((((uint64_t)blocks[1] << 32) + all - 1) / all);
   const bool bf = a.type == T_BF16;
   const auto two = a.halves ? (bf ? k_rope<true, true, 2> : k_rope<false, true, 2>)

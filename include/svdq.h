@@ -409,7 +409,8 @@ typedef enum {
  *   out      : out, [M, K] contiguous, out_type (SVDQ_TYPE_INT8, _E4M3 or x_type).
  *   scales   : out, fp32 [M]; required for an 8-bit out_type.
  *   residual_out : out, rows residual_out_stride apart; may be residual, or x where the types agree.
- * 1 <= K <= 2^24, M >= 0 (0 = nothing to do), strides >= K.
+ * 1 <= K <= 2^24, 0 <= M <= 2^24 (0 = nothing to do), strides >= K.  SVDQ_ERR_SHAPE also where the
+ * rows need 2^32 threads or more (never below 2^34 elements).
  */
 svdq_status svdq_add_rmsnorm(const void* x, int64_t x_stride, svdq_type x_type, const void* residual,
                              int64_t residual_stride, svdq_type residual_type, const void* weight,
@@ -474,7 +475,8 @@ typedef struct {
  *              `axes`, batch stride position_batch (0: shared by the batch).
  *   inv_freq : fp32 [P].  axis_pairs : host memory, `axes` (1 ... SVDQ_ROPE_MAX_AXES) counts >= 0.
  * batch, tokens >= 0 (0 = nothing to do); 1 <= dim <= 1024; 1 <= P, 2 P <= dim; eps finite, > 0
- * where a weight is given. */
+ * where a weight is given.  Sizes past one launch's 2^32 threads give SVDQ_ERR_SHAPE (never below
+ * 2^25 heads of tokens). */
 svdq_status svdq_rope_axes(const svdq_rope_operand* operands, int count, int batch, int tokens, int dim,
                            svdq_type type, const void* positions, int positions_fp32, int64_t position_batch,
                            const float* inv_freq, int axes, const int* axis_pairs, int halves, float eps,

@@ -1,6 +1,6 @@
 """Refusals of the block operators (svdq_add_rmsnorm, svdq_gemm_act_residual, svdq_rope_axes), on
 the CPU: the C ABI's status codes, returned before any HIP call, and the binding's argument
-checks, raised before the library is called."""
+checks, raised before the library is called; and the offline weights and frequencies."""
 import ctypes
 import os
 import shutil
@@ -10,7 +10,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from bit_w4a4_quantized_amd import binding  # noqa: E402
+from bit_w4a4_quantized_amd import binding, prepare  # noqa: E402
 from bit_w4a4_quantized_amd.binding import RopeOperand  # noqa: E402
 
 OK, NULL, SHAPE, ALIGN, FORMAT = 0, -1, -2, -3, -4
@@ -82,6 +82,14 @@ def rope(count=2, B=1, T=4, D=64, t=T16, pos=P, pf=0, pb=0, f=P, axes=(8, 24), h
 ])
 def test_rope_statuses(bad, status):
     assert rope(**bad) == status
+
+
+def test_sizes_past_one_launch():
+    """A launch holds fewer than 2^32 threads; sizes that need more are refused, not cut."""
+    assert norm(M=1 << 24, K=4096, rt=T32, xst=4096, rst=4096, rost=4096) == SHAPE
+    assert norm(M=1 << 23, K=40000, r=None, xst=40000) == SHAPE
+    assert rope(T=1 << 24, D=6, axes=(3,), heads=14) == SHAPE
+    assert rope(B=1 << 6, T=1 << 24, D=1024, axes=(512,), heads=1) == SHAPE
 
 
 # ------------------------------------------------------------------ the binding
@@ -215,3 +223,25 @@ def test_statuses_under_address_and_undefined_behaviour_sanitizers():
     r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "OK: 0 failure(s)" in r.stdout, r.stdout
+
+
+# ------------------------------------------------------------------ offline preparation
+@pytest.mark.parametrize("types,qmax", [("int8", 127.0), ("e4m3", 448.0)])
+def test_quantize_rows(types, qmax):
+    """Codes times scale give the weight back within half a step; a row of zeros has codes 0 and a finite scale."""
+    w = torch.randn(7, 40, generator=torch.Generator().manual_seed(4)) * 10.0 ** torch.arange(-3.0, 4.0)[:, None]
+    w[2] = 0
+    codes, scales = prepare.quantize_rows(w, types)
+    assert codes.shape == w.shape and codes.is_contiguous() and scales.dtype == torch.float32
+    assert bool(torch.isfinite(scales).all()) and not bool(codes[2].float().any())
+    c = codes.double()
+    assert float(c.abs().max()) == qmax
+    back = c * scales.double()[:, None]
+    step = 0.5 if types == "int8" else torch.clamp(c.abs() * 2.0 ** -4, min=2.0 ** -10)
+    assert bool(((back - w.double()).abs() <= step * scales.double()[:, None] * 1.001 + w.double().abs() * 2.0 ** -20).all())
+
+
+def test_rope_frequencies():
+    f = prepare.rope_frequencies((8, 0, 3), 100.0)
+    want = [100.0 ** (-j / 8) for j in range(8)] + [100.0 ** (-j / 3) for j in range(3)]
+    assert f.dtype == torch.float32 and torch.allclose(f.double(), torch.tensor(want, dtype=torch.float64), rtol=2.0 ** -23)

@@ -153,6 +153,27 @@ def test_norm_extremes():
     assert bool(torch.isfinite(s).all())
 
 
+@pytest.mark.parametrize("K", [700, 40000])
+@pytest.mark.parametrize("rt", [None, BF16, F32])
+@pytest.mark.parametrize("out_format", ["int8", "e4m3", "same"])
+def test_norm_not_finite(out_format, rt, K):
+    """An infinity or NaN shows in its own row's scale (or value) and in no other row."""
+    g = gen(11)
+    x, w = randn(g, 6, K).to(BF16), 1 + 0.2 * randn(g, K)
+    r = None if rt is None else randn(g, 6, K).to(rt).cuda()
+    clean = binding.svdq_add_rmsnorm(x.cuda(), w.cuda(), residual=r, out_format=out_format)
+    bad = [(1, 3, math.inf), (2, K - 1, math.nan), (4, 0, -math.inf)]
+    for row, col, v in bad:
+        x[row, col] = v
+    got = binding.svdq_add_rmsnorm(x.cuda(), w.cuda(), residual=r, out_format=out_format)
+    rows = [0, 3, 5]
+    for a, b in zip(clean, got):
+        if a is not None:
+            assert torch.equal(a.cpu()[rows].contiguous().view(torch.uint8), b.cpu()[rows].contiguous().view(torch.uint8))
+    for row, col, _ in bad:
+        assert math.isnan(float(got[0][row, col] if out_format == "same" else got[1][row]))
+
+
 def test_norm_in_place_and_streams():
     """The stream written over the residual, and over x; work on a side stream given by its handle."""
     g = gen(3)
@@ -264,6 +285,26 @@ def test_gemm_many_tiles(t, M, N, K):
 def test_gemm_few_rows(M):
     gemm_case(M, 528, 3072, TYPES[M % 4], BF16, "silu", scales=True)
     gemm_case(M, 96, 4112, TYPES[(M + 1) % 4], F16, "none", scales=True)
+
+
+@pytest.mark.parametrize("t", [E4M3, F16, BF16])
+@pytest.mark.parametrize("M", [5, 70, 300, 2500])
+def test_gemm_not_finite(t, M):
+    """NaN behind the rows of x reaches nothing; in x, w or the residual its own row, column or element."""
+    g = gen(12 + M)
+    N, K = 2060, 208
+    xb, w, r = randn(g, M, K + 16).to(t), randn(g, N, K).to(t), randn(g, M, N).to(F16)
+    clean = binding.svdq_gemm_act_residual(xb.cuda()[:, :K], w.cuda(), residual=r.cuda(), out_dtype=F16).cpu()
+    assert bool(torch.isfinite(clean).all())
+    xb[:, K:] = math.nan
+    xb[2, K - 1] = math.nan
+    w[N - 1, 0] = math.nan
+    r[0, 1] = math.nan
+    got = binding.svdq_gemm_act_residual(xb.cuda()[:, :K], w.cuda(), residual=r.cuda(), out_dtype=F16).cpu()
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[2], want[:, N - 1], want[0, 1] = True, True, True
+    assert torch.equal(torch.isnan(got), want)
+    assert torch.equal(got[~want], clean[~want])
 
 
 def test_gemm_int8_sums_are_exact():
