@@ -77,6 +77,30 @@ struct Tile {
   // the wave's longer side of tiles, and the other
   static constexpr bool XLONG = TI >= TJ;
   static constexpr int NO = XLONG ? TI : TJ, NI = XLONG ? TJ : TI;
+  // the epilogue's staging: bytes and 16-byte slots of a wave's row, rows a wave moves at once, times
+  static constexpr int RB = TJ * 64, SL = TJ * 4, PASS = 64 / SL, PASSES = TI * 32 / PASS;
+  // small tiles load the epilogue's row scales and residual before the K loop (fp16 333 x 1048 x 1999
+  // with a residual 10.7 -> 9.8 us; large ones have no registers for it)
+  static constexpr bool EARLY = TI * TJ == 1;
+  struct Rows {
+    float sx[TI];
+    uint32_t res[PASSES][4];
+  };
+  static __device__ __forceinline__ void load_rows(const Args& a, int m0, int n0, Rows& r) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int mw = m0 + wave / WN * TI * 32, nw = n0 + wave % WN * TJ * 32;
+    if (a.res) {
+#pragma unroll
+      for (int i = 0; i < PASSES; i++) {
+        const int m = mw + i * PASS + lane / SL, n = nw + lane % SL * 8;
+#pragma unroll
+        for (int j = 0; j < 4; j++) r.res[i][j] = 0;
+        if (m < a.M && n < a.N) load_piece<8>(a.res, m * a.res_stride + n, a.N - n, r.res[i]);
+      }
+    }
+#pragma unroll
+    for (int ti = 0; ti < TI; ti++) r.sx[ti] = a.xs ? a.xs[min(mw + ti * 32 + (lane & 31), a.M - 1)] : 1.f;
+  }
 
   // The tile's product over stages first ... last - 1 of K, then the epilogue, or with `part` the
   // sums as they are to this split's place there.  cs: column scales and bias of the tile, BN
@@ -171,6 +195,8 @@ struct Tile {
       load(st + R, b);
       half_stage(nb, 0, Int<PX + PW>{});
     };
+    Rows rows;
+    if (EARLY && !part) load_rows(a, m0, n0, rows);
     load(first, b0);
     load(first + 1, b1);
     if (R > 2) load(first + 2, b2);
@@ -204,7 +230,8 @@ struct Tile {
       store_part(part, acc);
     } else {
       __syncthreads();                       // nobody reads the ring any more
-      finish(a, m0, n0, b0, b1, cs, acc);
+      if (!EARLY) load_rows(a, m0, n0, rows);
+      finish(a, m0, n0, b0, b1, cs, rows, acc);
     }
   }
 
@@ -236,11 +263,9 @@ struct Tile {
   // Epilogue: each wave stages its block in 16-bit row pieces, so that global accesses take whole
   // lines.  b0, b1: LDS that nobody else uses.
   static __device__ __forceinline__ void finish(const Args& a, int m0, int n0, uint8_t* b0, uint8_t* b1, const float* cs,
-                                                const Acc (&acc)[TJ][TI]) {
+                                                const Rows& rows, const Acc (&acc)[TJ][TI]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int h = lane >> 5, r32 = lane & 31, wm = wave / WN, wn = wave % WN;
-    constexpr int RB = TJ * 64, SL = TJ * 4;                 // bytes and 16-byte slots of a staged row
-    constexpr int PASS = 64 / SL;                            // rows a wave moves at once
     static_assert(NW / 2 * TI * 32 * RB <= BUF, "the staged blocks must fit two ring buffers");
     uint8_t* ys = (wave < NW / 2 ? b0 : b1) + (wave % (NW / 2)) * TI * 32 * RB;
     const int mw = m0 + wm * TI * 32, nw = wn * TJ * 32;
@@ -252,17 +277,10 @@ struct Tile {
     const int sr = lane / SL, ss = lane % SL;                // row and slot of this lane's line pieces
     if (a.res) {
 #pragma unroll
-      for (int i = 0; i < TI * 32 / PASS; i++) {
-        const int row = i * PASS + sr, m = mw + row, n = n0 + nw + ss * 8;
-        uint32_t v[4] = {0, 0, 0, 0};
-        if (m < a.M && n < a.N) load_piece<8>(a.res, m * a.res_stride + n, a.N - n, v);
-        *at(row, ss) = make_uint4(v[0], v[1], v[2], v[3]);
-      }
+      for (int i = 0; i < PASSES; i++)
+        *at(i * PASS + sr, ss) = make_uint4(rows.res[i][0], rows.res[i][1], rows.res[i][2], rows.res[i][3]);
       sync();
     }
-    float sx[TI];
-#pragma unroll
-    for (int ti = 0; ti < TI; ti++) sx[ti] = a.xs ? a.xs[min(mw + ti * 32 + r32, a.M - 1)] : 1.f;
 #pragma unroll
     for (int tj = 0; tj < TJ; tj++)
 #pragma unroll
@@ -286,7 +304,7 @@ struct Tile {
             v[4 + j] = __uint_as_float(s[1]);
           }
 #pragma unroll
-          for (int e = 0; e < 8; e++) v[e] = activate(v[e] * sx[ti] * sw[e] + bv[e], a.act);
+          for (int e = 0; e < 8; e++) v[e] = activate(v[e] * rows.sx[ti] * sw[e] + bv[e], a.act);
           if (a.res) {
             float r[8];
             unpack8(*at(row, slot), a.bf, r);
@@ -298,7 +316,7 @@ struct Tile {
       }
     sync();
 #pragma unroll
-    for (int i = 0; i < TI * 32 / PASS; i++) {
+    for (int i = 0; i < PASSES; i++) {
       const int row = i * PASS + sr, m = mw + row, n = n0 + nw + ss * 8;
       const uint4 u = *at(row, ss);
       const uint32_t v[4] = {u.x, u.y, u.z, u.w};
