@@ -100,7 +100,7 @@ struct GemmActArgs {
 // The kernel a product takes, and the bytes its splits of K need (0: one split); with less room than
 // `part_bytes` K is split less or not at all.
 struct GemmActPlan {
-  enum Kind { FEW, T64, T64x128, T128x256, LARGE };
+  enum Kind { FEW, T64, T64x128, T128x192, T128x256, LARGE };
   int kind, splits;
   size_t bytes;
 };

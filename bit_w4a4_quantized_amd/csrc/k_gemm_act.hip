@@ -77,8 +77,10 @@ struct Tile {
   // the wave's longer side of tiles, and the other
   static constexpr bool XLONG = TI >= TJ;
   static constexpr int NO = XLONG ? TI : TJ, NI = XLONG ? TJ : TI;
-  // the epilogue's staging: bytes and 16-byte slots of a wave's row, rows a wave moves at once, times
-  static constexpr int RB = TJ * 64, SL = TJ * 4, PASS = 64 / SL, PASSES = TI * 32 / PASS;
+  // the epilogue's staging: bytes and 16-byte slots of a wave's row, the slots a lane moves, and the
+  // bits of the row that a slot is swapped by (within groups of a power of two)
+  static constexpr int RB = TJ * 64, SL = TJ * 4, PASSES = TI * 32 * SL / 64, SWAP = (SL & -SL) - 1;
+  static_assert(TI * 32 * SL % 64 == 0, "whole passes");
   // small tiles load the epilogue's row scales and residual before the K loop (fp16 333 x 1048 x 1999
   // with a residual 10.7 -> 9.8 us; large ones have no registers for it)
   static constexpr bool EARLY = TI * TJ == 1;
@@ -92,7 +94,7 @@ struct Tile {
     if (a.res) {
 #pragma unroll
       for (int i = 0; i < PASSES; i++) {
-        const int m = mw + i * PASS + lane / SL, n = nw + lane % SL * 8;
+        const int m = mw + (i * 64 + lane) / SL, n = nw + (i * 64 + lane) % SL * 8;
 #pragma unroll
         for (int j = 0; j < 4; j++) r.res[i][j] = 0;
         if (m < a.M && n < a.N) load_piece<8>(a.res, m * a.res_stride + n, a.N - n, r.res[i]);
@@ -269,16 +271,16 @@ struct Tile {
     static_assert(NW / 2 * TI * 32 * RB <= BUF, "the staged blocks must fit two ring buffers");
     uint8_t* ys = (wave < NW / 2 ? b0 : b1) + (wave % (NW / 2)) * TI * 32 * RB;
     const int mw = m0 + wm * TI * 32, nw = wn * TJ * 32;
-    auto at = [&](int row, int slot) { return reinterpret_cast<uint4*>(ys + row * RB + 16 * (slot ^ (row & (SL - 1)))); };
+    auto at = [&](int row, int slot) { return reinterpret_cast<uint4*>(ys + row * RB + 16 * (slot ^ (row & SWAP))); };
     auto sync = [&]() {                                      // the wave's own LDS writes before its reads
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     };
-    const int sr = lane / SL, ss = lane % SL;                // row and slot of this lane's line pieces
     if (a.res) {
 #pragma unroll
       for (int i = 0; i < PASSES; i++)
-        *at(i * PASS + sr, ss) = make_uint4(rows.res[i][0], rows.res[i][1], rows.res[i][2], rows.res[i][3]);
+        *at((i * 64 + lane) / SL, (i * 64 + lane) % SL) =
+            make_uint4(rows.res[i][0], rows.res[i][1], rows.res[i][2], rows.res[i][3]);
       sync();
     }
 #pragma unroll
@@ -317,7 +319,7 @@ struct Tile {
     sync();
 #pragma unroll
     for (int i = 0; i < PASSES; i++) {
-      const int row = i * PASS + sr, m = mw + row, n = n0 + nw + ss * 8;
+      const int row = (i * 64 + lane) / SL, ss = (i * 64 + lane) % SL, m = mw + row, n = n0 + nw + ss * 8;
       const uint4 u = *at(row, ss);
       const uint32_t v[4] = {u.x, u.y, u.z, u.w};
       if (m < a.M && n < a.N) store_piece<8>(a.y, m * a.y_stride + n, a.N - n, v);
@@ -448,6 +450,7 @@ hipError_t launch_type(const Args& a, const GemmActPlan& p, void* part, hipStrea
   switch (p.kind) {
     case GemmActPlan::T64: return go_split<TYPE, 2, 2, 1, 1, 3, 2>(a, p.splits, part, s);
     case GemmActPlan::T64x128: return go_split<TYPE, 2, 4, 1, 1, 3, 2>(a, p.splits, part, s);
+    case GemmActPlan::T128x192: return go<TYPE, 4, 2, 1, 3, 3, 1>(a, 1, nullptr, s);
     case GemmActPlan::T128x256: return go<TYPE, 2, 4, 2, 2, 3, 1>(a, 1, nullptr, s);
     case GemmActPlan::LARGE: return go_large<TYPE>(a, s);
     default: return hipErrorInvalidValue;
@@ -459,20 +462,21 @@ int64_t tiles_of(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) /
 }  // namespace
 
 // The kernel that costs least, in microseconds fitted to every kernel's time over M = 1 ... 4608,
-// N = 1024 ... 12288 and K = 1024 ... 12288 in int8 and bf16: of 152 such sizes the choice is the
-// best kernel or within 10% of it at 149, and within 13% at the others (777 x 3072 x 12288 in bf16:
-// 78 us, 69 in 256 x 256 tiles).  A stage of 128 bytes of K costs a CU its LDS-DMA (0.21 us
-// for each 64 x 64 tile it holds, 0.29 for 64 x 128) but no less than the ring's latency with one
-// tile (0.25); 128 x 256 tiles take 0.95 a stage and 256 x 256 1.72 with all CUs at work
-// (power-bound) and less with few.  A split of K costs the sums' round trip and a second launch
-// (2.8 us on the GPU, and 3 more that its host work counts).
+// N = 1024 ... 12288 and K = 1024 ... 12288 in int8 and bf16: of 202 such sizes the choice is the
+// best kernel or within 10% of it at 200, and within 17% at the others (65 x 3072 x 3072 in bf16:
+// 14.8 us, 12.7 in 64 x 128 tiles with more splits).  A stage of 128 bytes of K costs a CU its LDS-DMA
+// (0.21 us for each 64 x 64 tile it holds, 0.29 for 64 x 128) but no less than the ring's latency
+// with one tile (0.25).  With all CUs at work 128 x 192 tiles take 0.7 a stage, 128 x 256 0.95 and
+// 256 x 256 1.72 (power-bound), and less with few.  A split of K costs the sums' round trip and a
+// second launch (2.8 us on the GPU, and 3 more that its host work counts).
 //
 // Both sides, in us, int8 (M x K x N): few rows / tiles 1 x 3072 x 12288 8.9 / 10.6, 17 x 3072 x 12288
 // 9.3 / 10.7, 33 x 3072 x 12288 13.7 / 10.9, 64 x 3072 x 3072 6.7 / 8.2; 64 x 64 / 64 x 128 tiles
-// 65 x 3072 x 3072 8.8 / 10.0, 512 x 3072 x 3072 13.9 / 12.3; 64 x 128 / 128 x 256
-// 256 x 3072 x 12288 19.0 / 22.5, 512 x 3072 x 12288 28.4 / 26.2; 128 x 256 / 256 x 256
-// 2048 x 3072 x 3072 25.9 / 30.6, 4608 x 3072 x 12288 183 / 170; 64 x 12288 x 3072 26.5 whole, 14.5
-// in five splits.
+// 65 x 3072 x 3072 8.8 / 10.0, 512 x 3072 x 3072 13.9 / 12.3; 64 x 128 / 128 x 192 384 x 3072 x 3072
+// 12.0 / 17.9, 512 x 3072 x 9216 26.5 / 21.0; 128 x 192 / 128 x 256 the same 21.0 / 23.0,
+// 777 x 3072 x 9216 38.5 / 28.9; 128 x 192 / 256 x 256 1536 x 3072 x 3072 21.1 / 28.2,
+// 3000 x 12288 x 3072 125 / 119; 128 x 256 / 256 x 256 777 x 3072 x 9216 28.9 / 40.3,
+// 4608 x 3072 x 12288 183 / 170; 64 x 12288 x 3072 26.5 whole, 14.5 in five splits.
 GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
   const double cus = resident_workgroups() / 2;
   const double S = (KB + BK - 1) / BK;
@@ -499,9 +503,12 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
     consider(GemmActPlan::T64, splits, (c64 > 1 ? 0.21 * ceil(c64) * st + 3 : 0.25 * st + 3.7) + 0.5 * c64 + join(b64), b64);
     consider(GemmActPlan::T64x128, splits, 0.29 * c128 * st + 4 + c128 + join(b128), b128);
   }
-  // rounds of 256 workgroups, the last with its share of CUs at work
-  const double t2 = tiles_of(M, N, 128, 256), whole2 = floor(t2 / cus), rest2 = t2 - whole2 * cus;
-  consider(GemmActPlan::T128x256, 1, whole2 * (0.95 * S + 5.5) + (rest2 > 0 ? (0.55 + 0.4 * rest2 / cus) * S + 6.5 : 0), 0);
+  // rounds of one workgroup a CU, the last with its share of CUs at work
+  const double t1 = tiles_of(M, N, 128, 192) / cus, whole1 = floor(t1), rest1 = t1 - whole1;
+  consider(GemmActPlan::T128x192, 1,
+           whole1 * (0.7 * S + 8) + (rest1 > 0 ? (0.4 + 0.15 * rest1) * S + (whole1 > 0 ? 4.5 : 10) : 0), 0);
+  const double t2 = tiles_of(M, N, 128, 256) / cus, whole2 = floor(t2), rest2 = t2 - whole2;
+  consider(GemmActPlan::T128x256, 1, whole2 * (0.95 * S + 5.5) + (rest2 > 0 ? (0.5 + 0.3 * rest2) * S + 8 : 0), 0);
   const double tl = tiles_of(M, N, 256, 256), whole = floor(tl / cus), rest = tl - whole * cus;
   const double tail = rest == 0          ? 0
                       : 4 * rest <= cus ? 0.65 * S + 6.5

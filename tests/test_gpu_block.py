@@ -281,6 +281,12 @@ def test_gemm_many_tiles(t, M, N, K):
     gemm_case(M, N, K, t, F16, "gelu")
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,N,K,ypad", [(500, 9201, 2064, 0), (770, 9210, 2064, 6), (1000, 3075, 4112, 5)])
+def test_gemm_wide_tiles(t, M, N, K, ypad):
+    gemm_case(M, N, K, t, BF16, "silu", ypad=ypad)
+
+
 @pytest.mark.parametrize("M", [1, 2, 5, 8, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 96, 128, 160])
 def test_gemm_few_rows(M):
     gemm_case(M, 528, 3072, TYPES[M % 4], BF16, "silu", scales=True)
