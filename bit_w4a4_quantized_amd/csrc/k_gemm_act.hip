@@ -142,7 +142,7 @@ struct Tile {
     const int xb = (wm * TI * 32 + r32) * BK, wb = BM * BK + (wn * TJ * 32 + r32) * BK;
     const int ob = XLONG ? xb : wb, ib = XLONG ? wb : xb;
     auto read = [&](const uint8_t* b, int base, int half, int j, int tile) {
-      return *reinterpret_cast<const uint4*>(b + base + (swz ^ (64 * half + 32 * j)) + tile * 32 * BK);
+      return lds_piece(b, base + (swz ^ (64 * half + 32 * j)) + tile * 32 * BK);
     };
     Acc acc[TJ][TI];
 #pragma unroll
@@ -151,44 +151,54 @@ struct Tile {
       for (int ti = 0; ti < TI; ti++)
 #pragma unroll
         for (int i = 0; i < 16; i++) acc[tj][ti][i] = 0;
-    // the MFMA of piece j (both pieces for FP8) of long-side tile o and short-side tile i
+    // the MFMA of piece j of long-side tile o and short-side tile i (E4M3: two, of the piece's halves;
+    // the short side's fp16 is kept for all o)
     uint4 fo[NO][2], fi[NI][2], fn[NI][2];
-    auto mma = [&](int o, int i, int j) {
-      const uint4 (&x)[2] = XLONG ? fo[o] : fi[i];
-      const uint4 (&w)[2] = XLONG ? fi[i] : fo[o];
+    auto operand = [](const uint4& u, int e) {
+      return TYPE == T_E4M3 ? __builtin_bit_cast(uint4, e4m3_half(u, e)) : u;
+    };
+    auto mfma = [&](int o, int i, const uint4& u, const uint4& v) {
+      const uint4 &x = XLONG ? u : v, &w = XLONG ? v : u;
       Acc& c = XLONG ? acc[i][o] : acc[o][i];
-      if constexpr (TYPE == T_E4M3)
-        c = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(as_i8(w[0], w[1]), as_i8(x[0], x[1]), c, 0, 0, 0, 0, 0, 0);
-      else if constexpr (TYPE == T_INT8)
-        c = __builtin_amdgcn_mfma_i32_32x32x32_i8(as_i4(w[j]), as_i4(x[j]), c, 0, 0, 0);
-      else if constexpr (TYPE == T_F16)
-        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(w[j]), as_h8(x[j]), c, 0, 0, 0);
+      if constexpr (TYPE == T_INT8)
+        c = __builtin_amdgcn_mfma_i32_32x32x32_i8(as_i4(w), as_i4(x), c, 0, 0, 0);
+      else if constexpr (TYPE == T_BF16)
+        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf8(w), as_bf8(x), c, 0, 0, 0);
       else
-        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf8(w[j]), as_bf8(x[j]), c, 0, 0, 0);
+        c = __builtin_amdgcn_mfma_f32_32x32x16_f16(as_h8(w), as_h8(x), c, 0, 0, 0);
     };
     // Half a stage's MFMAs, with the next half's fragments (half `half` of the stage in nb) read
     // behind them: the short side's into a second set, the long side's each over the one its MFMAs
     // have used, so that both and a large tile's accumulators fit the registers.
-    constexpr int NJ = TYPE == T_E4M3 ? 1 : 2;
+    constexpr int NH = TYPE == T_E4M3 ? 2 : 1;               // MFMAs a piece
     auto half_stage = [&](const uint8_t* nb, int half, auto loads) {
 #pragma unroll
       for (int i = 0; i < NI; i++)
 #pragma unroll
         for (int j = 0; j < 2; j++) fn[i][j] = read(nb, ib, half, j, i);
 #pragma unroll
-      for (int j = 0; j < NJ; j++)
+      for (int j = 0; j < 2; j++) {
+        uint4 si[NI][NH];
+#pragma unroll
+        for (int i = 0; i < NI; i++)
+#pragma unroll
+          for (int e = 0; e < NH; e++) si[i][e] = operand(fi[i][j], e);
 #pragma unroll
         for (int o = 0; o < NO; o++) {
 #pragma unroll
-          for (int i = 0; i < NI; i++) mma(o, i, j);
+          for (int e = 0; e < NH; e++) {
+            const uint4 so = operand(fo[o][j], e);
 #pragma unroll
-          for (int k = j; k < 2; k += NJ) fo[o][k] = read(nb, ob, half, k, o);
+            for (int i = 0; i < NI; i++) mfma(o, i, so, si[i][e]);
+          }
+          fo[o][j] = read(nb, ob, half, j, o);
         }
+      }
 #pragma unroll
       for (int i = 0; i < NI; i++)
 #pragma unroll
         for (int j = 0; j < 2; j++) fi[i][j] = fn[i][j];
-      interleave<0, NJ * NO * NI, 2 * (NO + NI), decltype(loads)::value>();
+      interleave<0, 2 * NH * NO * NI, 2 * (NO + NI), decltype(loads)::value>();
       __builtin_amdgcn_sched_barrier(0);
     };
     // stage st in b (its first half already in registers), stage st + 1 in nb; stage st + R goes into b
@@ -478,7 +488,23 @@ int64_t tiles_of(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) /
 // 777 x 3072 x 9216 38.5 / 28.9; 128 x 192 / 256 x 256 1536 x 3072 x 3072 21.1 / 28.2,
 // 3000 x 12288 x 3072 125 / 119; 128 x 256 / 256 x 256 777 x 3072 x 9216 28.9 / 40.3,
 // 4608 x 3072 x 12288 183 / 170; 64 x 12288 x 3072 26.5 whole, 14.5 in five splits.
-GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
+//
+// E4M3 has its own constants: its products take the time of 16-bit ones (twice an 8-bit stage's
+// MFMAs) and the conversion to fp16 comes on top, so that the matrix cores and the vector units
+// bound the stages that LDS-DMA bounds in the other types.  Of 114 sizes the choice is the best
+// kernel or within 9% of it.  With the other types' constants 777 x 12288 x 3072 took 93 us in
+// 128 x 192 tiles (64 x 64: 74) and 384 x 6144 x 6144 51 (39).
+struct Costs {
+  double few, few_rows;                      // few rows: a turn of K, and more for each 16 rows
+  double t64, t64_one, t64x128;              // a stage, 64 x 64 tiles with several and one a CU; 64 x 128
+  double t192, t192_rest, t192_share;        // a stage with all CUs at work; with few, and more for their share
+  double t256, t256_rest, t256_share;
+  double large, quarter, quarter_share, half, rest, share;
+};
+constexpr Costs kCosts{0.19, 0.055, 0.21, 0.25, 0.29, 0.7, 0.4, 0.15, 0.95, 0.5, 0.3, 1.72, 0.65, 0, 0.85, 0.75, 0.95};
+constexpr Costs kCostsE4M3{0.2, 0.06, 0.28, 0.32, 0.46, 1.2, 0.75, 0.4, 1.57, 1.0, 0.4, 2.75, 0.65, 0.6, 1.2, 1.2, 1.6};
+
+GemmActPlan plan(int M, int N, int KB, int64_t part_bytes, const Costs& t) {
   const double cus = resident_workgroups() / 2;
   const double S = (KB + BK - 1) / BK;
   GemmActPlan best{};
@@ -492,7 +518,8 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
   if (M <= kFewRows) {
     const int ti = (M + 15) / 16;
     const double c = (N + 15) / 16 / cus, rounds = ceil(c / (ti <= 2 ? 3 : 2));
-    consider(GemmActPlan::FEW, 1, ceil(S / 4) * ceil(c) * (0.19 + 0.055 * ti) + 3.2 + 0.25 * ti + 0.3 * c + 1.5 * (rounds - 1), 0);
+    consider(GemmActPlan::FEW, 1,
+             ceil(S / 4) * ceil(c) * (t.few + t.few_rows * ti) + 3.2 + 0.25 * ti + 0.3 * c + 1.5 * (rounds - 1), 0);
   }
   for (int splits = 1; splits <= 16; splits++) {
     if (splits > 1 && S / splits < 4) break;
@@ -501,21 +528,23 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
     const int64_t t64 = tiles_of(M, N, 64, 64), t128 = tiles_of(M, N, 64, 128);
     const double c64 = (double)(t64 * splits) / cus, c128 = ceil((double)(t128 * splits) / cus);
     const int64_t b64 = splits > 1 ? t64 * splits * 64 * 64 * 4 : 0, b128 = splits > 1 ? t128 * splits * 64 * 128 * 4 : 0;
-    consider(GemmActPlan::T64, splits, (c64 > 1 ? 0.21 * ceil(c64) * st + 3 : 0.25 * st + 3.7) + 0.5 * c64 + join(b64), b64);
-    consider(GemmActPlan::T64x128, splits, 0.29 * c128 * st + 4 + c128 + join(b128), b128);
+    consider(GemmActPlan::T64, splits, (c64 > 1 ? t.t64 * ceil(c64) * st + 3 : t.t64_one * st + 3.7) + 0.5 * c64 + join(b64),
+             b64);
+    consider(GemmActPlan::T64x128, splits, t.t64x128 * c128 * st + 4 + c128 + join(b128), b128);
   }
   // rounds of one workgroup a CU, the last with its share of CUs at work
   const double t1 = tiles_of(M, N, 128, 192) / cus, whole1 = floor(t1), rest1 = t1 - whole1;
   consider(GemmActPlan::T128x192, 1,
-           whole1 * (0.7 * S + 8) + (rest1 > 0 ? (0.4 + 0.15 * rest1) * S + (whole1 > 0 ? 4.5 : 10) : 0), 0);
+           whole1 * (t.t192 * S + 8) + (rest1 > 0 ? (t.t192_rest + t.t192_share * rest1) * S + (whole1 > 0 ? 4.5 : 10) : 0), 0);
   const double t2 = tiles_of(M, N, 128, 256) / cus, whole2 = floor(t2), rest2 = t2 - whole2;
-  consider(GemmActPlan::T128x256, 1, whole2 * (0.95 * S + 5.5) + (rest2 > 0 ? (0.5 + 0.3 * rest2) * S + 8 : 0), 0);
+  consider(GemmActPlan::T128x256, 1,
+           whole2 * (t.t256 * S + 5.5) + (rest2 > 0 ? (t.t256_rest + t.t256_share * rest2) * S + 8 : 0), 0);
   const double tl = tiles_of(M, N, 256, 256), whole = floor(tl / cus), rest = tl - whole * cus;
   const double tail = rest == 0          ? 0
-                      : 4 * rest <= cus ? 0.65 * S + 6.5
-                      : 2 * rest <= cus ? 0.85 * S + 11
-                                        : (0.75 + 0.95 * rest / cus) * S + 14;
-  consider(GemmActPlan::LARGE, 1, whole * (1.72 * S + 6) + tail, 0);
+                      : 4 * rest <= cus ? (t.quarter + t.quarter_share * rest / cus) * S + 6.5
+                      : 2 * rest <= cus ? t.half * S + 11
+                                        : (t.rest + t.share * rest / cus) * S + 14;
+  consider(GemmActPlan::LARGE, 1, whole * (t.large * S + 6) + tail, 0);
   return best;
 }
 
@@ -523,7 +552,8 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes) {
 
 GemmActPlan gemm_act_plan(int M, int N, int K, int type, size_t part_bytes) {
   const int eb = type == T_F16 || type == T_BF16 ? 2 : 1;
-  return gact::plan(M, N, K * eb, part_bytes > (size_t)1 << 40 ? (int64_t)1 << 40 : (int64_t)part_bytes);
+  return gact::plan(M, N, K * eb, part_bytes > (size_t)1 << 40 ? (int64_t)1 << 40 : (int64_t)part_bytes,
+                    type == T_E4M3 ? gact::kCostsE4M3 : gact::kCosts);
 }
 
 hipError_t launch_gemm_act(const GemmActArgs& g, hipStream_t s) {
@@ -544,7 +574,7 @@ hipError_t launch_gemm_act(const GemmActArgs& g, hipStream_t s) {
   a.bf = g.out_type == T_BF16;
   a.y = g.y;
   a.y_stride = g.y_stride;
-  const GemmActPlan p = gact::plan(a.M, a.N, a.KB, (int64_t)g.part_bytes);
+  const GemmActPlan p = gemm_act_plan(g.M, g.N, g.K, g.type, g.part_bytes);
   if (p.kind == GemmActPlan::FEW) return gact::launch_few(a, g.type, s);
   switch (g.type) {
     case T_INT8: return gact::launch_type<T_INT8>(a, p, g.part, s);

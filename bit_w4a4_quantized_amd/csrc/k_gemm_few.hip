@@ -31,17 +31,30 @@ struct Mma<T_INT8> {
   using Acc = v4i;
 };
 
+// A piece's MFMA operands: one, or for E4M3 its two halves in fp16.
 template <int TYPE>
-__device__ __forceinline__ void mma(const uint4 (&w)[2], const uint4 (&x)[2], typename Mma<TYPE>::Acc& acc) {
-  if constexpr (TYPE == T_E4M3) {
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(as_i8(w[0], w[1]), as_i8(x[0], x[1]), acc, 0, 0, 0, 0, 0, 0);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; j++) {
-      if constexpr (TYPE == T_INT8) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i4(w[j]), as_i4(x[j]), acc, 0, 0, 0);
-      else if constexpr (TYPE == T_F16) acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(w[j]), as_h8(x[j]), acc, 0, 0, 0);
-      else acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf8(w[j]), as_bf8(x[j]), acc, 0, 0, 0);
+struct Frag {
+  uint4 v[TYPE == T_E4M3 ? 2 : 1];
+  __device__ __forceinline__ explicit Frag(const uint4& u) {
+    if constexpr (TYPE == T_E4M3) {
+      v[0] = __builtin_bit_cast(uint4, e4m3_half(u, 0));
+      v[1] = __builtin_bit_cast(uint4, e4m3_half(u, 1));
+    } else {
+      v[0] = u;
     }
+  }
+};
+template <int TYPE>
+__device__ __forceinline__ void mma(const Frag<TYPE>& w, const Frag<TYPE>& x, typename Mma<TYPE>::Acc& acc) {
+  if constexpr (TYPE == T_E4M3) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(w.v[0]), as_h8(x.v[0]), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(w.v[1]), as_h8(x.v[1]), acc, 0, 0, 0);
+  } else if constexpr (TYPE == T_INT8) {
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(as_i4(w.v[0]), as_i4(x.v[0]), acc, 0, 0, 0);
+  } else if constexpr (TYPE == T_F16) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(as_h8(w.v[0]), as_h8(x.v[0]), acc, 0, 0, 0);
+  } else {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf8(w.v[0]), as_bf8(x.v[0]), acc, 0, 0, 0);
   }
 }
 
@@ -96,18 +109,21 @@ __global__ void __launch_bounds__(256) k_gemm_few(Args a) {
   auto step = [&](int st, uint8_t* b) {
     wait_loads<(R - 1) * L>();               // stage st is in
     uint4 w[2], x[TI][2];
-    const uint8_t* p = b + wave * BUF;
 #pragma unroll
     for (int j = 0; j < 2; j++) {
-      const int slot = 16 * ((q + 4 * j) ^ ((r16 >> 1) & 7));
-      w[j] = *reinterpret_cast<const uint4*>(p + r16 * BK + slot);
+      const int at = wave * BUF + r16 * BK + 16 * ((q + 4 * j) ^ ((r16 >> 1) & 7));
+      w[j] = lds_piece(b, at);
 #pragma unroll
-      for (int t = 0; t < TI; t++) x[t][j] = *reinterpret_cast<const uint4*>(p + 2048 + (t * 16 + r16) * BK + slot);
+      for (int t = 0; t < TI; t++) x[t][j] = lds_piece(b, at + 2048 + t * 16 * BK);
     }
     wait_loads<(R - 1) * L>();               // the reads are done: the stage's bytes may be loaded again
     load(st + R, b);
 #pragma unroll
-    for (int t = 0; t < TI; t++) mma<TYPE>(w, x[t], acc[t]);
+    for (int j = 0; j < 2; j++) {
+      const Frag<TYPE> fw(w[j]);
+#pragma unroll
+      for (int t = 0; t < TI; t++) mma<TYPE>(fw, Frag<TYPE>(x[t][j]), acc[t]);
+    }
   };
   load(0, b0);
   load(1, b1);

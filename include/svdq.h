@@ -430,8 +430,8 @@ svdq_status svdq_add_rmsnorm(const void* x, int64_t x_stride, svdq_type x_type, 
  * INT8 sums are exact in int32 (K <= 2^17 for INT8: 2^17 * 127^2 < 2^31).  x and w are 16-byte
  * aligned, K and x_stride multiples of 16 bytes, and a row of either (x_stride for x) takes at
  * most 4 MiB.  Any M >= 0 and N >= 0 up to 2^24, at most 2^31 - 1 output tiles of 64 x 64; strides
- * >= the row's length.  E4M3: the matrix cores add eight products at a time with 13 bits below the
- * largest of the eight, and those sums in fp32.
+ * >= the row's length.  E4M3 products are exact and their sums fp32, as for 16-bit types (and at their
+ * rate: the FP8 matrix instructions drop small products beside a large one).
  *   workspace, workspace_bytes : caller-owned device scratch, 16-byte aligned, for the sums of K's
  *           splits when few output tiles leave CUs idle (svdq_gemm_act_residual_workspace_bytes).
  *           Its contents need no initialisation and are dead after the call; two calls in flight at
