@@ -585,10 +585,22 @@ def _vector(t, dtypes, n, what):
                          f"got {tuple(t.shape)} {t.dtype}")
 
 
-def _launch(fn, args, tensors, made, stream):
-    """One C call on the tensors' device: on `stream` when given, else on that device's current
-    stream.  tensors: the caller's; made: those allocated for this call (the allocator learns that
-    another stream than theirs uses them)."""
+def _new_on(stream, shape, dtype, device, returned=True):
+    """torch.empty from the pool of `stream`, a handle: what a call writes there must not be a block
+    that the current stream has freed and may still be using.  A returned tensor may be used and
+    freed on the current stream, so the allocator learns of that stream too."""
+    import torch
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(here)
+    return t
+
+
+def _launch(fn, args, tensors, stream):
+    """One C call on the device of the tensors, the caller's: on `stream` when given, else on that
+    device's current stream."""
     dev = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
@@ -602,9 +614,6 @@ def _launch(fn, args, tensors, made, stream):
             st = getattr(lib(), fn)(*args, d.raw_stream(dev) if stream is None else stream)
     if st != 0:
         raise SvdqError(fn, st)
-    if stream is not None:
-        for t in made:
-            t.record_stream(torch.cuda.ExternalStream(stream, device=dev))
 
 
 def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=None, scales=None,
@@ -642,20 +651,18 @@ def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=
     if scales is not None:
         _need(scales, torch.float32, (M,), "scales")
     given = (x, weight, residual, out, scales, residual_out)
-    made = []
+    new = torch.empty if stream is None else functools.partial(_new_on, stream)
     if out is None:
-        out = torch.empty(shape, dtype=od, device=x.device)
-        made.append(out)
+        out = new(shape, dtype=od, device=x.device)
     if scales is None and od is not xd:
-        scales = torch.empty(M, dtype=torch.float32, device=x.device)
-        made.append(scales)
+        scales = new((M,), dtype=torch.float32, device=x.device)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual) if rs == K else torch.empty(shape, dtype=residual.dtype, device=x.device)
+        residual_out = torch.empty_like(residual) if rs == K and stream is None else \
+            new(shape, dtype=residual.dtype, device=x.device)
         ros = K
-        made.append(residual_out)
     _launch("svdq_add_rmsnorm",
             (x.data_ptr(), xs, code[xd], _p(residual), rs, rt, weight.data_ptr(), code[weight.dtype], eps, M, K,
-             code[od], out.data_ptr(), _p(scales), _p(residual_out), ros), given, made, stream)
+             code[od], out.data_ptr(), _p(scales), _p(residual_out), ros), given, stream)
     return out, scales, residual_out
 
 
@@ -695,24 +702,23 @@ def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none",
         _vector(bias, (out_dtype,), N, "bias")
     rs = 0 if residual is None else _rows(residual, (out_dtype,), (M, N), "residual")
     given = (x, w, xs, ws, bias, residual, y, workspace)
-    made = []
     if workspace is not None:
         _need(workspace, None, None, "workspace")
         room = workspace.numel() * workspace.element_size()
     else:
         room = gemm_act_residual_workspace_bytes(M, N, K, code[dtype])
         if room:
-            workspace = torch.empty(room, dtype=torch.uint8, device=x.device)
-            made.append(workspace)
+            workspace = torch.empty(room, dtype=torch.uint8, device=x.device) if stream is None else \
+                _new_on(stream, room, torch.uint8, x.device, returned=False)
     if y is not None:
         yt = _rows(y, (out_dtype,), (M, N), "y")
     else:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device)
+        y = torch.empty((M, N), dtype=out_dtype, device=x.device) if stream is None else \
+            _new_on(stream, (M, N), out_dtype, x.device)
         yt = N
-        made.append(y)
     _launch("svdq_gemm_act_residual",
             (x.data_ptr(), xt, _p(xs), w.data_ptr(), _p(ws), _p(bias), _p(residual), rs, M, N, K, code[dtype], act,
-             code[out_dtype], y.data_ptr(), yt, _p(workspace), room), given, made, stream)
+             code[out_dtype], y.data_ptr(), yt, _p(workspace), room), given, stream)
     return y
 
 
@@ -770,6 +776,12 @@ def _rope_plan(q, k, q_out, k_out, positions, axis_pairs, heads_first):
     return bytes(ops), (B, T, D), sum(axis_pairs), (_c_int * axes)(*axis_pairs), pos_batch, shapes
 
 
+def _rope_out(x, shape, stream):
+    if stream is not None:
+        return _new_on(stream, shape, x.dtype, x.device)
+    return _dtypes.torch.empty_like(x) if shape == x.shape and x.is_contiguous() else x.new_empty(shape)
+
+
 def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_weight=None, k_weight=None, eps=1e-6,
                    inverse=False, heads_first=False, q_out=None, k_out=None, stream=None):
     """Rotary positions with several axes on q [batch, tokens, heads, dim] and k (the same with its
@@ -804,27 +816,24 @@ def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_we
     _vector(inv_freq, d.f32, P, "inv_freq")
     ops = _RopeOperands.from_buffer_copy(blank)
     given = (q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
-    made = []
     if q_weight is not None:
         _vector(q_weight, d.f32, D, "q_weight")
         ops[0].weight = q_weight.data_ptr()
     if q_out is None:
-        q_out = torch.empty_like(q) if shapes[0] == q.shape and q.is_contiguous() else q.new_empty(shapes[0])
-        made.append(q_out)
+        q_out = _rope_out(q, shapes[0], stream)
     ops[0].inp, ops[0].out = q.data_ptr(), q_out.data_ptr()
     if k is not None:
         if k_weight is not None:
             _vector(k_weight, d.f32, D, "k_weight")
             ops[1].weight = k_weight.data_ptr()
         if k_out is None:
-            k_out = torch.empty_like(k) if shapes[1] == k.shape and k.is_contiguous() else k.new_empty(shapes[1])
-            made.append(k_out)
+            k_out = _rope_out(k, shapes[1], stream)
         ops[1].inp, ops[1].out = k.data_ptr(), k_out.data_ptr()
     _launch("svdq_rope_axes",
             (ctypes.addressof(ops), 1 if k is None else 2, B, T, D, d.code[dtype], positions.data_ptr(),
              1 if positions.dtype == torch.float32 else 0, pos_batch, inv_freq.data_ptr(), len(axis_pairs), axes,
              1 if pairs == "halves" else 0, eps, 1 if inverse else 0),
-            given, made, stream)
+            given, stream)
     return q_out, k_out
 
 

@@ -45,3 +45,33 @@ def test_gemm_sums_beside_large_products(M, N, K, t, big):
     want = x.cuda().to(F64) @ w.cuda().to(F64).T
     assert float(want.abs().max()) < 2048
     assert torch.equal(y.to(F64), want)
+
+
+# ------------------------------------------------------------------ other streams
+def block_calls():
+    g = gen(21)
+    x, r, w = (torch.randn(*s, generator=g).to(BF16).cuda() for s in ((70, 4096), (70, 4096), (96, 4096)))
+    n, q, f = torch.ones(4096).cuda(), torch.randn(5, 4, 64, generator=g).to(F16).cuda(), torch.rand(32).cuda()
+    pos = torch.arange(5, dtype=torch.int32).unsqueeze(-1).cuda()
+    return [lambda s: binding.svdq_add_rmsnorm(x, n, residual=r, stream=s),
+            lambda s: (binding.svdq_gemm_act_residual(x, w, stream=s),),            # K split: a workspace
+            lambda s: binding.svdq_rope_axes(q, q, pos, f, (32,), stream=s)]
+
+
+def test_calls_on_another_stream():
+    """A stream's handle, and 0 for the default stream: the same bits, in memory that the current
+    stream has not just freed."""
+    assert binding.gemm_act_residual_workspace_bytes(70, 96, 4096, 1) > 0
+    side = torch.cuda.Stream()
+    for call in block_calls():
+        want = call(None)
+        torch.cuda.synchronize()
+        for handle in (side.cuda_stream, 0):
+            got = call(handle)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got))
+        freed = {t.data_ptr() for t in call(None)}          # handed back to the current stream's pool
+        got = call(side.cuda_stream)
+        assert not freed & {t.data_ptr() for t in got}
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
