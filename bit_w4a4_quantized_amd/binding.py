@@ -123,6 +123,31 @@ def _raw_stream_fn():
     return lambda dev: torch.cuda.current_stream(dev).cuda_stream
 
 
+def _new_on(stream, shape, dtype, device, returned=True):
+    """torch.empty from the pool of `stream`, a handle: what a call writes there must not be a block
+    that the current stream has freed and may still be using.  A returned tensor may be used and
+    freed on the current stream, so the allocator learns of that stream too."""
+    import torch
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(here)
+    return t
+
+
+def _new(stream, shape, dtype, device):
+    """torch.empty where a call on `stream` (None: the current one) may write at once."""
+    import torch
+    return torch.empty(shape, dtype=dtype, device=device) if stream is None else _new_on(stream, shape, dtype, device)
+
+
+def _new_workspace(stream, nbytes, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if stream is None else \
+        _new_on(stream, nbytes, torch.uint8, device, returned=False)
+
+
 def _check(name: str, st: int):
     if st != 0:
         raise SvdqError(name, st)
@@ -260,7 +285,7 @@ def quantize_down_workspace_bytes(M: int, K: int, r: int, fmt) -> int:
     return int(lib().svdq_quantize_down_workspace_bytes(M, K, r, _fmt(fmt)))
 
 
-def _outputs_kernel_a(M, K, r, fmt, dev, xq, xs, t):
+def _outputs_kernel_a(M, K, r, fmt, dev, xq, xs, t, stream):
     """Kernel A's outputs: every given one is checked before any missing one is allocated."""
     import torch
     if xq is not None:
@@ -273,21 +298,20 @@ def _outputs_kernel_a(M, K, r, fmt, dev, xq, xs, t):
     else:
         _absent(t, "t", "when l1t is None (no branch)")
     if xq is None:
-        xq = torch.empty(code_shape(M, K, fmt), dtype=torch.uint8, device=dev)
+        xq = _new(stream, code_shape(M, K, fmt), torch.uint8, dev)
     if xs is None:
-        xs = torch.empty(scale_shape(M, K, fmt), dtype=scale_dtype(fmt), device=dev)
+        xs = _new(stream, scale_shape(M, K, fmt), scale_dtype(fmt), dev)
     if r and t is None:
-        t = torch.empty((M, r), dtype=torch.float16, device=dev)
+        t = _new(stream, (M, r), torch.float16, dev)
     return xq, xs, t
 
 
-def _workspace_kernel_a(M, K, r, fmt, dev, workspace, no_workspace):
-    import torch
+def _workspace_kernel_a(M, K, r, fmt, dev, workspace, no_workspace, stream):
     if no_workspace:
         return None, 0
     if workspace is None:
         nb = quantize_down_workspace_bytes(M, K, r, fmt)
-        workspace = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+        workspace = _new_workspace(stream, nb, dev) if nb else None
     else:
         _need(workspace, None, None, "workspace")
     return workspace, (0 if workspace is None else workspace.numel() * workspace.element_size())
@@ -305,8 +329,8 @@ def svdq_quantize_down(x_hat, l1t, fmt, xq=None, xs=None, t=None, workspace=None
     if l1t is not None:
         _need(l1t, torch.float16, (r, K), "l1t")
     dev = x_hat.device
-    xq, xs, t = _outputs_kernel_a(M, K, r, fmt, dev, xq, xs, t)
-    workspace, ws_bytes = _workspace_kernel_a(M, K, r, fmt, dev, workspace, no_workspace)
+    xq, xs, t = _outputs_kernel_a(M, K, r, fmt, dev, xq, xs, t, stream)
+    workspace, ws_bytes = _workspace_kernel_a(M, K, r, fmt, dev, workspace, no_workspace, stream)
     _check("svdq_quantize_down", lib().svdq_quantize_down(
         _p(x_hat), _p(l1t), M, K, r, _fmt(fmt), _p(xq), _p(xs), _p(t), _p(workspace), ws_bytes,
         _stream(stream)))
@@ -318,13 +342,13 @@ def svdq_gemm_w4a4_up(xq, xs, t, wq, ws, l2, bias, K, fmt, y=None, stream=None):
     import torch
     M, N, r = _check_kernel_b(xq, xs, t, wq, ws, l2, bias, K, fmt, y)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=xq.device)
+        y = _new(stream, (M, N), torch.float16, xq.device)
     _check("svdq_gemm_w4a4_up", lib().svdq_gemm_w4a4_up(
         _p(xq), _p(xs), _p(t), _p(wq), _p(ws), _p(l2), _p(bias), M, N, K, r, _fmt(fmt), _p(y), _stream(stream)))
     return y
 
 
-def _layer_args(x, l1t, wq, ws, l2, bias, fmt, y, workspace, need_fn, what="x_hat"):
+def _layer_args(x, l1t, wq, ws, l2, bias, fmt, y, workspace, stream, need_fn, what="x_hat"):
     """Checks of a whole-layer call's tensors; returns (M, N, K, r, y, workspace, bytes)."""
     import torch
     _need(x, torch.float16, None, what)
@@ -334,12 +358,12 @@ def _layer_args(x, l1t, wq, ws, l2, bias, fmt, y, workspace, need_fn, what="x_ha
     if bias is not None:
         _need(bias, torch.float16, (N,), "bias")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _new(stream, (M, N), torch.float16, x.device)
     else:
         _need(y, torch.float16, (M, N), "y")
     need = need_fn(M, N, K, r)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _new_workspace(stream, max(need, 16), x.device)
     else:
         _need(workspace, None, None, "workspace")
     return M, N, K, r, y, workspace, workspace.numel() * workspace.element_size()
@@ -347,7 +371,7 @@ def _layer_args(x, l1t, wq, ws, l2, bias, fmt, y, workspace, need_fn, what="x_ha
 
 def svdq_linear(x_hat, l1t, wq, ws, l2, bias, fmt, workspace=None, y=None, stream=None):
     """Kernel A then Kernel B.  Returns y fp16 [M, N]."""
-    M, N, K, r, y, workspace, wb = _layer_args(x_hat, l1t, wq, ws, l2, bias, fmt, y, workspace,
+    M, N, K, r, y, workspace, wb = _layer_args(x_hat, l1t, wq, ws, l2, bias, fmt, y, workspace, stream,
                                                lambda M, N, K, r: linear_workspace_bytes(M, K, r, fmt))
     _check("svdq_linear", lib().svdq_linear(
         _p(x_hat), _p(l1t), _p(wq), _p(ws), _p(l2), _p(bias), M, N, K, r, _fmt(fmt),
@@ -355,7 +379,7 @@ def svdq_linear(x_hat, l1t, wq, ws, l2, bias, fmt, workspace=None, y=None, strea
     return y
 
 
-def _outputs_weight(N, K, fmt, dev, wq, ws):
+def _outputs_weight(N, K, fmt, dev, wq, ws, stream):
     """The weight quantizer's outputs: every given one is checked before any missing one is
     allocated."""
     import torch
@@ -364,9 +388,9 @@ def _outputs_weight(N, K, fmt, dev, wq, ws):
     if ws is not None:
         _need(ws, scale_dtype(fmt), scale_shape(N, K, fmt), "ws")
     if wq is None:
-        wq = torch.empty(code_shape(N, K, fmt), dtype=torch.uint8, device=dev)
+        wq = _new(stream, code_shape(N, K, fmt), torch.uint8, dev)
     if ws is None:
-        ws = torch.empty(scale_shape(N, K, fmt), dtype=scale_dtype(fmt), device=dev)
+        ws = _new(stream, scale_shape(N, K, fmt), scale_dtype(fmt), dev)
     return wq, ws
 
 
@@ -375,7 +399,7 @@ def svdq_quantize_weight(r_t, fmt, wq=None, ws=None, stream=None):
     import torch
     _need(r_t, torch.float32, None, "r_t")
     N, K = r_t.shape
-    wq, ws = _outputs_weight(N, K, fmt, r_t.device, wq, ws)
+    wq, ws = _outputs_weight(N, K, fmt, r_t.device, wq, ws, stream)
     _check("svdq_quantize_weight", lib().svdq_quantize_weight(
         _p(r_t), N, K, _fmt(fmt), _p(wq), _p(ws), _stream(stream)))
     return wq, ws
@@ -388,7 +412,7 @@ def svdq_pack_weight(codes, scales, fmt, wq=None, ws=None, stream=None):
     _need(codes, torch.int8, None, "codes")
     N, K = codes.shape
     _need(scales, torch.float16, (N, K // 64), "scales")
-    wq, ws = _outputs_weight(N, K, fmt, codes.device, wq, ws)
+    wq, ws = _outputs_weight(N, K, fmt, codes.device, wq, ws, stream)
     _check("svdq_pack_weight", lib().svdq_pack_weight(_p(codes), _p(scales), N, K, _fmt(fmt), _p(wq), _p(ws),
                                                       _stream(stream)))
     return wq, ws
@@ -397,7 +421,7 @@ def svdq_pack_weight(codes, scales, fmt, wq=None, ws=None, stream=None):
 def svdq_linear_unfused(x_hat, l1t, wq, ws, l2, bias, fmt, workspace=None, y=None, stream=None):
     """The branch as separate kernels (measurement only).  Returns y fp16 [M, N]."""
     M, N, K, r, y, workspace, wb = _layer_args(
-        x_hat, l1t, wq, ws, l2, bias, fmt, y, workspace,
+        x_hat, l1t, wq, ws, l2, bias, fmt, y, workspace, stream,
         lambda M, N, K, r: linear_unfused_workspace_bytes(M, N, K, r, fmt))
     _check("svdq_linear_unfused", lib().svdq_linear_unfused(
         _p(x_hat), _p(l1t), _p(wq), _p(ws), _p(l2), _p(bias), M, N, K, r, _fmt(fmt),
@@ -415,7 +439,7 @@ def svdq_gemm_w4a16(x, wq, ws, bias, y=None, stream=None):
     if bias is not None:
         _need(bias, torch.float16, (N,), "bias")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=x.device)
+        y = _new(stream, (M, N), torch.float16, x.device)
     else:
         _need(y, torch.float16, (M, N), "y")
     _check("svdq_gemm_w4a16", lib().svdq_gemm_w4a16(
@@ -430,7 +454,7 @@ def svdq_gelu_tanh_smooth(y, lam, out=None, stream=None):
     M, C = y.shape
     _need(lam, torch.float32, (C,), "lam")
     if out is None:
-        out = torch.empty_like(y)
+        out = _new(stream, (M, C), torch.float16, y.device)
     else:
         _need(out, torch.float16, (M, C), "out")
     _check("svdq_gelu_tanh_smooth", lib().svdq_gelu_tanh_smooth(
@@ -451,8 +475,8 @@ def svdq_quantize_down_smooth(x, lam, l1t, fmt, xq=None, xs=None, t=None, worksp
     if l1t is not None:
         _need(l1t, torch.float16, (r, K), "l1t")
     dev = x.device
-    xq, xs, t = _outputs_kernel_a(M, K, r, fmt, dev, xq, xs, t)
-    workspace, ws_bytes = _workspace_kernel_a(M, K, r, fmt, dev, workspace, no_workspace)
+    xq, xs, t = _outputs_kernel_a(M, K, r, fmt, dev, xq, xs, t, stream)
+    workspace, ws_bytes = _workspace_kernel_a(M, K, r, fmt, dev, workspace, no_workspace, stream)
     _check("svdq_quantize_down_smooth", lib().svdq_quantize_down_smooth(
         _p(x), _p(lam), _p(l1t), M, K, r, _fmt(fmt), _p(xq), _p(xs), _p(t), _p(workspace), ws_bytes,
         _stream(stream)))
@@ -466,7 +490,7 @@ def svdq_gemm_w4a4_up_gelu_smooth(xq, xs, t, wq, ws, l2, bias, lam_next, K, fmt,
         raise ValueError("lam_next is required")
     M, N, r = _check_kernel_b(xq, xs, t, wq, ws, l2, bias, K, fmt, y, lam_next)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float16, device=xq.device)
+        y = _new(stream, (M, N), torch.float16, xq.device)
     _check("svdq_gemm_w4a4_up_gelu_smooth", lib().svdq_gemm_w4a4_up_gelu_smooth(
         _p(xq), _p(xs), _p(t), _p(wq), _p(ws), _p(l2), _p(bias), _p(lam_next), M, N, K, r, _fmt(fmt), _p(y),
         _stream(stream)))
@@ -477,7 +501,7 @@ def svdq_linear_folded(x, lam_in, l1t, wq, ws, l2, bias, lam_next, fmt, workspac
     """The layer with either fold: lam_in fp32 [K] (x unsmoothed) and/or lam_next fp32 [N]
     (output fp16(gelu(Y) / lam_next)); None for a fold not taken.  Returns y fp16 [M, N]."""
     import torch
-    M, N, K, r, y, workspace, wb = _layer_args(x, l1t, wq, ws, l2, bias, fmt, y, workspace,
+    M, N, K, r, y, workspace, wb = _layer_args(x, l1t, wq, ws, l2, bias, fmt, y, workspace, stream,
                                                lambda M, N, K, r: linear_workspace_bytes(M, K, r, fmt), "x")
     if lam_in is not None:
         _need(lam_in, torch.float32, (K,), "lam_in")
@@ -520,9 +544,9 @@ def svdq_relayout(codes, scales, K, fmt, to_canonical, codes_out=None, scales_ou
     if scales_out is not None:
         _need(scales_out, scale_dtype(fmt), dst_s, "scales_out")
     if codes_out is None:
-        codes_out = torch.empty(dst_c, dtype=torch.uint8, device=codes.device)
+        codes_out = _new(stream, dst_c, torch.uint8, codes.device)
     if scales_out is None:
-        scales_out = torch.empty(dst_s, dtype=scale_dtype(fmt), device=codes.device)
+        scales_out = _new(stream, dst_s, scale_dtype(fmt), codes.device)
     _check("svdq_relayout", lib().svdq_relayout(_p(codes), _p(scales), rows, K, _fmt(fmt), 1 if to_canonical else 0,
                                                 _p(codes_out), _p(scales_out), _stream(stream)))
     return codes_out, scales_out
@@ -583,19 +607,6 @@ def _vector(t, dtypes, n, what):
     if not t.is_cuda or t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous device tensor of shape ({n},) and one of {dtypes}, "
                          f"got {tuple(t.shape)} {t.dtype}")
-
-
-def _new_on(stream, shape, dtype, device, returned=True):
-    """torch.empty from the pool of `stream`, a handle: what a call writes there must not be a block
-    that the current stream has freed and may still be using.  A returned tensor may be used and
-    freed on the current stream, so the allocator learns of that stream too."""
-    import torch
-    here = torch.cuda.current_stream(device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        t.record_stream(here)
-    return t
 
 
 def _launch(fn, args, tensors, stream):
@@ -708,13 +719,11 @@ def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none",
     else:
         room = gemm_act_residual_workspace_bytes(M, N, K, code[dtype])
         if room:
-            workspace = torch.empty(room, dtype=torch.uint8, device=x.device) if stream is None else \
-                _new_on(stream, room, torch.uint8, x.device, returned=False)
+            workspace = _new_workspace(stream, room, x.device)
     if y is not None:
         yt = _rows(y, (out_dtype,), (M, N), "y")
     else:
-        y = torch.empty((M, N), dtype=out_dtype, device=x.device) if stream is None else \
-            _new_on(stream, (M, N), out_dtype, x.device)
+        y = _new(stream, (M, N), out_dtype, x.device)
         yt = N
     _launch("svdq_gemm_act_residual",
             (x.data_ptr(), xt, _p(xs), w.data_ptr(), _p(ws), _p(bias), _p(residual), rs, M, N, K, code[dtype], act,
@@ -865,9 +874,9 @@ class SvdqLinear:
 
     The weight-side tensors -- residual codes and scales, L1^T, L2, bias -- are checked once
     here and their pointers kept (with references that keep the tensors alive); each call then
-    checks only its activations and output, reuses a workspace kept for the largest M seen, and
+    checks only its activations and output, reuses a workspace kept for each stream and its largest M, and
     makes one svdq_linear call: the same kernels and results as svdq_linear, with a fraction of
-    its per-call host work.
+    its per-call host work.  One thread at a time calls it.
     """
 
     def __init__(self, wq, ws, l1t, l2, bias, K: int, fmt):
@@ -882,17 +891,20 @@ class SvdqLinear:
         self.device = wq.device
         self._dev_index = wq.device.index if wq.device.index is not None else torch.cuda.current_device()
         self._f16 = torch.float16
-        self._ws, self._ws_bytes, self._ws_rows = None, 0, -1
+        self._kept = {}                      # of each stream's handle: (workspace, its bytes, rows it holds)
+        self._ws_bytes, self._on = 0, (0, None)
         self._fn = lib().svdq_linear
         self._raw_stream = _raw_stream_fn()
 
     def _workspace(self, M: int):
-        if M > self._ws_rows:
-            import torch
+        """The workspace of the call's stream, self._on: its handle, and the caller's `stream`."""
+        handle, stream = self._on
+        kept = self._kept.get(handle)
+        if kept is None or M > kept[2]:
             nb = max(linear_workspace_bytes(M, self.K, self.r, self.fmt), 16)
-            self._ws = torch.empty(nb, dtype=torch.uint8, device=self.device)
-            self._ws_bytes, self._ws_rows = nb, M
-        return self._ws
+            kept = self._kept[handle] = (_new_workspace(stream, nb, self.device), nb, M)
+        self._ws_bytes = kept[1]
+        return kept[0]
 
     def __call__(self, x_hat, y=None, stream=None):
         """x_hat fp16 [M, K] (smoothed) -> y fp16 [M, N] (allocated when None)."""
@@ -901,14 +913,15 @@ class SvdqLinear:
             _need(x_hat, self._f16, (x_hat.shape[0] if x_hat.dim() == 2 else -1, self.K), "x_hat")
         M = int(x_hat.shape[0])
         if y is None:
-            import torch
-            y = torch.empty((M, self.N), dtype=self._f16, device=x_hat.device)
+            y = _new(stream, (M, self.N), self._f16, x_hat.device)
         elif not (y.is_cuda and y.dtype == self._f16 and y.shape == (M, self.N) and y.is_contiguous()):
             _need(y, self._f16, (M, self.N), "y")
+        handle = self._raw_stream(self._dev_index) if stream is None else stream
+        self._on = (handle, stream)
         ws = self._workspace(M)
         l1t, wq, ws_, l2, b = self._ptrs
         st = self._fn(x_hat.data_ptr(), l1t, wq, ws_, l2, b, M, self.N, self.K, self.r, self._F, ws.data_ptr(),
-                      self._ws_bytes, y.data_ptr(), self._raw_stream(self._dev_index) if stream is None else stream)
+                      self._ws_bytes, y.data_ptr(), handle)
         if st != 0:
             raise SvdqError("svdq_linear", st)
         return y

@@ -89,3 +89,69 @@ def test_block_operators_on_the_current_stream(op, made, rec):  # noqa: F811
     BLOCK[op](None)
     assert len(made) == MADE[op] and all(t.under == "current" and not t.recorded for t in made)
     assert rec.calls[-1][1][-1] == 7
+
+
+# ------------------------------------------------------------------ the W4A4 layer and its parts
+M, K, N, R = 8, 128, 64, 16
+FMT = "int4_e2m3"
+
+
+def codes(rows, fmt=FMT):
+    return T(binding.code_shape(rows, K, fmt), torch.uint8), T(binding.scale_shape(rows, K, fmt), binding.scale_dtype(fmt))
+
+
+def half(*shape):
+    return T(shape, F16)
+
+
+def layer():
+    return half(R, K), *codes(N), half(R, N), half(N)
+
+
+LAYER = {
+    "quantize_down": (4, lambda s: binding.svdq_quantize_down(half(M, K), half(R, K), FMT, stream=s)),
+    "quantize_down_smooth": (4, lambda s: binding.svdq_quantize_down_smooth(half(M, K), T((K,), F32), half(R, K), FMT, stream=s)),
+    "gemm_up": (1, lambda s: binding.svdq_gemm_w4a4_up(*codes(M), half(M, R), *codes(N), half(R, N), None, K, FMT, stream=s)),
+    "gemm_up_gelu": (1, lambda s: binding.svdq_gemm_w4a4_up_gelu_smooth(*codes(M), half(M, R), *codes(N), half(R, N), None,
+                                                                        T((N,), F32), K, FMT, stream=s)),
+    "linear": (2, lambda s: binding.svdq_linear(half(M, K), *layer(), FMT, stream=s)),
+    "linear_unfused": (2, lambda s: binding.svdq_linear_unfused(half(M, K), *layer(), FMT, stream=s)),
+    "linear_folded": (2, lambda s: binding.svdq_linear_folded(half(M, K), None, *layer(), None, FMT, stream=s)),
+    "quantize_weight": (2, lambda s: binding.svdq_quantize_weight(T((N, K), F32), FMT, stream=s)),
+    "pack_weight": (2, lambda s: binding.svdq_pack_weight(T((N, K), I8), half(N, K // 64), FMT, stream=s)),
+    "w4a16": (1, lambda s: binding.svdq_gemm_w4a16(half(M, K), *codes(N, "int4"), None, stream=s)),
+    "gelu": (1, lambda s: binding.svdq_gelu_tanh_smooth(half(M, N), T((N,), F32), stream=s)),
+    "relayout": (2, lambda s: binding.svdq_relayout(*codes(N), K, FMT, True, stream=s)),
+}
+
+
+@pytest.fixture
+def layer_made(made, monkeypatch):
+    for f in ("linear_workspace_bytes", "linear_unfused_workspace_bytes", "quantize_down_workspace_bytes"):
+        monkeypatch.setattr(binding, f, lambda *a: 4096)
+    return made
+
+
+@pytest.mark.parametrize("op", LAYER)
+def test_layer_allocates_on_the_launch_stream(op, layer_made, rec):  # noqa: F811
+    count, call = LAYER[op]
+    out = call(SIDE)
+    assert len(layer_made) == count and all(t.under == SIDE for t in layer_made)
+    assert rec.calls[-1][1][-1] == SIDE
+    assert all(t.recorded == ["current"] for t in (out if isinstance(out, tuple) else (out,)))
+
+
+def test_prepared_layer_keeps_a_workspace_for_each_stream(layer_made, rec):  # noqa: F811
+    """Calls on two streams may run at once: they share no workspace, and each is of its stream's pool."""
+    l1t, wq, ws, l2, bias = layer()
+    net = binding.SvdqLinear(wq, ws, l1t, l2, bias, K, FMT)
+    net._raw_stream = lambda dev: 7
+    net(half(M, K))
+    assert [t.under for t in layer_made] == ["current"] * 2
+    net(half(M, K), stream=SIDE)
+    assert [t.under for t in layer_made[2:]] == [SIDE] * 2
+    net(half(M, K), y=half(M, N), stream=SIDE)
+    net(half(M, K), y=half(M, N))
+    assert len(layer_made) == 4              # both kept
+    net(half(2 * M, K), y=half(2 * M, N), stream=SIDE)
+    assert [t.under for t in layer_made[4:]] == [SIDE]
