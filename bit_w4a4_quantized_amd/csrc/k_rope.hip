@@ -8,25 +8,31 @@
 // with respect to u.  HBM bounds it: every value is read once and written once; cosines and sines
 // are computed once per wave, each by one lane, and shared through LDS by the token's heads.
 //
-// The angle is the exact product: its fp32 rounding alone is 2^-25 of the angle, 1e-3 radians at
-// position 32768.  The product and its rounding error (one fma) are reduced to (-pi/4, pi/4]
-// before sine and cosine.
+// The angle is the product in fp64: exact for fp32 positions and frequencies (an fp32 product is
+// off by 1e-3 radians at position 32768), rounded to 2^-53 for int32 positions past 2^29.
 #include "block_ops.h"
 
 namespace svdq {
 
 namespace {
 
-// cos and sin of p f: q + e is the exact product, and k quarter turns are taken off q in three
-// steps, pi/2 being 201/128 (both that multiple and q are multiples of a power of two that the
-// difference still holds exactly), the fp32 rest and the rest's own error.  Taylor polynomials
-// on a quarter turn: the next terms are below 2^-25.
-__device__ __forceinline__ void cos_sin(float p, float f, float* c, float* s) {
-  const float q = p * f, e = __builtin_fmaf(p, f, -q);
-  const float k = __builtin_rintf(q * 0.6366197723675814f);
-  float r = __builtin_fmaf(-k, 1.5703125f, q);
-  r = __builtin_fmaf(-k, 0.00048382679233327508f, r);
-  r = __builtin_fmaf(-k, 2.563344e-12f, r) + e;
+// Angles are reduced up to this size; larger ones are taken as it (int32 positions reach it only
+// with frequencies past 2^17).
+constexpr double kMaxAngle = 0x1p48;
+
+// cos and sin of p f.  k quarter turns are taken off the angle, one fma each with pi/2 in two fp64
+// parts: the remainder is good to 2^-52, and the quotient's rounding leaves it within 0.03 of
+// (-pi/4, pi/4] at 2^48 and closer below.  Taylor polynomials there: the next terms are below
+// 2^-24.  The fp64 operations hide behind the loads (4608 tokens of 24 + 24 heads of 128 21.3 us, an
+// fp32 reduction good up to 2^20 21.2; one token 4.2 and 4.1).
+__device__ __forceinline__ void cos_sin(double p, float f, float* c, float* s) {
+  double q = p * (double)f;
+  if (__builtin_fabs(q) > kMaxAngle) q = __builtin_copysign(kMaxAngle, q);
+  const double k = __builtin_rint(q * 0.63661977236758134);
+  double rem = __builtin_fma(-k, 1.5707963267948966, q);
+  rem = __builtin_fma(-k, 6.123233995736766e-17, rem);
+  const float r = (float)rem;
+  const int n = (int)(k - 4.0 * __builtin_floor(0.25 * k));     // k modulo 4
   const float z = r * r;
   float sn = __builtin_fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
   sn = __builtin_fmaf(z, sn, 1.f / 120.f);
@@ -36,7 +42,6 @@ __device__ __forceinline__ void cos_sin(float p, float f, float* c, float* s) {
   cs = __builtin_fmaf(z, cs, 1.f / 24.f);
   cs = __builtin_fmaf(z, cs, -0.5f);
   cs = __builtin_fmaf(z, cs, 1.f);
-  const int n = __float2int_rn(k);
   const float a = n & 1 ? sn : cs, b = n & 1 ? cs : sn;
   *c = (n + 1) & 2 ? -a : a;
   *s = n & 2 ? -b : b;
@@ -63,8 +68,8 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
 
 __device__ __forceinline__ void pair_cos_sin(const RopeArgs& a, int64_t pos, int p, float* c, float* s) {
   const int ax = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);   // ends of absent axes are never reached
-  const float at = a.pos_float ? static_cast<const float*>(a.positions)[pos + ax]
-                               : (float)static_cast<const int*>(a.positions)[pos + ax];
+  const double at = a.pos_float ? (double)static_cast<const float*>(a.positions)[pos + ax]
+                                : (double)static_cast<const int*>(a.positions)[pos + ax];
   cos_sin(at, a.inv_freq[p], c, s);
   if (a.inverse) *s = -*s;
 }

@@ -458,7 +458,8 @@ size_t svdq_gemm_act_residual_workspace_bytes(int M, int N, int K, svdq_type typ
  *   by axis a, P = sum of axis_pairs; the values from 2 P on are u unturned.
  *   inverse != 0 turns by -angle: the inverse map, and the gradient of the output with respect
  *   to x; it takes no weights.
- * The product of position and frequency is carried to about 48 bits into the sine and cosine.
+ * The product of position and frequency is taken in fp64 (exact for fp32 positions) up to a size of
+ * 2^48; a larger or infinite angle counts as 2^48 with its sign.
  */
 typedef struct {
   const void* in;        /* [batch, tokens, heads, dim], strides below, innermost contiguous */

@@ -7,6 +7,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from bit_w4a4_quantized_amd import binding  # noqa: E402
+from test_gpu_block import SMALL, U, check, rope64  # noqa: E402
 
 F16, BF16, F32, F64 = torch.float16, torch.bfloat16, torch.float32, torch.float64
 E4M3 = torch.float8_e4m3fn
@@ -75,3 +76,61 @@ def test_calls_on_another_stream():
         assert not freed & {t.data_ptr() for t in got}
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# ------------------------------------------------------------------ rotary positions
+def rope_both(q, pos, freq, axis_pairs, pairs="adjacent", inverse=False, **kw):
+    """The operator on q as it is and on a copy one element off 16-byte alignment, which takes the
+    element-wise kernel; both in the operator's layout, on the CPU."""
+    buf = torch.zeros(q.numel() + 1, dtype=q.dtype, device="cuda")
+    off = buf[1:].view(q.shape)
+    off.copy_(q)
+    return [binding.svdq_rope_axes(v, None, pos.cuda(), freq.cuda(), axis_pairs, pairs, inverse=inverse, **kw)[0].cpu()
+            for v in (q.cuda(), off)]
+
+
+def check_turned(q, pos, freq, axis_pairs, pairs):
+    want, size = rope64(q, None, pos, freq, axis_pairs, pairs, 1e-6, False)
+    # cosine and sine within 2^-21, two products and their difference, one rounding
+    tol = U[q.dtype] * 1.001 * want.abs() + 2.0 ** -20 * size + SMALL[q.dtype]
+    for y in rope_both(q, pos, freq, axis_pairs, pairs):
+        check(y, want, tol, f"positions up to {float(pos.abs().max()):.3g}")
+
+
+@pytest.mark.parametrize("pairs", ["adjacent", "halves"])
+@pytest.mark.parametrize("octave", list(range(18, 31)))
+def test_rope_every_int_position(octave, pairs):
+    """Positions of every size an int32 holds, both signs, with frequencies of one and below."""
+    g = gen(octave)
+    pos = torch.randint(1 << octave, (1 << (octave + 1)) - 1, (257, 1), generator=g, dtype=torch.int64)
+    pos[0], pos[1] = 1 << octave, (1 << (octave + 1)) - 1
+    pos[2::2] *= -1
+    freq = torch.cat([torch.ones(1), torch.rand(31, generator=g)])
+    check_turned(torch.randn(257, 2, 64, generator=g).to(F16), pos.to(torch.int32), freq, (32,), pairs)
+
+
+@pytest.mark.parametrize("exponent", [20, 30, 36, 42, 47])
+def test_rope_large_fp32_angles(exponent):
+    g = gen(exponent)
+    pos = (torch.rand(64, 1, generator=g) + 1) * 2.0 ** (exponent // 2) * (torch.randint(0, 2, (64, 1), generator=g) * 2 - 1)
+    freq = (torch.rand(32, generator=g) + 1) * 2.0 ** ((exponent - 1) // 2)
+    check_turned(torch.randn(64, 2, 64, generator=g).to(F16), pos, freq, (32,), "adjacent")
+
+
+def test_rope_angles_past_the_limit():
+    """Angles past 2^48, infinite ones too, are taken as 2^48 with their sign; NaN shows in its pair alone."""
+    limit, q = 2.0 ** 48, torch.zeros(8, 1, 16, dtype=F16)
+    q[..., 0::2] = 1                         # pairs (1, 0) become (cos, sin)
+    values = [limit, limit * 1.5, 1e30, float("inf"), -limit, -1e30, float("-inf"), float("nan")]
+    pos = torch.tensor([[v] for v in values])
+    freq = torch.tensor([1.0] + [0.0] * 7)
+    pos2 = torch.where(torch.isfinite(pos), pos, torch.zeros(()))      # 0 times an infinity is NaN too
+    for y in rope_both(q, torch.cat([pos, pos2], -1), freq, (1, 7)):
+        assert bool((y[:, 0, 2::2] == 1).all()) and bool((y[:, 0, 3::2] == 0).all())
+        turned = y[:, 0, :2].double()
+        want = torch.tensor([torch.cos(torch.tensor(limit, dtype=F64)), torch.sin(torch.tensor(limit, dtype=F64))])
+        assert float((turned[0] - want).abs().max()) < 2.0 ** -11
+        assert all(torch.equal(turned[i], turned[0]) for i in (1, 2, 3))
+        for i in (4, 5, 6):
+            assert float(turned[i, 0]) == float(turned[0, 0]) and float(turned[i, 1]) == -float(turned[0, 1])
+        assert bool(torch.isnan(turned[7]).all())
