@@ -88,7 +88,11 @@ struct Splits {
   uint32_t share;                            // of the second operand's workgroups among all, times 2^32, rounded up
 };
 
-template <bool BF, bool HALVES, int U>
+// Pairs of neighbours over the whole head or behind which values stay unturned, or half apart (whole
+// heads).  A form of its own for the second costs the others nothing (5 registers and 1% if tested in one).
+enum Form { ADJACENT, PARTIAL, HALVES };
+
+template <bool BF, Form FORM, int U>
 __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) {
   __shared__ __attribute__((aligned(16))) float table[4][2][512];   // cosines and sines of each wave's tokens
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) 
       if (in1) raw[i][1] = *reinterpret_cast<const uint4*>(p + (j + half) * 8);
     }
   }
-  // pairs past the turned ones get the identity
+  // pairs past the turned ones get the identity (not used: below)
   for (int i = lane; i < nt * pairs; i += 64) {
     const int tl_ = w_.tw > 1 ? i / pairs : 0, p = i - tl_ * pairs;
     int b = b0, t = t0 + tl_;
@@ -162,7 +166,7 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) 
     // the lane's eight pairs: of its two pieces (adjacent), or between them (half apart)
 #pragma unroll
     for (int v = 0; v < 2; v++) {
-      const int p = tl[i] * pairs + min(HALVES ? j * 8 + v * 4 : (j + v * half) * 4, pairs - 4);
+      const int p = tl[i] * pairs + min(FORM == HALVES ? j * 8 + v * 4 : (j + v * half) * 4, pairs - 4);
       *reinterpret_cast<float4*>(c + 4 * v) = *reinterpret_cast<const float4*>(&table[wave][0][p]);
       *reinterpret_cast<float4*>(s + 4 * v) = *reinterpret_cast<const float4*>(&table[wave][1][p]);
     }
@@ -176,7 +180,7 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) 
 #pragma unroll
         for (int e = 0; e < 8; e++) u[v][e] = u[v][e] * rstd * w[v][e];
     }
-    if (HALVES) {
+    if (FORM == HALVES) {
 #pragma unroll
       for (int e = 0; e < 8; e++) {
         y[0][e] = u[0][e] * c[e] - u[1][e] * s[e];
@@ -191,6 +195,14 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) 
           y[v][2 * e] = u[v][2 * e] * cc - u[v][2 * e + 1] * sn;
           y[v][2 * e + 1] = u[v][2 * e] * sn + u[v][2 * e + 1] * cc;
         }
+    }
+    // values behind the pairs as they are: turned by the identity, an infinity or NaN would reach its neighbour
+    if (FORM == PARTIAL) {
+#pragma unroll
+      for (int v = 0; v < 2; v++)
+#pragma unroll
+        for (int e = 0; e < 8; e++)
+          if ((j + v * half) * 4 + e / 2 >= a.pairs) y[v][e] = u[v][e];
     }
     if (out[i]) {
       if (in0) stream16(out[i] + j * 8, pack8(y[0], BF));
@@ -290,10 +302,12 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
   if (!launchable(all, 256)) return hipErrorInvalidConfiguration;
   sp.share = (uint32_t)((((uint64_t)blocks[1] << 32) + all - 1) / all);
   const bool bf = a.type == T_BF16;
-  const auto two = a.halves ? (bf ? k_rope<true, true, 2> : k_rope<false, true, 2>)
-                            : (bf ? k_rope<true, false, 2> : k_rope<false, false, 2>);
-  const auto three = a.halves ? (bf ? k_rope<true, true, 3> : k_rope<false, true, 3>)
-                              : (bf ? k_rope<true, false, 3> : k_rope<false, false, 3>);
+  const auto two = a.halves            ? (bf ? k_rope<true, HALVES, 2> : k_rope<false, HALVES, 2>)
+                   : 2 * a.pairs < a.dim ? (bf ? k_rope<true, PARTIAL, 2> : k_rope<false, PARTIAL, 2>)
+                                         : (bf ? k_rope<true, ADJACENT, 2> : k_rope<false, ADJACENT, 2>);
+  const auto three = a.halves            ? (bf ? k_rope<true, HALVES, 3> : k_rope<false, HALVES, 3>)
+                     : 2 * a.pairs < a.dim ? (bf ? k_rope<true, PARTIAL, 3> : k_rope<false, PARTIAL, 3>)
+                                           : (bf ? k_rope<true, ADJACENT, 3> : k_rope<false, ADJACENT, 3>);
   hipLaunchKernelGGL(U == 2 ? two : three, dim3(all), dim3(256), 0, s, a, lanes, sp);
   return hipGetLastError();
 }

@@ -134,3 +134,24 @@ def test_rope_angles_past_the_limit():
         for i in (4, 5, 6):
             assert float(turned[i, 0]) == float(turned[0, 0]) and float(turned[i, 1]) == -float(turned[0, 1])
         assert bool(torch.isnan(turned[7]).all())
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("pairs", ["adjacent", "halves"])
+@pytest.mark.parametrize("D,axis_pairs", [(128, (8, 24)), (64, (5,)), (72, (3, 4, 8)), (256, (60, 60)), (16, (1,))])
+def test_rope_values_behind_the_pairs(D, axis_pairs, pairs, dtype):
+    """Infinities, NaN and negative zeros behind the turned values stay where they are, bit for bit,
+    and reach no neighbour; so do all other values there."""
+    g, P = gen(D), sum(axis_pairs)
+    q = torch.randn(130, 3, D, generator=g).to(dtype)
+    pos = torch.randint(0, 5000, (130, len(axis_pairs)), generator=g, dtype=torch.int32)
+    freq = torch.rand(P, generator=g)
+    clean = rope_both(q, pos, freq, axis_pairs, pairs)
+    odd = torch.tensor([float("inf"), float("nan"), -0.0, float("-inf"), 0.0, 1.0]).to(dtype)
+    pick = torch.randint(0, len(odd), q[..., 2 * P:].shape, generator=g)
+    q[..., 2 * P:] = odd[pick]
+    for y, c in zip(rope_both(q, pos, freq, axis_pairs, pairs), clean):
+        assert torch.equal(y[..., :2 * P], c[..., :2 * P])
+        nan = torch.isnan(q[..., 2 * P:])
+        assert torch.equal(torch.isnan(y[..., 2 * P:]), nan)
+        assert torch.equal(y[..., 2 * P:][~nan].view(torch.int16), q[..., 2 * P:][~nan].view(torch.int16))
