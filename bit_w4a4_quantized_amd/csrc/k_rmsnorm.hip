@@ -31,22 +31,38 @@ __device__ __forceinline__ float wave_max(float v) {
 }
 
 // Sum of squares and maximum over the row's wpr waves, `first` being the first of them in the block.
-__device__ __forceinline__ void row_reduce(float& ss, float& mx, int wpr, int first, float (*red)[16]) {
+// Returns whether the sum of any of the block's rows is not finite (one row a wave: of the wave's).
+__device__ __forceinline__ bool row_reduce(float& ss, float& mx, int wpr, int first, float (*red)[16]) {
   ss = wave_sum(ss);
   mx = wave_max(mx);
-  if (wpr > 1) {
-    if ((threadIdx.x & 63) == 0) {
-      red[0][threadIdx.x >> 6] = ss;
-      red[1][threadIdx.x >> 6] = mx;
-    }
-    __syncthreads();
-    ss = 0.f;
-    mx = 0.f;
-    for (int i = first; i < first + wpr; i++) {
-      ss += red[0][i];
-      mx = fmaxf(mx, red[1][i]);
-    }
+  if (wpr == 1) return !(ss < INFINITY);
+  if ((threadIdx.x & 63) == 0) {
+    red[0][threadIdx.x >> 6] = ss;
+    red[1][threadIdx.x >> 6] = mx;
   }
+  __syncthreads();
+  ss = 0.f;
+  mx = 0.f;
+  for (int i = first; i < first + wpr; i++) {
+    ss += red[0][i];
+    mx = fmaxf(mx, red[1][i]);
+  }
+  return !((wpr == 2 ? (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]) : ss) < INFINITY);   // two rows, or one
+}
+
+// The squares of finite values from 2^64 on pass fp32's range (bf16 and fp32 hold them up to 2^128):
+// such a row's values are squared and summed once more, times 2^-80.
+constexpr float kDown = 0x1p-80f;
+// The sum over the row, for the block's rows at once.
+__device__ __forceinline__ float row_sum(float ss, int wpr, int first, float (*red)[16]) {
+  ss = wave_sum(ss);
+  if (wpr == 1) return ss;
+  __syncthreads();                           // everyone has read the first sums
+  if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = ss;
+  __syncthreads();
+  ss = 0.f;
+  for (int i = first; i < first + wpr; i++) ss += red[0][i];
+  return ss;
 }
 
 __device__ __forceinline__ uint32_t code_i8(float v) { return (uint32_t)(int)__builtin_rintf(v) & 0xFFu; }
@@ -121,6 +137,15 @@ __device__ __forceinline__ void unpack(const F8& u, float* f) {
   f[4] = u.b.x; f[5] = u.b.y; f[6] = u.b.z; f[7] = u.b.w;
 }
 
+template <bool BF, typename T>
+__device__ __forceinline__ float small_squares(const T* h, int n) {
+  float f[8], ss = 0.f;
+  unpack<BF>(load_piece(h, n), f);
+#pragma unroll
+  for (int e = 0; e < 8; e++) ss += (f[e] * kDown) * (f[e] * kDown);
+  return ss;
+}
+
 // The weighted values v of n <= 8 elements from element o of the output, as codes or 16-bit values.
 template <bool BF>
 __device__ __forceinline__ void store_out(const NormArgs& a, int64_t o, const float* v, float mul, int n) {
@@ -154,9 +179,12 @@ __device__ __forceinline__ void store_out(const NormArgs& a, int64_t o, const fl
   }
 }
 
+__device__ __forceinline__ float root(const NormArgs& a, float ss) { return 1.0f / sqrtf(ss / (float)a.K + a.eps); }
+// from the squares of values times 2^-80, next to which eps is nothing
+__device__ __forceinline__ float root_down(const NormArgs& a, float ss) { return kDown / sqrtf(ss / (float)a.K); }
+
 // The factor of the weighted values, and the row's scale.
-__device__ __forceinline__ float row_factor(const NormArgs& a, int64_t r, float ss, float mx, bool first) {
-  const float rstd = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+__device__ __forceinline__ float row_factor(const NormArgs& a, int64_t r, float rstd, float mx, bool first) {
   if (a.out_type != T_INT8 && a.out_type != T_E4M3) return rstd;
   mx = fmaxf(mx, kTiny);
   const float qmax = a.out_type == T_INT8 ? 127.f : 448.f;
@@ -248,9 +276,18 @@ __global__ void __launch_bounds__(1024) k_rmsnorm(NormArgs a, int wpr) {
       mx = fmaxf(mx, fabsf(v[p][e]));
     }
   }
-  row_reduce(ss, mx, wpr, in_block * wpr, red);
+  const bool over = row_reduce(ss, mx, wpr, in_block * wpr, red);
+  float rstd = root(a, ss);
+  if (over) {
+    float sd = 0.f;
+#pragma unroll 1
+    for (int i = lane * 8; i < a.K; i += LANES * 8)        // the lane's own pieces; the stream as just written
+      sd += RES ? small_squares<BF>(res_out + i, a.K - i) : small_squares<BF>(x + i, a.K - i);
+    sd = row_sum(sd, wpr, in_block * wpr, red);
+    if (!(ss < INFINITY)) rstd = root_down(a, sd);
+  }
   if (!live) return;
-  const float mul = row_factor(a, r, ss, mx, lane == 0);
+  const float mul = row_factor(a, r, rstd, mx, lane == 0);
 #pragma unroll
   for (int p = 0; p < V; p++) {
     const int i = (p * LANES + lane) * 8;
@@ -299,8 +336,16 @@ k_rmsnorm_long(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; e++) mx = fmaxf(mx, fabsf(v[e]));
   }
-  row_reduce(ss, mx, 16, 0, red);
-  const float mul = row_factor(a, r, ss, mx, threadIdx.x == 0);
+  float rstd;
+  if (row_reduce(ss, mx, 16, 0, red)) {
+    ss = 0.f;
+    for (int i = threadIdx.x * 8; i < a.K; i += 8192)
+      ss += RES ? small_squares<BF>(res_out + i, a.K - i) : small_squares<BF>(x + i, a.K - i);
+    rstd = root_down(a, row_sum(ss, 16, 0, red));
+  } else {
+    rstd = root(a, ss);
+  }
+  const float mul = row_factor(a, r, rstd, mx, threadIdx.x == 0);
   for (int i = threadIdx.x * 8; i < a.K; i += 8192) {
     float v[8];
     if (RES) unpack<BF>(load_piece(res_out + i, a.K - i), v);

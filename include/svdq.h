@@ -399,6 +399,7 @@ typedef enum {
  *   8-bit out_type: a = max(max_k |v|, 2^-100), code = rnd(v * (qmax / a)) with qmax 127 (INT8,
  *     ties to even) or 448 (E4M3), scale = a * rstd / qmax, so code * scale is the normed value.
  *     rstd is a factor of the whole row and cancels in the codes: they are exact functions of h.
+ *   v is an fp32 value (|h weight| below 2^128); the mean of h^2 holds for every finite h.
  *   out_type == x_type: out = rnd(v * rstd), scales unused.  With weight / lambda in place of
  *     weight this is the smoothed input of svdq_linear.
  *   x        : [M, K], x_type SVDQ_TYPE_F16 or _BF16, rows x_stride apart.

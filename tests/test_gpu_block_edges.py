@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from bit_w4a4_quantized_amd import binding  # noqa: E402
-from test_gpu_block import SMALL, U, check, rope64  # noqa: E402
+from test_gpu_block import EPS32, SMALL, U, check, norm64, norm_case, rope64  # noqa: E402
 
 F16, BF16, F32, F64 = torch.float16, torch.bfloat16, torch.float32, torch.float64
 E4M3 = torch.float8_e4m3fn
@@ -24,6 +24,32 @@ def _gpu():
 
 def gen(seed):
     return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------ norm
+@pytest.mark.parametrize("out_format", ["int8", "e4m3", "same"])
+@pytest.mark.parametrize("rt", [None, BF16, F32])
+@pytest.mark.parametrize("K", [1, 200, 1500, 2000, 5000, 12288, 30000, 40003])
+def test_norm_of_large_values(K, rt, out_format):
+    """Values whose squares, or the sum of them, pass fp32's range (from 1.8e19 on), beside ordinary
+    rows of the same workgroup: the tolerances of every other row."""
+    scale = torch.tensor([1.0, 1e18, 1e19, 1e25, 3.0, 1e33, 1e37, 0.0, 1e37])[:, None]
+    norm_case(9, K, BF16, rt, F32, out_format, 0, K, scale)
+
+
+@pytest.mark.parametrize("out_format", ["int8", "same"])
+@pytest.mark.parametrize("K", [700, 2000, 5000, 40000])
+def test_norm_of_large_values_in_place(K, out_format):
+    """The stream written over the residual: the second sum reads what was written."""
+    g = gen(K)
+    x, r = (torch.randn(7, K, generator=g) * 1e30).to(BF16), (torch.randn(7, K, generator=g) * 1e30).to(BF16)
+    want = binding.svdq_add_rmsnorm(x.cuda(), torch.ones(K).cuda(), residual=r.cuda(), out_format=out_format)
+    rc = r.cuda()
+    got = binding.svdq_add_rmsnorm(x.cuda(), torch.ones(K).cuda(), residual=rc, residual_out=rc, out_format=out_format)
+    assert all(torch.equal(a, b) for a, b in zip(want, got) if a is not None)
+    y, _, _ = norm64(x, r, torch.ones(K), 1e-6, "same", K)
+    if out_format == "same":
+        check(got[0], y, (U[BF16] * 1.001 + (K / 64 + 16) * EPS32) * y.abs() + SMALL[BF16], "out")
 
 
 # ------------------------------------------------------------------ product
