@@ -66,6 +66,17 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
+// 1 / sqrt(mean + eps) of a head from its sum of squares.  Squares of bf16 values from 2^64 on pass
+// fp32's range; they are then summed of the values times 2^-80, next to which eps is nothing.
+constexpr float kDown = 0x1p-80f;
+__device__ __forceinline__ float root(const RopeArgs& a, float ss) {
+  return __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / (float)a.dim, a.eps));
+}
+__device__ __forceinline__ float small_square(float v) { return (v * kDown) * (v * kDown); }
+__device__ __forceinline__ float root_down(const RopeArgs& a, float ss) {
+  return kDown * __builtin_amdgcn_rsqf(ss * (1.0f / (float)a.dim));
+}
+
 __device__ __forceinline__ void pair_cos_sin(const RopeArgs& a, int64_t pos, int p, float* c, float* s) {
   const int ax = (p >= a.end[0]) + (p >= a.end[1]) + (p >= a.end[2]);   // ends of absent axes are never reached
   const double at = a.pos_float ? (double)static_cast<const float*>(a.positions)[pos + ax]
@@ -174,7 +185,15 @@ __global__ void __launch_bounds__(256) k_rope(RopeArgs a, int lanes, Splits sp) 
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; e++) ss += u[0][e] * u[0][e] + u[1][e] * u[1][e];
-      const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(group_sum(ss, lanes), 1.0f / (float)a.dim, a.eps));
+      ss = group_sum(ss, lanes);
+      float rstd = root(a, ss);
+      if (BF && __any(!(ss < INFINITY))) {   // the whole wave, for the sum's lanes
+        float sd = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; e++) sd += small_square(u[0][e]) + small_square(u[1][e]);
+        sd = group_sum(sd, lanes);
+        if (!(ss < INFINITY)) rstd = root_down(a, sd);
+      }
 #pragma unroll
       for (int v = 0; v < 2; v++)
 #pragma unroll
@@ -233,7 +252,13 @@ __global__ void __launch_bounds__(256) k_rope_any(RopeArgs a, int64_t units) {
       const float v = load16(in, d, bf);
       ss += v * v;
     }
-    rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(group_sum(ss, 64), 1.0f / (float)a.dim, a.eps));
+    ss = group_sum(ss, 64);
+    rstd = root(a, ss);
+    if (!(ss < INFINITY)) {                  // the same in every lane
+      float sd = 0.f;
+      for (int d = lane; d < a.dim; d += 64) sd += small_square(load16(in, d, bf));
+      rstd = root_down(a, group_sum(sd, 64));
+    }
   }
   auto val = [&](int d) {
     const float v = load16(in, d, bf);

@@ -181,3 +181,23 @@ def test_rope_values_behind_the_pairs(D, axis_pairs, pairs, dtype):
         nan = torch.isnan(q[..., 2 * P:])
         assert torch.equal(torch.isnan(y[..., 2 * P:]), nan)
         assert torch.equal(y[..., 2 * P:][~nan].view(torch.int16), q[..., 2 * P:][~nan].view(torch.int16))
+
+
+@pytest.mark.parametrize("pairs", ["adjacent", "halves"])
+@pytest.mark.parametrize("D", [1, 8, 64, 100, 128, 256])
+def test_rope_norm_of_large_values(D, pairs):
+    """Heads whose squares pass fp32's range beside ordinary ones."""
+    if D == 1:
+        D, P = 2, 1
+    else:
+        P = D // 2
+    g = gen(D)
+    scale = torch.tensor([1.0, 1e18, 2e19, 1e25, 3.0, 1e33, 1e37])[:, None, None]
+    q = (torch.randn(7, 5, D, generator=g) * scale).to(BF16)
+    w = 1 + 0.2 * torch.randn(D, generator=g)
+    pos, freq = torch.arange(7, dtype=torch.int32)[:, None], torch.rand(P, generator=g)
+    want, size = rope64(q, w, pos, freq, (P,), pairs, 1e-6, False)
+    # the norm's sum and root, cosine and sine, one rounding
+    tol = U[BF16] * 1.001 * want.abs() + (2.0 ** -20 + (D / 8 + 8) * EPS32) * size + SMALL[BF16]
+    for y in rope_both(q, pos, freq, (P,), pairs, q_weight=w.cuda()):
+        check(y, want, tol, f"heads of {D}")
