@@ -63,6 +63,7 @@ _SIGS = {
     "svdq_gemm_act_residual": (_c_int, [_vp, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_int, _c_int, _c_int, _c_int,
                                         _c_int, _c_int, _vp, _c_i64, _vp, _c_size, _vp]),
     "svdq_gemm_act_residual_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "svdq_gemm_act_residual_kernel": (ctypes.c_char_p, [_c_int, _c_int, _c_int, _c_int, _c_size, _vp, _vp]),
     "svdq_rope_axes": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _c_i64, _vp, _c_int, _vp,
                                 _c_int, _c_float, _c_int, _vp]),
     "svdq_status_string": (ctypes.c_char_p, [_c_int]),
@@ -680,6 +681,17 @@ def svdq_add_rmsnorm(x, weight, eps=1e-6, residual=None, out_format="int8", out=
 @functools.lru_cache(maxsize=4096)
 def gemm_act_residual_workspace_bytes(M: int, N: int, K: int, type_code: int) -> int:
     return int(lib().svdq_gemm_act_residual_workspace_bytes(M, N, K, type_code))
+
+
+def gemm_act_residual_kernel(M: int, N: int, K: int, type_code: int, workspace_bytes=None):
+    """(kernel, splits, tail) that svdq_gemm_act_residual takes for these sizes, with the workspace it
+    asks for when None; see include/svdq.h."""
+    if workspace_bytes is None:
+        workspace_bytes = gemm_act_residual_workspace_bytes(M, N, K, type_code)
+    splits, tail = ctypes.c_int(0), ctypes.c_int(0)
+    name = lib().svdq_gemm_act_residual_kernel(M, N, K, type_code, workspace_bytes, ctypes.addressof(splits),
+                                               ctypes.addressof(tail))
+    return None if name is None else (name.decode(), splits.value, tail.value)
 
 
 def svdq_gemm_act_residual(x, w, xs=None, ws=None, bias=None, activation="none", residual=None, out_dtype=None,

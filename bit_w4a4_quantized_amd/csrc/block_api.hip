@@ -90,6 +90,22 @@ size_t svdq_gemm_act_residual_workspace_bytes(int M, int N, int K, svdq_type typ
   return gemm_act_plan(M, N, K, type, ~(size_t)0).bytes;
 }
 
+const char* svdq_gemm_act_residual_kernel(int M, int N, int K, svdq_type type, size_t workspace_bytes, int* splits,
+                                          int* tail) {
+  if ((!is8(type) && !is16(type)) || check_product(M, N, K, type) != SVDQ_OK || M == 0 || N == 0) return nullptr;
+  const GemmActPlan p = gemm_act_plan(M, N, K, type, workspace_bytes);
+  if (splits) *splits = p.splits;
+  if (tail) *tail = p.tail;
+  switch (p.kind) {
+    case GemmActPlan::FEW: return "few rows";
+    case GemmActPlan::T64: return "64x64";
+    case GemmActPlan::T64x128: return "64x128";
+    case GemmActPlan::T128x192: return "128x192";
+    case GemmActPlan::T128x256: return "128x256";
+    default: return "256x256";
+  }
+}
+
 svdq_status svdq_rope_axes(const svdq_rope_operand* operands, int count, int batch, int tokens, int dim,
                            svdq_type type, const void* positions, int positions_fp32, int64_t position_batch,
                            const float* inv_freq, int axes, const int* axis_pairs, int halves, float eps,

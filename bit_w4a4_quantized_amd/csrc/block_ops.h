@@ -98,11 +98,13 @@ struct GemmActArgs {
   void* part; size_t part_bytes;             // room for the sums of K's splits (may be null)
 };
 // The kernel a product takes, and the bytes its splits of K need (0: one split); with less room than
-// `part_bytes` K is split less or not at all.
+// `part_bytes` K is split less or not at all.  LARGE: the tiles taken as they are, and the parts that
+// each of the others, a last partial round, is cut into (0: there are none).
 struct GemmActPlan {
   enum Kind { FEW, T64, T64x128, T128x192, T128x256, LARGE };
   int kind, splits;
   size_t bytes;
+  int whole, tail;
 };
 GemmActPlan gemm_act_plan(int M, int N, int K, int type, size_t part_bytes);
 hipError_t launch_gemm_act(const GemmActArgs& a, hipStream_t s);

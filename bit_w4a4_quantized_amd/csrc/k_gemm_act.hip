@@ -446,13 +446,10 @@ __global__ void __launch_bounds__(512, 1) k_gemm_large(Args a, int whole, int pa
 }
 
 template <int TYPE>
-hipError_t go_large(const Args& a, hipStream_t s) {
-  const int cus = resident_workgroups() / 2;
-  const int64_t tiles = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-  const int rest = (int)(tiles % cus), whole = (int)(tiles - rest);
-  const int parts = 4 * rest <= cus ? 4 : 2 * rest <= cus ? 2 : 1;
-  if (!launchable(whole + rest * parts, 512)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(k_gemm_large<TYPE>, dim3((unsigned)(whole + rest * parts)), dim3(512), 0, s, a, whole, parts);
+hipError_t go_large(const Args& a, const GemmActPlan& p, hipStream_t s) {
+  const int64_t rest = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256) - p.whole, blocks = p.whole + rest * p.tail;
+  if (!launchable(blocks, 512)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL(k_gemm_large<TYPE>, dim3((unsigned)blocks), dim3(512), 0, s, a, p.whole, p.tail);
   return hipGetLastError();
 }
 
@@ -463,7 +460,7 @@ hipError_t launch_type(const Args& a, const GemmActPlan& p, void* part, hipStrea
     case GemmActPlan::T64x128: return go_split<TYPE, 2, 4, 1, 1, 3, 2>(a, p.splits, part, s);
     case GemmActPlan::T128x192: return go<TYPE, 4, 2, 1, 3, 3, 1>(a, 1, nullptr, s);
     case GemmActPlan::T128x256: return go<TYPE, 2, 4, 2, 2, 3, 1>(a, 1, nullptr, s);
-    case GemmActPlan::LARGE: return go_large<TYPE>(a, s);
+    case GemmActPlan::LARGE: return go_large<TYPE>(a, p, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -505,14 +502,15 @@ constexpr Costs kCosts{0.19, 0.055, 0.21, 0.25, 0.29, 0.7, 0.4, 0.15, 0.95, 0.5,
 constexpr Costs kCostsE4M3{0.2, 0.06, 0.28, 0.32, 0.46, 1.2, 0.75, 0.4, 1.57, 1.0, 0.4, 2.75, 0.65, 0.6, 1.2, 1.2, 1.6};
 
 GemmActPlan plan(int M, int N, int KB, int64_t part_bytes, const Costs& t) {
-  const double cus = resident_workgroups() / 2;
+  const int ncu = resident_workgroups() / 2;
+  const double cus = ncu;
   const double S = (KB + BK - 1) / BK;
   GemmActPlan best{};
   double least = 1e30;
   auto consider = [&](int kind, int splits, double cost, int64_t bytes) {
     if (bytes <= part_bytes && cost < least) {
       least = cost;
-      best = GemmActPlan{kind, splits, (size_t)bytes};
+      best = GemmActPlan{kind, splits, (size_t)bytes, 0, 0};
     }
   };
   if (M <= kFewRows) {
@@ -539,12 +537,19 @@ GemmActPlan plan(int M, int N, int KB, int64_t part_bytes, const Costs& t) {
   const double t2 = tiles_of(M, N, 128, 256) / cus, whole2 = floor(t2), rest2 = t2 - whole2;
   consider(GemmActPlan::T128x256, 1,
            whole2 * (t.t256 * S + 5.5) + (rest2 > 0 ? (t.t256_rest + t.t256_share * rest2) * S + 8 : 0), 0);
-  const double tl = tiles_of(M, N, 256, 256), whole = floor(tl / cus), rest = tl - whole * cus;
-  const double tail = rest == 0          ? 0
-                      : 4 * rest <= cus ? (t.quarter + t.quarter_share * rest / cus) * S + 6.5
-                      : 2 * rest <= cus ? t.half * S + 11
-                                        : (t.rest + t.share * rest / cus) * S + 14;
-  consider(GemmActPlan::LARGE, 1, whole * (t.large * S + 6) + tail, 0);
+  // 256 x 256: a last partial round is cut so that it finds all CUs
+  const int64_t tl = tiles_of(M, N, 256, 256), rounds = tl / ncu, rest = tl - rounds * ncu;
+  const int tail = rest == 0 ? 0 : 4 * rest <= ncu ? 4 : 2 * rest <= ncu ? 2 : 1;
+  const double share = (double)rest / cus;
+  const double last = tail == 0   ? 0
+                      : tail == 4 ? (t.quarter + t.quarter_share * share) * S + 6.5
+                      : tail == 2 ? t.half * S + 11
+                                  : (t.rest + t.share * share) * S + 14;
+  consider(GemmActPlan::LARGE, 1, rounds * (t.large * S + 6) + last, 0);
+  if (best.kind == GemmActPlan::LARGE) {
+    best.whole = (int)(tl - rest);
+    best.tail = tail;
+  }
   return best;
 }
 

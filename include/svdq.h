@@ -449,6 +449,14 @@ svdq_status svdq_gemm_act_residual(const void* x, int64_t x_stride, const float*
 /* Workspace bytes svdq_gemm_act_residual uses for these sizes (0: none, or a bad type or size). */
 size_t svdq_gemm_act_residual_workspace_bytes(int M, int N, int K, svdq_type type);
 
+/* The kernel that svdq_gemm_act_residual takes for these sizes with this much workspace, by its tiles:
+ * "few rows", "64x64", "64x128", "128x192", "128x256" or "256x256"; NULL for a bad type or size or
+ * an empty product.  For tests and measurements.  *splits: the parts K is split into.  *tail: with
+ * 256x256, the parts each tile of the last partial round is cut into (1, 2 or 4; 0: no such round).
+ * Either pointer may be NULL. */
+const char* svdq_gemm_act_residual_kernel(int M, int N, int K, svdq_type type, size_t workspace_bytes, int* splits,
+                                          int* tail);
+
 /*
  * Rotary positions with several axes on queries and keys, with the heads' root-mean-square norm
  * in front where a weight is given.  For each (batch, token, head) and its `dim` values x:
