@@ -605,6 +605,8 @@ def _rows(t, dtypes, shape, what):
 
 
 def _vector(t, dtypes, n, what):
+    if t is None:
+        raise ValueError(f"{what} is required")
     if not t.is_cuda or t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous device tensor of shape ({n},) and one of {dtypes}, "
                          f"got {tuple(t.shape)} {t.dtype}")
@@ -828,7 +830,7 @@ def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_we
     for name, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
         if t is not None and not (t.is_cuda and t.dtype == dtype):
             raise ValueError(f"{name} must be a {dtype} device tensor")
-    if not positions.is_cuda or positions.dtype not in (torch.int32, torch.float32) or not positions.is_contiguous():
+    if positions is None or not positions.is_cuda or positions.dtype not in (torch.int32, torch.float32) or not positions.is_contiguous():
         raise ValueError("positions must be a contiguous int32 or float32 device tensor")
     layout = lambda t: None if t is None else (t.shape, t.stride())  # noqa: E731
     axis_pairs = tuple(axis_pairs)
