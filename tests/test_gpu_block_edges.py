@@ -201,3 +201,31 @@ def test_rope_norm_of_large_values(D, pairs):
     tol = U[BF16] * 1.001 * want.abs() + (2.0 ** -20 + (D / 8 + 8) * EPS32) * size + SMALL[BF16]
     for y in rope_both(q, pos, freq, (P,), pairs, q_weight=w.cuda()):
         check(y, want, tol, f"heads of {D}")
+
+
+@pytest.mark.parametrize("M", [16, 256])
+def test_gemm_every_e4m3_code(M):
+    """All 256 codes times one, as x and as w: fp16 holds each value, subnormal ones too, and NaN stays NaN."""
+    codes = torch.arange(256, dtype=torch.int32).to(torch.uint8).view(E4M3).view(16, 16).cuda()
+    x = torch.zeros(M, 256, device="cuda").to(E4M3)
+    x[:16, :16] = codes
+    one = torch.eye(256, device="cuda").to(E4M3)
+    value = codes.to(F16)
+    got = binding.svdq_gemm_act_residual(x, one, out_dtype=F16)[:16, :16]
+    nan = torch.isnan(value)                 # in x, NaN reaches its whole row
+    assert int(nan.sum()) == 2 and bool(torch.isnan(got[nan.any(1)]).all())
+    assert torch.equal(got[~nan.any(1)], value[~nan.any(1)])
+    got = binding.svdq_gemm_act_residual(torch.eye(256, device="cuda")[:M].to(E4M3), x[:16].contiguous(), out_dtype=F16)[:16]
+    assert torch.equal(got[:, ~nan.any(1)], value[~nan.any(1)].T) and bool(torch.isnan(got[:, nan.any(1)]).all())
+
+
+@pytest.mark.parametrize("t,least,large", [(F16, -24, 10), (BF16, -133, 125), (E4M3, -9, 4)])
+@pytest.mark.parametrize("M,N,K", [(3, 64, 1040), (70, 136, 1040), (520, 1100, 528), (4030, 3931, 160)])
+def test_gemm_subnormal_operands(M, N, K, t, least, large):
+    """Whole multiples of the type's smallest value: they count in full."""
+    g = gen(M + K)
+    x, w = torch.randint(-7, 8, (M, K), generator=g), torch.randint(-3, 4, (N, K), generator=g)
+    xt, wt = (x.to(F64) * 2.0 ** least).to(t), (w.to(F64) * 2.0 ** large).to(t)
+    assert torch.equal(xt.to(F64), x.to(F64) * 2.0 ** least)
+    y = binding.svdq_gemm_act_residual(xt.cuda(), wt.cuda(), xs=torch.full((M,), 2.0 ** -(least + large)).cuda(), out_dtype=F16)
+    assert torch.equal(y, (x.to(F64).cuda() @ w.to(F64).cuda().T).to(F16))
