@@ -5,9 +5,11 @@
 // LDS-DMA: whole cache lines (64-byte row pieces fetched each line twice: 4608 x 3072 x 12288 in
 // int8 214 us, 184 with the same pieces contiguous).  A stage's fragments are read half a stage
 // ahead of their MFMAs, one LDS read and at most one load after each MFMA, so the matrix core works
-// while the LDS serves the reads; one barrier a stage.  4608 x 3072 x 12288 takes 185 us in int8
-// (1.88 PFLOP/s, the chip at 1.94 GHz under its matrix cores' load), 8192 cubed 2.36 PFLOP/s.  Piece p (16 bytes) of row r sits in slot
-// p ^ (r / 2 % 8): the reads of sixteen rows at one piece hit distinct banks.
+// while the LDS serves the reads; one barrier a stage.  4608 x 3072 x 12288 takes 179 us in int8
+// (1.95 PFLOP/s; 186 with GELU), 8192 cubed 2.27 PFLOP/s, in bf16 1.29, in E4M3 1.45.  The chip runs at
+// 1.94 GHz under this load; neither the matrix cores (busy 45%) nor, by count, the LDS (256 KB a
+// stage of a 256 x 256 tile, 2050 of its 3300 cycles at 128 bytes a cycle) are full.  Piece p (16 bytes)
+// of row r sits in slot p ^ (r / 2 % 8): the reads of sixteen rows at one piece hit distinct banks.
 //
 // The weight tile is the MFMA's row operand: lane (r32, h) gets token row r32 and columns
 // 8 q + 4 h + 0 ... 3.  The epilogue exchanges halves between the lanes of a row (two 4-column
@@ -470,27 +472,26 @@ int64_t tiles_of(int M, int N, int bm, int bn) { return (int64_t)((M + bm - 1) /
 }  // namespace
 
 // The kernel that costs least, in microseconds fitted to every kernel's time over M = 1 ... 4608,
-// N = 1024 ... 12288 and K = 1024 ... 12288 in int8 and bf16: of 202 such sizes the choice is the
-// best kernel or within 10% of it at 200, and within 17% at the others (65 x 3072 x 3072 in bf16:
-// 14.8 us, 12.7 in 64 x 128 tiles with more splits).  A stage of 128 bytes of K costs a CU its LDS-DMA
-// (0.21 us for each 64 x 64 tile it holds, 0.29 for 64 x 128) but no less than the ring's latency
-// with one tile (0.25).  With all CUs at work 128 x 192 tiles take 0.7 a stage, 128 x 256 0.95 and
-// 256 x 256 1.72 (power-bound), and less with few.  A split of K costs the sums' round trip and a
-// second launch (2.8 us on the GPU, and 3 more that its host work counts).
+// N = 1024 ... 12288 and K = 1024 ... 12288 in int8 and bf16, and for E4M3 with constants of its
+// own.  Of 114 such sizes in each of the four types the choice is the best kernel or within 9% of it,
+// except 65 x 3072 x 3072 in 16 bits (14.8 us, 12.8 in 64 x 128 tiles with more splits).  A stage of
+// 128 bytes of K costs a CU its LDS-DMA (0.21 us for each 64 x 64 tile it holds, 0.29 for 64 x 128) but
+// no less than the ring's latency with one tile (0.25).  With all CUs at work 128 x 192 tiles take
+// 0.7 a stage, 128 x 256 0.95 and 256 x 256 1.72, and less with few.  A split of K costs the sums'
+// round trip and a second launch (2.8 us on the GPU, and 3 more that its host work counts).
 //
-// Both sides, in us, int8 (M x K x N): few rows / tiles 1 x 3072 x 12288 8.9 / 10.6, 17 x 3072 x 12288
-// 9.3 / 10.7, 33 x 3072 x 12288 13.7 / 10.9, 64 x 3072 x 3072 6.7 / 8.2; 64 x 64 / 64 x 128 tiles
-// 65 x 3072 x 3072 8.8 / 10.0, 512 x 3072 x 3072 13.9 / 12.3; 64 x 128 / 128 x 192 384 x 3072 x 3072
-// 12.0 / 17.9, 512 x 3072 x 9216 26.5 / 21.0; 128 x 192 / 128 x 256 the same 21.0 / 23.0,
-// 777 x 3072 x 9216 38.5 / 28.9; 128 x 192 / 256 x 256 1536 x 3072 x 3072 21.1 / 28.2,
-// 3000 x 12288 x 3072 125 / 119; 128 x 256 / 256 x 256 777 x 3072 x 9216 28.9 / 40.3,
-// 4608 x 3072 x 12288 183 / 170; 64 x 12288 x 3072 26.5 whole, 14.5 in five splits.
+// Both sides, in us without an activation, int8 (M x K x N): few rows / tiles 1 x 3072 x 12288 9.1 / 10.6,
+// 17 x 3072 x 12288 9.3 / 10.7, 33 x 3072 x 12288 13.7 / 10.9, 64 x 3072 x 3072 6.8 / 8.1; 64 x 64 / 64 x 128
+// tiles 65 x 3072 x 3072 8.1 / 9.6, 512 x 3072 x 3072 13.5 / 11.9; 64 x 128 / 128 x 192 384 x 3072 x 3072
+// 11.7 / 17.8, 512 x 3072 x 9216 28.1 / 22.6; 128 x 192 / 128 x 256 the same 22.6 / 25.3,
+// 777 x 3072 x 9216 41.3 / 30.6; 128 x 192 / 256 x 256 1536 x 3072 x 3072 22.8 / 29.7,
+// 3000 x 12288 x 3072 130 / 128; 128 x 256 / 256 x 256 777 x 3072 x 9216 30.6 / 42.0,
+// 4608 x 3072 x 12288 194 / 179; 64 x 12288 x 3072 in 64 x 64 tiles 26.5 whole, 14.8 in five splits.
 //
-// E4M3 has its own constants: its products take the time of 16-bit ones (twice an 8-bit stage's
-// MFMAs) and the conversion to fp16 comes on top, so that the matrix cores and the vector units
-// bound the stages that LDS-DMA bounds in the other types.  Of 114 sizes the choice is the best
-// kernel or within 9% of it.  With the other types' constants 777 x 12288 x 3072 took 93 us in
-// 128 x 192 tiles (64 x 64: 74) and 384 x 6144 x 6144 51 (39).
+// E4M3: its products take the time of 16-bit ones (twice an 8-bit stage's MFMAs) and the conversion
+// to fp16 comes on top, so that the matrix cores and the vector units bound the stages that LDS-DMA
+// bounds in the other types.  With the others' constants 777 x 12288 x 3072 took 93 us in 128 x 192
+// tiles (64 x 64: 74) and 384 x 6144 x 6144 51 (39).
 struct Costs {
   double few, few_rows;                      // few rows: a turn of K, and more for each 16 rows
   double t64, t64_one, t64x128;              // a stage, 64 x 64 tiles with several and one a CU; 64 x 128

@@ -12,9 +12,10 @@
 //
 // The rings are short, so that two or three workgroups share a CU: with R = 4 and one or two of
 // them 16 x 3072 x 12288 (M x K x N) in int8 took 11.4 us, 9.2 with R = 3; 64 rows 20.9, 14.5 with R = 2.
-// 1 x 12288 x 3072 takes 9.1 us in int8 (13.3 in split 64 x 64 tiles) and 13.9 in bf16, 1 x 3072 x 12288
-// 8.9 and 13.8 (tiles 10.7 and 16.2): 4.1 ... 5.5 TB/s of weight.  With 33 rows and more the token
-// rows' traffic (each workgroup reads them all) passes the weight's, and wide products go to tiles.
+// 1 x 12288 x 3072 takes 9.1 us in int8 (13.3 in split 64 x 64 tiles), 9.6 in E4M3 with its conversion to
+// fp16 and 13.9 in bf16; 1 x 3072 x 12288 8.9, 9.1 and 13.8 (tiles 10.7, 12.0 and 16.2): 4.1 ... 5.5
+// TB/s of weight.  With 33 rows and more the token rows' traffic (each workgroup reads them all)
+// passes the weight's, and wide products go to tiles.
 #include "gemm_act.h"
 
 namespace svdq {
