@@ -36,6 +36,21 @@ class RopeOperand(ctypes.Structure):
 
 _RopeOperands = RopeOperand * 2
 
+
+class CacheStruct(ctypes.Structure):
+    """svdq_paged_cache."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scales", _vp), ("v_scales", _vp), ("type", _c_int), ("pages", _c_i64),
+                ("page_size", _c_int), ("heads", _c_int), ("dim", _c_int), ("page_stride", _c_i64),
+                ("token_stride", _c_i64), ("head_stride", _c_i64), ("scale_page_stride", _c_i64),
+                ("scale_token_stride", _c_i64), ("scale_head_stride", _c_i64)]
+
+
+class BatchStruct(ctypes.Structure):
+    """svdq_paged_batch."""
+    _fields_ = [("page_table", _vp), ("table_stride", _c_i64), ("table_width", _c_int), ("starts", _vp), ("context", _vp),
+                ("sequences", _c_int)]
+
+
 _SIGS = {
     "svdq_code_row_bytes": (_c_size, [_c_int, _c_int]),
     "svdq_scale_row_bytes": (_c_size, [_c_int, _c_int]),
@@ -66,6 +81,12 @@ _SIGS = {
     "svdq_gemm_act_residual_kernel": (ctypes.c_char_p, [_c_int, _c_int, _c_int, _c_int, _c_size, _vp, _vp]),
     "svdq_rope_axes": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int, _c_i64, _vp, _c_int, _vp,
                                 _c_int, _c_float, _c_int, _vp]),
+    "svdq_rope_append": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _vp, _c_int, _vp, _c_int, _vp,
+                                  _c_int, _c_float, _vp]),
+    "svdq_tree_attention": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp, _c_i64, _c_int,
+                                     _vp, _c_i64, _c_i64, _vp, _c_size, _vp]),
+    "svdq_tree_attention_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "svdq_cache_keep": (_c_int, [_vp, _vp, _vp, _c_i64, _c_int, _vp]),
     "svdq_status_string": (ctypes.c_char_p, [_c_int]),
     "svdq_version": (ctypes.c_char_p, []),
 }
@@ -858,6 +879,275 @@ def svdq_rope_axes(q, k, positions, inv_freq, axis_pairs, pairs="adjacent", q_we
              1 if pairs == "halves" else 0, eps, 1 if inverse else 0),
             given, stream)
     return q_out, k_out
+
+
+# ------------------------------------------------------------------ a paged cache of keys and values
+def _apart(shape, stride, what):
+    """The strides of a tensor's dimensions, 0 for those of one element or none; ValueError where elements share
+    memory."""
+    step = tuple(0 if n <= 1 else s for n, s in zip(shape, stride))
+    reach = 1
+    for s, n in sorted((s, n) for s, n in zip(step, shape) if n > 1):
+        if s < reach:
+            raise ValueError(f"{what} must not overlap itself")
+        reach = s * (n - 1) + reach
+    return step
+
+
+class PagedCache:
+    """The pages of a cache, checked once: keys k and values v [pages, page_size, heads, dim] of one type (fp16 or
+    bf16, or int8 or float8_e4m3fn codes) and one layout (any strides, multiples of 16 bytes, with contiguous
+    heads; e.g. a transposed view of pages that keep heads first), and for codes the fp32 scales [pages,
+    page_size, heads] of both, a head's value being code * scale.  page_size: a power of two; dim: a multiple of
+    8 (of 16 for codes) up to 256.  The operators read and write the tensors in place; the handle keeps
+    references to them.  A captured graph holds the tensors' addresses, not this object's."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        d = _dtypes or _d()
+        for name, t in (("k", k), ("v", v)):
+            if t is None:
+                raise ValueError(f"{name} is required")
+            if not t.is_cuda or t.dtype not in d.operand:
+                raise ValueError(f"{name} must be a device tensor and one of {d.operand}, got {t.dtype}")
+            if t.dim() != 4:
+                raise ValueError(f"{name} must have shape [pages, page_size, heads, dim], got {tuple(t.shape)}")
+        if v.dtype != k.dtype or v.shape != k.shape:
+            raise ValueError(f"v must have k's type and shape, got {v.dtype} {tuple(v.shape)}")
+        pages, size, heads, dim = k.shape
+        if size < 1 or size & (size - 1) or size > 1 << 16:
+            raise ValueError(f"page_size must be a power of two up to {1 << 16}, got {size}")
+        each = 8 if k.dtype in d.half else 16
+        if not 8 <= dim <= 256 or dim % each or heads < 1:
+            raise ValueError(f"a head of {k.dtype} must have a multiple of {each} values up to 256, got {dim} ({heads} heads)")
+        steps = [_apart(t.shape, t.stride(), name) for name, t in (("k", k), ("v", v))]
+        if any(t.stride()[3] != 1 for t in (k, v)):
+            raise ValueError("the heads of k and v must be contiguous")
+        if steps[0] != steps[1]:
+            raise ValueError(f"k and v must have the same strides, got {k.stride()} and {v.stride()}")
+        if any(s % each for s in steps[0][:3]) or k.data_ptr() % 16 or v.data_ptr() % 16:
+            raise ValueError("the strides and addresses of k and v must be multiples of 16 bytes")
+        scale_step = (0, 0, 0)
+        if k.dtype in d.half:
+            _absent(k_scales, "k_scales", "for a 16-bit cache")
+            _absent(v_scales, "v_scales", "for a 16-bit cache")
+        else:
+            for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+                if t is None:
+                    raise ValueError(f"{name} is required for a cache of codes")
+                if not t.is_cuda or t.dtype != d.torch.float32 or t.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must be a float32 device tensor of shape {tuple(k.shape[:3])}")
+            scale_steps = [_apart(t.shape, t.stride(), name) for name, t in (("k_scales", k_scales), ("v_scales", v_scales))]
+            if scale_steps[0] != scale_steps[1]:
+                raise ValueError("k_scales and v_scales must have the same strides")
+            scale_step = scale_steps[0]
+        for t in (v, k_scales, v_scales):
+            if t is not None and t.get_device() != k.get_device():
+                raise ValueError("all tensors of a cache must be on one device")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.pages, self.page_size, self.heads, self.dim, self.dtype = pages, size, heads, dim, k.dtype
+        self.step_types = (k.dtype,) if k.dtype in d.half else d.half
+        self._struct = CacheStruct(k.data_ptr(), v.data_ptr(), _p(k_scales), _p(v_scales), d.code[k.dtype], pages, size,
+                                   heads, dim, *steps[0][:3], *scale_step)
+        self._at = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, pages, page_size, heads, dim, dtype, device="cuda"):
+        """A cache of new pages, zeroed (what attention does not see may hold anything)."""
+        import torch
+        shape = (pages, page_size, heads, dim)
+        new = lambda: torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) if dtype.itemsize == 1 else \
+            torch.zeros(shape, dtype=dtype, device=device)  # noqa: E731
+        scale = lambda: torch.zeros(shape[:3], device=device) if dtype.itemsize == 1 else None  # noqa: E731
+        return cls(new(), new(), scale(), scale())
+
+
+class PagedBatch:
+    """A step's sequences, checked once and shared by the step's layers: page_table int32 [sequences, width] (slot s
+    of a sequence is token s % page_size of page page_table[s // page_size]; an entry that is no page, e.g. -1, holds
+    nothing), starts int32 [sequences + 1] (sequence b has the step's tokens starts[b] ... starts[b + 1] - 1) and
+    context int32 [sequences] (tokens in the cache before the step).  The handle keeps references to the tensors;
+    their contents may change between calls."""
+
+    def __init__(self, page_table, starts, context):
+        d = _dtypes or _d()
+        i32 = (d.torch.int32,)
+        step = _rows(page_table, i32, None, "page_table")
+        n, width = page_table.shape
+        _vector(starts, i32, n + 1, "starts")
+        _vector(context, i32, n, "context")
+        for t in (starts, context):
+            if t.get_device() != page_table.get_device():
+                raise ValueError("all tensors of a batch must be on one device")
+        self.page_table, self.starts, self.context, self.sequences, self.width = page_table, starts, context, n, width
+        self._struct = BatchStruct(page_table.data_ptr(), step, width, starts.data_ptr(), context.data_ptr(), n)
+        self._at = ctypes.addressof(self._struct)
+
+
+def _paged(cache, batch):
+    if not isinstance(cache, PagedCache) or not isinstance(batch, PagedBatch):
+        raise ValueError("cache must be a PagedCache and batch a PagedBatch")
+
+
+@functools.lru_cache(maxsize=1024)
+def _append_plan(q, k, v, q_out, positions, axis_pairs, heads, dim):
+    """What svdq_rope_append checks and works out from sizes alone: operands as (shape, strides), q None for none.
+    Returns the operands without their pointers, tokens, P, the axes' array and the strides of v."""
+    ops = _RopeOperands()
+    tokens = k[0][0] if len(k[0]) == 3 else -1
+    for name, x in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
+        if x is None:
+            continue
+        shape, step = x
+        want = (tokens, heads, dim) if name in "kv" else None
+        if len(shape) != 3 or (want and tuple(shape) != want) or shape[0] != tokens or shape[2] != dim:
+            raise ValueError(f"{name} must have shape [tokens, {heads if want else 'heads'}, {dim}], got {tuple(shape)}")
+        if step[2] != 1:
+            raise ValueError(f"{name}'s heads must be contiguous")
+    if q is not None:
+        if q[0][1] < 1:
+            raise ValueError("q must have a head")
+        out = q_out or (q[0], (q[0][1] * dim, dim, 1))
+        if tuple(out[0]) != tuple(q[0]):
+            raise ValueError(f"q_out must have q's shape, got {tuple(out[0])}")
+        _apart(out[0], out[1], "q_out")
+        ops[0] = RopeOperand(0, 0, 0, q[0][1], 0, *q[1][:2], 0, *out[1][:2])
+    ops[1] = RopeOperand(0, 0, 0, heads, 0, *k[1][:2], 0, 0, 0)
+    axes = len(axis_pairs)
+    if tuple(positions) != (tokens, axes):
+        raise ValueError(f"positions must have shape ({tokens}, {axes}), got {tuple(positions)}")
+    return bytes(ops), tokens, sum(axis_pairs), (_c_int * axes)(*axis_pairs), v[1][:2]
+
+
+_OPERAND_BYTES = ctypes.sizeof(RopeOperand)
+
+
+def svdq_rope_append(cache, batch, q, k, v, positions, inv_freq, axis_pairs, pairs="adjacent", q_weight=None,
+                     k_weight=None, eps=1e-6, q_out=None, stream=None):
+    """A step's tokens into a paged cache, with the rotary positions of svdq_rope_axes on queries and keys.  q
+    [tokens, heads, dim] (None for no queries), k and v [tokens, cache heads, dim], fp16 or bf16 (a 16-bit cache's
+    own type); any strides with contiguous heads.  positions [tokens, axes] int32 or fp32; inv_freq fp32 [P],
+    axis_pairs, pairs, q_weight, k_weight and eps as for svdq_rope_axes.  Keys and values go to the slots behind
+    their sequence's context, quantized for a cache of codes (a scale per token and head).  Returns the turned
+    queries [tokens, heads, dim] (q_out, which may be q)."""
+    d = _dtypes or _d()
+    torch = d.torch
+    _paged(cache, batch)
+    if k is None or v is None:
+        raise ValueError("k and v are required")
+    dtype = k.dtype
+    if dtype not in cache.step_types:
+        raise ValueError(f"k must be one of {cache.step_types} for a cache of {cache.dtype}, got {dtype}")
+    if q is None:
+        _absent(q_weight, "q_weight", "without q")
+        _absent(q_out, "q_out", "without q")
+    for name, t in (("k", k), ("v", v), ("q", q), ("q_out", q_out)):
+        if t is not None and not (t.is_cuda and t.dtype == dtype):
+            raise ValueError(f"{name} must be a {dtype} device tensor")
+    if pairs not in ("adjacent", "halves"):
+        raise ValueError(f"pairs must be 'adjacent' or 'halves', got {pairs!r}")
+    if positions is None or not positions.is_cuda or positions.dtype not in (torch.int32, torch.float32) or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 or float32 device tensor")
+    axis_pairs = tuple(axis_pairs)
+    blank, tokens, P, axes, v_step = _append_plan(
+        None if q is None else (q.shape, q.stride()), (k.shape, k.stride()), (v.shape, v.stride()),
+        None if q_out is None else (q_out.shape, q_out.stride()), positions.shape, axis_pairs, cache.heads, cache.dim)
+    _vector(inv_freq, d.f32, P, "inv_freq")
+    ops = _RopeOperands.from_buffer_copy(blank)
+    given = (cache.k, batch.page_table, k, v, q, positions, inv_freq, q_weight, k_weight, q_out)
+    ops[1].inp = k.data_ptr()
+    if k_weight is not None:
+        _vector(k_weight, d.f32, cache.dim, "k_weight")
+        ops[1].weight = k_weight.data_ptr()
+    at = ctypes.addressof(ops)
+    if q is not None:
+        if q_weight is not None:
+            _vector(q_weight, d.f32, cache.dim, "q_weight")
+            ops[0].weight = q_weight.data_ptr()
+        if q_out is None:
+            q_out = _new(stream, q.shape, dtype, q.device)
+        ops[0].inp, ops[0].out = q.data_ptr(), q_out.data_ptr()
+    _launch("svdq_rope_append",
+            (cache._at, batch._at, None if q is None else at, at + _OPERAND_BYTES, v.data_ptr(), *v_step, tokens,
+             d.code[dtype], positions.data_ptr(), 1 if positions.dtype == torch.float32 else 0, inv_freq.data_ptr(),
+             len(axis_pairs), axes, 1 if pairs == "halves" else 0, eps), given, stream)
+    return q_out
+
+
+@functools.lru_cache(maxsize=4096)
+def tree_attention_workspace_bytes(sequences: int, tokens: int, heads: int, kv_heads: int, dim: int, table_width: int,
+                                   page_size: int) -> int:
+    return int(lib().svdq_tree_attention_workspace_bytes(sequences, tokens, heads, kv_heads, dim, table_width, page_size))
+
+
+def svdq_tree_attention(cache, batch, q, tree=None, scale=None, out=None, workspace=None, stream=None):
+    """Attention of a step's queries q [tokens, heads, dim] (fp16 or bf16; any strides with contiguous heads; turned
+    as by svdq_rope_append) over their sequences' cached keys and values, the step's own among them.  Every token
+    sees its sequence's context; of the step's tokens it sees those that its row of tree marks (bool or uint8
+    [tokens, width]: column j is the sequence's j-th token of the step, columns past the width are not seen), or,
+    without a tree, those up to itself: one decoded token, or a chunk of a prompt.  heads: a multiple of the
+    cache's.  scale: dim ** -0.5 when None.  A row that sees nothing is zeros; tokens of no sequence keep what out
+    held.  out may be q.  workspace: device bytes for the sums of the keys' parts (tree_attention_workspace_bytes;
+    allocated here when None)."""
+    d = _dtypes or _d()
+    torch = d.torch
+    _paged(cache, batch)
+    if q is None:
+        raise ValueError("q is required")
+    dtype = q.dtype
+    if dtype not in cache.step_types or not q.is_cuda:
+        raise ValueError(f"q must be a device tensor and one of {cache.step_types} for a cache of {cache.dtype}, got {dtype}")
+    if q.dim() != 3 or q.shape[2] != cache.dim:
+        raise ValueError(f"q must have shape [tokens, heads, {cache.dim}], got {tuple(q.shape)}")
+    tokens, heads, dim = q.shape
+    if heads < 1 or heads % cache.heads:
+        raise ValueError(f"q's heads must be a multiple of the cache's {cache.heads}, got {heads}")
+    q_step = q.stride()
+    if q_step[2] != 1:
+        raise ValueError("q's heads must be contiguous")
+    if scale is None:
+        scale = dim ** -0.5
+    t_step = t_width = 0
+    at = None
+    if tree is not None:
+        t_step = _rows(tree, (torch.bool, torch.uint8), None, "tree")
+        if tree.shape[0] != tokens:
+            raise ValueError(f"tree must have a row for each of the {tokens} tokens, got {tree.shape[0]}")
+        t_width = tree.shape[1]
+        at = tree.data_ptr() or q.data_ptr()       # a tree without columns has no memory, and is a tree all the same
+    if out is None:
+        o_step = (heads * dim, dim)
+    else:
+        if not out.is_cuda or out.dtype != dtype or out.shape != q.shape or out.stride()[2] != 1:
+            raise ValueError(f"out must be a {dtype} device tensor of shape {tuple(q.shape)} with contiguous heads")
+        _apart(out.shape, out.stride(), "out")
+        o_step = out.stride()
+    given = (cache.k, batch.page_table, q, tree, out, workspace)
+    if workspace is not None:
+        _need(workspace, None, None, "workspace")
+        room = workspace.numel() * workspace.element_size()
+    else:
+        room = tree_attention_workspace_bytes(batch.sequences, tokens, heads, cache.heads, dim, batch.width, cache.page_size)
+        if room:
+            workspace = _new_workspace(stream, room, q.device)
+    if out is None:
+        out = _new(stream, q.shape, dtype, q.device)
+    _launch("svdq_tree_attention",
+            (cache._at, batch._at, q.data_ptr(), q_step[0], q_step[1], heads, tokens, d.code[dtype], scale, at, t_step,
+             t_width, out.data_ptr(), o_step[0], o_step[1], _p(workspace), room), given, stream)
+    return out
+
+
+def svdq_cache_keep(cache, batch, path, stream=None):
+    """Keeps a draft's accepted tokens: slot context + i of sequence b takes keys, values and scales of slot context
+    + path[b, i], for path int32 [sequences, width] whose rows rise and end in negative entries.  batch: that of
+    the step which drafted them (its context before the draft)."""
+    d = _dtypes or _d()
+    _paged(cache, batch)
+    step = _rows(path, (d.torch.int32,), None, "path")
+    if path.shape[0] != batch.sequences:
+        raise ValueError(f"path must have a row for each of the {batch.sequences} sequences, got {path.shape[0]}")
+    _launch("svdq_cache_keep", (cache._at, batch._at, path.data_ptr(), step, path.shape[1]),
+            (cache.k, batch.page_table, path), stream)
 
 
 # svdq_linear_noalloc's static device scratch (SVDQ_STATIC_SCRATCH_BYTES in include/svdq.h)

@@ -1,0 +1,374 @@
+// Attention of a step's tokens over a paged cache (svdq_tree_attention), for few rows a cache head:
+//
+//   o[t, h] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q[t, h] . k_j - m)
+//
+// over the keys j of the token's sequence that it sees: the context's, and of the step's own tokens those
+// that its row of the tree marks (or, without a tree, those up to itself).  One pass over the keys with the
+// running maximum and sum of the softmax.
+//
+// The cache's bytes bound it.  A row is a token and one of the `group` query heads that share a cache head;
+// a workgroup has 16 NT rows of one sequence and cache head and a part of the keys, its waves take turns at
+// tiles of 32 keys, each with sums of its own, joined at the end through LDS and over the parts by
+// k_attn_join.  Nothing is shared between the waves in between, so there is no barrier in the loop and the
+// loads of many waves are in flight at once.
+//
+// Per tile the transposed products keep a row's values in one lane column: S^T = K Q^T (16 keys a result
+// tile) and O^T = V^T P^T.  A lane then has 8 of the 32 probabilities of its row c = lane % 16, in just the
+// order in which it feeds them back as the second product's operand: keys 16 t + 4 (lane / 16) + i in place
+// 4 t + i of the contraction, and V is read from LDS in that order, transposed on the way.
+#include "paged_attn.h"
+
+namespace svdq {
+
+namespace {
+
+using namespace attn;
+
+template <bool BF, int CK, int DP, int NT, int NW>
+__global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
+  constexpr int kV = DP + 16;                // halves a row of V in LDS: eight rows side by side reach every bank
+  constexpr int kSteps = DP / 32;            // of the contraction over the head's values
+  constexpr int kPieces = CK == C16 ? DP / 8 : DP / 16;   // 16-byte pieces a row of the cache
+  constexpr int kLoads = kPieces / 2;        // of a lane, for 32 rows of V
+  constexpr int kRows = 64 / kPieces;        // of V a load instruction
+  __shared__ __attribute__((aligned(16))) uint16_t lds_v[NW][32 * kV];
+  __shared__ __attribute__((aligned(16))) float lds_s[CK == C16 ? 1 : NW][3][32];    // scales of K and V, V's as they are
+  __shared__ float lds_ml[NW][16 * NT][2];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, quad = lane >> 4;
+
+  Work w;
+  if (!find_work<16 * NT>(a, w)) return;     // the whole workgroup
+  const int kmax = w.last_key(a, w.row0 + 16 * NT - 1);
+  int begin, end;
+  w.part(a, kmax, 32 * NW, &begin, &end);
+  const int dim = a.c.dim;
+
+  // rows and their queries
+  int tok[NT];
+  bool valid[NT];
+  float coef[NT];
+  v4u qf[NT][kSteps];
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    const int r = w.row0 + 16 * n + c;
+    valid[n] = r < w.rows;
+    const int i = r / a.group;
+    tok[n] = valid[n] ? i : 0;
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)(w.s0 + tok[n]) * a.q_token +
+                        (int64_t)(w.head * a.group + r - i * a.group) * a.q_head;
+#pragma unroll
+    for (int s = 0; s < kSteps; s++) {
+      const int d = CK == C16 ? s * 32 + quad * 8 : (s >> 1) * 64 + quad * 16 + (s & 1) * 8;
+      qf[n][s] = v4u{0, 0, 0, 0};
+      if (valid[n] && d < dim) __builtin_memcpy(&qf[n][s], q + d, 16);
+    }
+    coef[n] = a.scale;
+    if (CK != C16 && a.qbf) coef[n] *= queries_to_f16<kSteps>(qf[n]);
+  }
+
+  v4f acc[NT][DP / 16];
+  float m[NT], l[NT], ref = 0.f;             // ref: what V's scales are taken relative to (8-bit caches)
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    m[n] = -INFINITY;
+    l[n] = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] = v4f{0.f, 0.f, 0.f, 0.f};
+  }
+  uint16_t* vt = lds_v[wave];
+  const int es = CK == C16 ? 2 : 1;
+  const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + w.head * a.c.head * es;
+  const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + w.head * a.c.head * es;
+  const int l32 = lane & 31;
+
+  auto page_at = [&](int base) {             // of key base + lane % 32
+    const int key = base + l32;
+    return key < end ? page_of(a.b, a.c, w.seq, key) : -1;
+  };
+  int base = begin + wave * 32;
+  int page = page_at(base);
+  for (; base < end; base += 32 * NW) {
+    const int next = page_at(base + 32 * NW);
+    const int key0 = base + l32;
+    const int64_t in_page = key0 & ((1 << a.c.shift) - 1);
+    const int64_t off = page < 0 ? -1 : (page * a.c.page + in_page * a.c.token) * es;
+    const uint32_t live = (uint32_t)__ballot(page >= 0);
+    const int lo = (int)off, hi = (int)(off >> 32);
+    auto row_at = [&](int row) {             // byte offset of a row of the tile, below 0: absent
+      return ((int64_t)__shfl(hi, row) << 32) | (uint32_t)__shfl(lo, row);
+    };
+    // K: a lane's operands straight from memory; V: whole rows
+    v4u kf[2][CK == C16 ? kSteps : kSteps / 2], vr[kLoads];
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      const int64_t o = row_at(16 * t + c);
+#pragma unroll
+      for (int s = 0; s < (CK == C16 ? kSteps : kSteps / 2); s++) {
+        const int d = CK == C16 ? s * 32 + quad * 8 : s * 64 + quad * 16;
+        kf[t][s] = v4u{0, 0, 0, 0};
+        if (o >= 0 && d < dim) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + o + d * es);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int64_t o = row_at(i * kRows + lane / kPieces);
+      const int piece = lane % kPieces;
+      vr[i] = v4u{0, 0, 0, 0};
+      if (o >= 0 && piece * (16 / es) < dim) vr[i] = *reinterpret_cast<const v4u*>(vbase + o + piece * 16);
+    }
+    float ks = 0.f, vs = 0.f;
+    if (CK != C16 && page >= 0) {
+      const int64_t so = page * a.c.spage + in_page * a.c.stoken + w.head * a.c.shead;
+      ks = a.c.ks[so];
+      vs = a.c.vs[so];
+    }
+    const bool masked = base + 32 > w.ctx || live != 0xFFFFFFFFu;   // the same in every lane
+    uint32_t seen[NT];
+    if (masked) {
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        seen[n] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+          const int k = (e >> 2) * 16 + quad * 4 + (e & 3);
+          if (valid[n] && (live >> k & 1) && w.sees(a, tok[n], base + k)) seen[n] |= 1u << e;
+        }
+      }
+    }
+    page = next;
+
+    // S^T
+    v4f st[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; n++) st[n][0] = st[n][1] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+      for (int s = 0; s < kSteps; s++) {
+        const v4u kk = CK == C16 ? kf[t][s] : widen<CK>(kf[t][s >> 1], s & 1);
+#pragma unroll
+        for (int n = 0; n < NT; n++) st[n][t] = mfma16<BF>(kk, qf[n][s], st[n][t]);
+      }
+
+    // rows of V that hold an infinity or NaN and are hidden from some row: taken out of the product below
+    uint32_t bad = 0;
+    if (masked) {
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) {
+        const uint64_t b = __ballot(not_finite<BF, CK>(vr[i]));
+        if (b) {
+#pragma unroll
+          for (int r = 0; r < kRows; r++)
+            if (b >> (r * kPieces) & ((1ull << (kPieces - 1) << 1) - 1)) bad |= 1u << (i * kRows + r);
+        }
+      }
+      if (CK != C16) bad |= (uint32_t)__ballot(lane < 32 && !(__builtin_fabsf(vs) < INFINITY));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();         // the last tile's reads of LDS are done
+    if (CK != C16 && lane < 32) {
+      lds_s[wave][0][lane] = ks;
+      lds_s[wave][1][lane] = bad >> lane & 1 ? 0.f : vs;
+      lds_s[wave][2][lane] = vs;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      uint16_t* to = vt + (i * kRows + lane / kPieces) * kV + lane % kPieces * (CK == C16 ? 8 : 16);
+      if (CK == C16) {
+        *reinterpret_cast<v4u*>(to) = vr[i];
+      } else {
+        *reinterpret_cast<v4u*>(to) = widen<CK>(vr[i], 0);
+        *reinterpret_cast<v4u*>(to + 8) = widen<CK>(vr[i], 1);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+
+    // logits in powers of two
+    float z[NT][8], vsc[8];
+    if (CK != C16) {
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const v4f x = *reinterpret_cast<const v4f*>(&lds_s[wave][0][16 * t + 4 * quad]);
+        const v4f y = *reinterpret_cast<const v4f*>(&lds_s[wave][1][16 * t + 4 * quad]);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          vsc[4 * t + i] = y[i];
+#pragma unroll
+          for (int n = 0; n < NT; n++) z[n][4 * t + i] = st[n][t][i] * x[i] * coef[n];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) z[n][e] = st[n][e >> 2][e & 3] * coef[n];
+    }
+    if (masked) {
+#pragma unroll
+      for (int n = 0; n < NT; n++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) z[n][e] = seen[n] >> e & 1 ? z[n][e] : -INFINITY;
+    }
+    // The reference that a row's powers are taken from moves only when a logit passes it by kSlack, so
+    // that most tiles need no exchange between lanes and no rescaling: powers stay below 2^kSlack.
+    float top[NT], vtop = 0.f;
+    bool move = false;
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      top[n] = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 8; e++) top[n] = fmaxf(top[n], z[n][e]);
+      move = move || top[n] > m[n] + kSlack;
+    }
+    if (CK != C16) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) vtop = fmaxf(vtop, __builtin_fabsf(vsc[e]));
+      move = move || vtop > 8.f * ref;
+    }
+    if (__any(move)) {
+      float back = 1.f;
+      if (CK != C16) {
+        vtop = fmaxf(vtop, ref);
+        vtop = fmaxf(vtop, __shfl_xor(vtop, 16));
+        vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
+        back = vtop > 0.f ? ref / vtop : 1.f;
+        ref = vtop;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        float mn = fmaxf(top[n], m[n]);
+        mn = fmaxf(mn, __shfl_xor(mn, 16));
+        mn = fmaxf(mn, __shfl_xor(mn, 32));
+        const float f = mn == m[n] ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
+        m[n] = mn;
+        l[n] *= f;
+#pragma unroll
+        for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] *= f * back;
+      }
+    }
+    v4u pf[NT];
+    const float inv = CK != C16 && ref > 0.f ? 1.f / ref : 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; n++) {
+      const float mu = m[n] == -INFINITY ? 0.f : m[n];
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        z[n][e] = __builtin_amdgcn_exp2f(z[n][e] - mu);
+        l[n] += z[n][e];
+      }
+      // Rounded to 16 bits for the matrix cores (the sum above is of the unrounded): half an ulp of each
+      // term.  With 8-bit caches V's scale joins here, relative to ref (the largest so far, within a factor
+      // of 8): a product below fp16's range is below 2^-24 of the largest's weight.
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        pf[n][e] = CK == C16 ? pack16(z[n][2 * e], z[n][2 * e + 1], BF)
+                             : pack_f16(z[n][2 * e] * (vsc[2 * e] * inv), z[n][2 * e + 1] * (vsc[2 * e + 1] * inv));
+    }
+    if (bad) {                               // hidden rows keep out what 0 * infinity would bring in
+      for (uint32_t rest = bad; rest; rest &= rest - 1) {
+        const int k = __builtin_ctz(rest), e = (k >> 4) * 4 + (k & 3), from = (k >> 2 & 3) * 16 + c;
+        const float vscale = CK == C16 ? 1.f : lds_s[wave][2][k] * inv;
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+          float p = 0.f;
+          uint32_t sn = 0;
+#pragma unroll
+          for (int x = 0; x < 8; x++)
+            if (x == e) p = z[n][x], sn = seen[n] >> x & 1;
+          p = __shfl(p, from);
+          sn = __shfl((int)sn, from);
+#pragma unroll
+          for (int dt = 0; dt < DP / 16; dt++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              const uint32_t b = vt[k * kV + dt * 16 + quad * 4 + i];
+              if (sn) acc[n][dt][i] += p * ((BF ? bf16_f32(b) : f16_f32(b)) * vscale);
+            }
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      for (uint32_t rest = bad; rest; rest &= rest - 1)
+        for (int d = lane; d < DP; d += 64) vt[__builtin_ctz(rest) * kV + d] = 0;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+#pragma unroll
+    for (int dt = 0; dt < DP / 16; dt++) {
+      const uint16_t* at = vt + (quad * 4 + (c >> 2)) * kV + dt * 16 + (c & 3) * 4;
+      const v4u vv = transposed(at, at + 16 * kV);
+#pragma unroll
+      for (int n = 0; n < NT; n++) acc[n][dt] = mfma16<BF>(vv, pf[n], acc[n][dt]);
+    }
+  }
+
+  // the waves' sums joined
+#pragma unroll
+  for (int n = 0; n < NT; n++) {
+    l[n] += __shfl_xor(l[n], 16);
+    l[n] += __shfl_xor(l[n], 32);
+    if (quad == 0) {
+      lds_ml[wave][16 * n + c][0] = m[n];
+      lds_ml[wave][16 * n + c][1] = l[n];
+    }
+  }
+  constexpr int CH = DP / NT;                // columns a turn: NW * 16 NT rows of them take V's room
+  constexpr int kP = CH / 4;                 // pieces of four
+  const float unit = CK == C16 ? 1.f : ref;
+#pragma unroll
+  for (int turn = 0; turn < NT; turn++) {
+    __syncthreads();
+    float* mine = reinterpret_cast<float*>(vt);
+#pragma unroll
+    for (int n = 0; n < NT; n++)
+#pragma unroll
+      for (int x = 0; x < CH / 16; x++) {
+        const v4f v = acc[n][turn * (CH / 16) + x] * unit;
+        *reinterpret_cast<v4f*>(mine + (16 * n + c) * CH + (((x * 4 + quad) ^ c) & (kP - 1)) * 4) = v;
+      }
+    __syncthreads();
+    for (int u = threadIdx.x; u < 16 * NT * kP; u += 64 * NW) {
+      const int row = u / kP, piece = u % kP, d = turn * CH + piece * 4;
+      if (w.row0 + row >= w.rows || d >= dim) continue;
+      float mm = -INFINITY, sum = 0.f;
+      for (int x = 0; x < NW; x++) mm = fmaxf(mm, lds_ml[x][row][0]);
+      v4f o{0.f, 0.f, 0.f, 0.f};
+      for (int x = 0; x < NW; x++) {
+        const float f = lds_ml[x][row][0] == mm ? 1.f : __builtin_amdgcn_exp2f(lds_ml[x][row][0] - mm);
+        sum += f * lds_ml[x][row][1];
+        const float* at = reinterpret_cast<const float*>(lds_v[x]) + row * CH + ((piece ^ (row & 15)) & (kP - 1)) * 4;
+        o += f * *reinterpret_cast<const v4f*>(at);
+      }
+      put(a, w, row, d, o, mm, sum);
+    }
+  }
+}
+
+template <bool BF, int CK, int DP>
+hipError_t launch(const AttnArgs& a, hipStream_t s) {
+  constexpr int NT = 1, NW = 4;
+  const int64_t slots = (int64_t)a.tokens * a.group / (16 * NT) + a.b.n;
+  const int64_t blocks = slots * a.c.heads * a.splits;
+  if (!launchable(blocks, 64 * NW)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_attn_few<BF, CK, DP, NT, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, a);
+  return hipGetLastError();
+}
+
+template <bool BF, int CK>
+hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
+  return a.c.dim <= 64 ? launch<BF, CK, 64>(a, s) : a.c.dim <= 128 ? launch<BF, CK, 128>(a, s) : launch<BF, CK, 256>(a, s);
+}
+
+}  // namespace
+
+hipError_t attn::launch_few(const AttnArgs& a, hipStream_t s) {
+  switch (a.c.type) {
+    case T_F16: return launch_dim<false, C16>(a, s);
+    case T_BF16: return launch_dim<true, C16>(a, s);
+    case T_INT8: return launch_dim<false, CI8>(a, s);
+    default: return launch_dim<false, CE4>(a, s);
+  }
+}
+
+}  // namespace svdq

@@ -1,0 +1,57 @@
+// Shared by the operators around a paged cache of keys and values (k_append.hip, k_attn_few.hip):
+// the argument structs cache_api.hip fills, and how a kernel finds a token's sequence.
+#pragma once
+#include "block_ops.h"
+#include "slots.h"
+
+namespace svdq {
+
+constexpr float kTiny = 0x1p-100f;           // floor of a head's absolute maximum: zeros get codes 0 and a finite scale
+
+struct AppendArgs {
+  RopeArgs r;                                // op[0] queries (heads 0: none), op[1] keys (out unused)
+  const void* v; int64_t v_token, v_head;
+  PagedCache c; PagedBatch b;
+};
+hipError_t launch_append(const AppendArgs& a, hipStream_t s);
+
+struct KeepArgs {
+  PagedCache c; PagedBatch b;
+  const int* path; int64_t path_stride; int path_width;
+};
+hipError_t launch_keep(const KeepArgs& a, hipStream_t s);
+
+struct AttnArgs {
+  PagedCache c; PagedBatch b;
+  const void* q; int64_t q_token, q_head;
+  void* o; int64_t o_token, o_head;
+  int tokens, heads, group, qbf;             // group: query heads a cache head; qbf: q and o are bf16
+  float scale;                               // times log2(e)
+  const uint8_t* tree; int64_t tree_stride; int tree_width;
+  int splits;                                // of each sequence's keys
+  float* part;                               // fp32 [splits][tokens * heads][dim] sums, then [tokens * heads][splits][2]
+};
+// Parts that the keys are split into when the workspace has room for them, and its bytes.
+int attn_splits(int sequences, int tokens, int heads, int kv_heads, int64_t reach);
+size_t attn_part_bytes(int splits, int tokens, int heads, int dim);
+hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
+
+// The last i in [0, n) with f(i) <= target, for f that never falls; -1 if there is none.  The wave looks
+// at 64 places at once, so that 4096 sequences take two loads' time.
+template <typename F>
+__device__ __forceinline__ int last_below(int n, int64_t target, F f) {
+  const int lane = __lane_id();
+  int lo = 0, len = n;
+  for (;;) {
+    const int step = (len + 63) / 64;
+    const int i = lo + lane * step;
+    const bool in = lane * step < len && f(min(i, n - 1)) <= target;
+    const int count = __popcll(__ballot(in));
+    if (count == 0) return lo - 1;           // only in the first turn: later ones begin at a place that holds
+    lo += (count - 1) * step;
+    if (step == 1) return lo;
+    len = min(step, n - lo);
+  }
+}
+
+}  // namespace svdq

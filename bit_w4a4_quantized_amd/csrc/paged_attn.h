@@ -1,0 +1,168 @@
+// Shared by the attention kernels over a paged cache (k_attn_few.hip, k_attn_many.hip, k_attn_join.hip).
+#pragma once
+#include "paged.h"
+
+namespace svdq {
+namespace attn {
+
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// What the cache holds: the queries' own 16-bit type, or codes, which become fp16 (exactly: 8 bits and E4M3's
+// range fit it), and so do the queries then.
+enum Kind { C16, CI8, CE4 };
+
+constexpr float kSlack = 8.f;                // powers of two that a row's reference may lag behind
+
+template <bool BF>
+__device__ __forceinline__ v4f mfma16(const v4u& x, const v4u& y, const v4f& z) {
+  if (BF) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, x), __builtin_bit_cast(v8bf, y), z, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, x), __builtin_bit_cast(v8h, y), z, 0, 0, 0);
+}
+
+// Eight codes of a piece of sixteen (its first half or second) as fp16.
+template <int CK>
+__device__ __forceinline__ v4u widen(const v4u& u, int second) {
+  const uint32_t w[2] = {second ? u[2] : u[0], second ? u[3] : u[1]};
+  v4u r;
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    if (CK == CE4) {
+      r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], 1.0f, false));
+      r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w[i], 1.0f, true));
+    } else {
+      // code + 128 as the low byte of a half in [1024, 2048), whose steps are ones; 1152 off it is exact
+      const uint32_t b = w[i] ^ 0x80808080u;
+      const f16x2 off = {(_Float16)1152.f, (_Float16)1152.f};
+      const f16x2 lo = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04010400u)) - off;
+      const f16x2 hi = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, b, 0x04030402u)) - off;
+      r[2 * i] = __builtin_bit_cast(uint32_t, lo);
+      r[2 * i + 1] = __builtin_bit_cast(uint32_t, hi);
+    }
+  }
+  return r;
+}
+
+// Whether a piece of the cache holds an infinity or NaN.
+template <bool BF, int CK>
+__device__ __forceinline__ bool not_finite(const v4u& u) {
+  if (CK == CI8) return false;
+  bool r = false;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if (CK == CE4) {
+#pragma unroll
+      for (int b = 0; b < 4; b++) r = r || (u[i] >> (8 * b) & 0x7Fu) == 0x7Fu;
+    } else {
+      constexpr uint32_t e = BF ? 0x7F80u : 0x7C00u;
+      r = r || (u[i] & e) == e || (u[i] >> 16 & e) == e;
+    }
+  }
+  return r;
+}
+
+// A row of bf16 queries (its pieces lie in lanes c, c + 16, c + 32, c + 48, or c and c + 32) as fp16, divided by
+// a power of two that brings its largest into [1, 2): exact for values down to 2^-14 of the largest and
+// within 2^-25 of it below.  Returns the power.
+template <int N>
+__device__ __forceinline__ float queries_to_f16(v4u* q) {
+  float top = 0.f;
+#pragma unroll
+  for (int s = 0; s < N; s++)
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      top = fmaxf(top, fmaxf(__builtin_fabsf(bf16_f32(q[s][i] & 0xFFFFu)), __builtin_fabsf(bf16_f32(q[s][i] >> 16))));
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  const int e = top > 0.f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;
+#pragma unroll
+  for (int s = 0; s < N; s++)
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      q[s][i] = pack_f16(__builtin_ldexpf(bf16_f32(q[s][i] & 0xFFFFu), -e), __builtin_ldexpf(bf16_f32(q[s][i] >> 16), -e));
+  return __builtin_ldexpf(1.f, e);
+}
+
+// Four values of each of two blocks of a matrix in LDS, turned: among 16 lanes, lane 4 r + p points at values
+// 4 p ... of row r and gets column lane % 16 of the four rows.
+__device__ __forceinline__ v4u transposed(const uint16_t* x, const uint16_t* y) {
+  typedef __attribute__((address_space(3))) s16x4 lds4;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)x), b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)y);
+  const u32x2_t p = __builtin_bit_cast(u32x2_t, a), q = __builtin_bit_cast(u32x2_t, b);
+  return v4u{p[0], p[1], q[0], q[1]};
+}
+
+// A workgroup's share: rows row0 ... of a sequence (token * group + query head of the group), a cache head
+// and a part of the keys.
+struct Work {
+  int seq, head, split, s0, n, ctx, keys;    // s0: first token; n: tokens; keys: context and tokens that have a slot
+  int row0, rows;
+
+  // One past the last key that any row up to `row` sees.
+  __device__ __forceinline__ int last_key(const AttnArgs& a, int row) const {
+    return a.tree ? keys : min(keys, ctx + min(row / a.group, n - 1) + 1);
+  }
+  __device__ __forceinline__ void part(const AttnArgs& a, int kmax, int unit, int* begin, int* end) const {
+    int each = (kmax + a.splits - 1) / a.splits;
+    each = (each + unit - 1) / unit * unit;
+    *begin = (int)min((int64_t)kmax, (int64_t)split * each);
+    *end = min(kmax, *begin + each);
+  }
+  // Whether token i of the sequence sees an existing key.
+  __device__ __forceinline__ bool sees(const AttnArgs& a, int i, int key) const {
+    const int j = key - ctx;
+    if (j < 0) return true;
+    if (!a.tree) return j <= i;
+    return j < a.tree_width && a.tree[(int64_t)(s0 + i) * a.tree_stride + j];
+  }
+};
+
+// Workgroups are numbered heads first (those of a cache head on one XCD, which share rows of the cache where a
+// sequence has several row tiles), then parts, then slots of rows.  Sequence i has the slots from
+// floor(starts[i] group / R) + i on: one more than it may need, found without a sum over the sequences.
+template <int R>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
+  int id = blockIdx.x;
+  w.head = id % a.c.heads;
+  id /= a.c.heads;
+  w.split = id % a.splits;
+  const int slot = id / a.splits;
+  auto first = [&](int i) { return (int64_t)start_of(a.b, i, a.tokens) * a.group / R + i; };
+  w.seq = __builtin_amdgcn_readfirstlane(last_below(a.b.n, slot, first));
+  if (w.seq < 0) return false;
+  w.s0 = start_of(a.b, w.seq, a.tokens);
+  w.n = max(0, start_of(a.b, w.seq + 1, a.tokens) - w.s0);
+  w.rows = w.n * a.group;
+  const int64_t row0 = (slot - first(w.seq)) * R;
+  if (row0 >= w.rows) return false;
+  w.row0 = (int)row0;
+  w.ctx = context_of(a.b, w.seq);
+  const int64_t reach = (int64_t)a.b.width << a.c.shift;
+  w.keys = (int)min((int64_t)w.ctx + w.n, reach);
+  return true;
+}
+
+// Four values of a row's result: the output where the keys are whole, else this part's sums.
+__device__ __forceinline__ void put(const AttnArgs& a, const Work& w, int row, int d, const v4f& o, float m, float sum) {
+  const int r = w.row0 + row, i = r / a.group, t = w.s0 + i, h = w.head * a.group + r - i * a.group;
+  if (a.splits == 1) {
+    const float f = sum == 0.f ? 0.f : 1.f / sum;      // a row that sees nothing is zeros
+    uint16_t* to = static_cast<uint16_t*>(a.o) + (int64_t)t * a.o_token + (int64_t)h * a.o_head + d;
+    const uint32_t x[2] = {pack16(o[0] * f, o[1] * f, a.qbf), pack16(o[2] * f, o[3] * f, a.qbf)};
+    __builtin_memcpy(to, x, 8);
+    return;
+  }
+  const int64_t rows = (int64_t)a.tokens * a.heads, at = (int64_t)t * a.heads + h;
+  *reinterpret_cast<v4f*>(a.part + (w.split * rows + at) * a.c.dim + d) = o;
+  if (d == 0) {
+    float* ml = a.part + a.splits * rows * a.c.dim + (at * a.splits + w.split) * 2;
+    ml[0] = m;
+    ml[1] = sum;
+  }
+}
+
+hipError_t launch_few(const AttnArgs& a, hipStream_t s);
+
+}  // namespace attn
+}  // namespace svdq

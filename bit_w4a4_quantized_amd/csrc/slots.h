@@ -1,0 +1,42 @@
+// Where a sequence's tokens lie in a paged cache.  Everything here that the host cannot see (a batch's starts,
+// contexts and page table) may hold anything: starts are taken within the tokens there are, contexts within 0
+// and 2^30, and a slot whose column or page does not exist is absent (never written, hidden from attention).
+// Plain C++, for kernels and for tests without a GPU.
+#pragma once
+#include <stdint.h>
+
+#ifdef __HIP__
+#define SVDQ_BOTH __host__ __device__
+#else
+#define SVDQ_BOTH
+#endif
+
+namespace svdq {
+
+constexpr int kMaxContext = 1 << 30;
+
+struct PagedCache {
+  void* k; void* v; float* ks; float* vs; int type;
+  int pages, shift, heads, dim;              // 2^shift tokens a page
+  int64_t page, token, head;                 // strides in elements, of k and v
+  int64_t spage, stoken, shead;              // of ks and vs
+};
+
+struct PagedBatch {
+  const int* table; int64_t stride; int width;
+  const int* starts; const int* context; int n;
+};
+
+SVDQ_BOTH inline int within(int v, int most) { return v < 0 ? 0 : v > most ? most : v; }
+SVDQ_BOTH inline int start_of(const PagedBatch& b, int i, int tokens) { return within(b.starts[i], tokens); }
+SVDQ_BOTH inline int context_of(const PagedBatch& b, int i) { return within(b.context[i], kMaxContext); }
+
+// The page of a sequence's slot, -1 if it has none.
+SVDQ_BOTH inline int page_of(const PagedBatch& b, const PagedCache& c, int seq, int slot) {
+  const int col = slot >> c.shift;
+  if (col >= b.width) return -1;
+  const int id = b.table[seq * b.stride + col];
+  return (unsigned)id < (unsigned)c.pages ? id : -1;
+}
+
+}  // namespace svdq

@@ -492,6 +492,98 @@ svdq_status svdq_rope_axes(const svdq_rope_operand* operands, int count, int bat
                            const float* inv_freq, int axes, const int* axis_pairs, int halves, float eps,
                            int inverse, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The operators around a paged cache of keys and values, for decoding.  Conventions as for the block's
+ * operators above.  The cache's pages are handed out by the caller; a step adds `tokens` tokens of
+ * several sequences, packed one sequence behind the other:
+ *   svdq_rope_append      turns the step's queries and keys and writes keys and values to the cache;
+ *   svdq_tree_attention   lets the step's queries attend to the cache, the step's own tokens in it;
+ *   svdq_cache_keep       of a drafted tree, moves the accepted path's keys and values together.
+ */
+typedef struct {
+  void* k;               /* keys [pages, page_size, heads, dim] of `type`, by the strides below, the values of a */
+  void* v;               /* head contiguous; values the same.  16-byte aligned */
+  float* k_scales;       /* 8-bit types: [pages, page_size, heads], a head's value is code * scale; else ignored */
+  float* v_scales;
+  svdq_type type;        /* SVDQ_TYPE_F16 or _BF16 (the type of the step's tokens), _INT8 or _E4M3 */
+  int64_t pages;         /* 0 ... 2^31 - 1 */
+  int page_size;         /* tokens a page: a power of two up to 2^16 */
+  int heads;             /* 1 ... 2^16 */
+  int dim;               /* 8 ... 256, a multiple of 8 (16 for an 8-bit type) */
+  int64_t page_stride, token_stride, head_stride;   /* of k and v, in elements, multiples of 16 bytes */
+  int64_t scale_page_stride, scale_token_stride, scale_head_stride;   /* of the scales, in elements */
+} svdq_paged_cache;
+
+typedef struct {
+  const int* page_table; /* int32 [sequences, table_width], rows table_stride apart: slot s of a sequence is token
+                            s % page_size of page page_table[s / page_size].  An entry outside the cache's pages, or
+                            a column past the table, is no page: nothing is written there, and attention does not see it */
+  int64_t table_stride;
+  int table_width;       /* table_width * page_size <= 2^30 */
+  const int* starts;     /* int32 [sequences + 1], not falling: sequence b has the tokens starts[b] ... starts[b + 1] - 1 of
+                            the step.  Tokens outside starts[0] ... starts[sequences] - 1 belong to none */
+  const int* context;    /* int32 [sequences], 0 ... 2^30: tokens in the cache before the step; token i of the step has
+                            slot context[b] + i */
+  int sequences;         /* 0 ... 2^24 (0: the pointers may be NULL) */
+} svdq_paged_batch;
+
+/*
+ * Rotary positions on a step's queries and keys, and its keys and values into the cache, in one launch:
+ *   queries: turned as svdq_rope_axes turns them, to q->out;
+ *   keys: turned the same way, then rounded once to a 16-bit cache's type, or quantized: a =
+ *     max(max_d |u_d|, 2^-100), code = rnd(u * (qmax / a)) with qmax 127 (INT8, ties to even) or 448 (E4M3),
+ *     scale = a / qmax;
+ *   values: to the cache the same way, unturned.
+ *   q : queries ([tokens, heads, dim] by in_token, in_head; `out` by out_token, out_head; may be `in` with the
+ *       same strides), or NULL for none.  k : keys, k->heads the cache's; its `out` is unused.  The batch
+ *       strides of both are unused.  v : [tokens, cache heads, dim] by v_token, v_head.
+ *   positions : [tokens, axes] int32, or fp32 with positions_fp32 != 0; the position of a token need not be
+ *       its slot (tokens of a tree share positions).  Other arguments as for svdq_rope_axes.
+ * Queries of tokens that belong to no sequence are turned too; their keys and values go nowhere.  Two tokens
+ * of a step must not have the same slot of the same page (which one's values stay is then open).  8-bit
+ * codes are those of finite values. */
+svdq_status svdq_rope_append(const svdq_paged_cache* cache, const svdq_paged_batch* batch, const svdq_rope_operand* q,
+                             const svdq_rope_operand* k, const void* v, int64_t v_token, int64_t v_head, int tokens,
+                             svdq_type type, const void* positions, int positions_fp32, const float* inv_freq, int axes,
+                             const int* axis_pairs, int halves, float eps, void* stream);
+
+/*
+ * Attention of a step's tokens over the cache (which svdq_rope_append has brought the step's own keys and
+ * values into):
+ *   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[t, h] . k_j - max),
+ * over the keys j of cache head h / (heads / cache heads) that token t, the i-th of its sequence in the step, sees:
+ * the slots below the sequence's context, and of the step's own tokens the j-th where
+ *   tree[t, j] != 0 (a byte; j >= tree_width: not seen)    with a tree,
+ *   j <= i                                                 without (a chain: one token, or a chunk of a prompt).
+ * A row that sees nothing is zeros.  What a token does not see has no effect on it, infinities and NaN included.
+ *   q, out : [tokens, heads, dim] of `type` by their strides; heads a multiple of the cache's.  out may be q with
+ *            the same strides.  Rows of tokens that belong to no sequence are left as they were.
+ *   scale  : finite, > 0.
+ *   tree   : bytes [tokens, tree_width], rows tree_stride apart, or NULL.
+ * Logits, the softmax's statistics and sums are fp32; probabilities are rounded to 16 bits for the matrix
+ * cores (to fp16 with an 8-bit cache, whose scales of values join them there).
+ *   workspace, workspace_bytes : caller-owned device scratch, 16-byte aligned, for the sums of the keys' parts
+ *            where there are few rows (svdq_tree_attention_workspace_bytes); rules as for svdq_gemm_act_residual's.
+ */
+svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_batch* batch, const void* q,
+                                int64_t q_token, int64_t q_head, int heads, int tokens, svdq_type type, float scale,
+                                const void* tree, int64_t tree_stride, int tree_width, void* out, int64_t out_token,
+                                int64_t out_head, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes svdq_tree_attention uses for these sizes (0: none, or a bad size). */
+size_t svdq_tree_attention_workspace_bytes(int sequences, int tokens, int heads, int kv_heads, int dim, int table_width,
+                                           int page_size);
+
+/*
+ * A draft's accepted path: slot context[b] + i takes the keys, values and scales of slot context[b] + path[b, i]
+ * for each i below path_width with path[b, i] >= 0 and i and path[b, i] below the sequence's number of tokens
+ * in the step (starts as in the step that drafted them); other entries leave their slot as it is.  The path of
+ * a sequence rises (path[b, i] < path[b, i + 1], negative ends apart), so that path[b, i] >= i; two
+ * sequences of one call must not share pages that the path writes.
+ *   path : int32 [sequences, path_width], rows path_stride apart; path_width <= 2^16. */
+svdq_status svdq_cache_keep(const svdq_paged_cache* cache, const svdq_paged_batch* batch, const int* path,
+                            int64_t path_stride, int path_width, void* stream);
+
 /* Static description of a status code. */
 const char* svdq_status_string(svdq_status s);
 
