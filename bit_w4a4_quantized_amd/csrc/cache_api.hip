@@ -138,6 +138,7 @@ svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_
   if (st != SVDQ_OK) return st;
   if (tokens < 0 || tokens > kMaxDim || heads < 1 || heads > kMaxHeads || heads % cache->heads) return SVDQ_ERR_SHAPE;
   if ((int64_t)tokens * heads >= (int64_t)1 << 31 || !isfinite(scale) || scale <= 0.f) return SVDQ_ERR_SHAPE;
+  if (((int64_t)tokens * (heads / cache->heads) / 16 + batch->sequences) * cache->heads > 1 << 24) return SVDQ_ERR_SHAPE;
   for (const int64_t s : {q_token, q_head, out_token, out_head})
     if (!stride_ok(s)) return SVDQ_ERR_SHAPE;
   if (tree && (!stride_ok(tree_stride) || tree_width < 0)) return SVDQ_ERR_SHAPE;
@@ -163,9 +164,12 @@ svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_
   a.tree = static_cast<const uint8_t*>(tree);
   a.tree_stride = tree_stride;
   a.tree_width = tree_width;
-  a.splits = attn_splits(batch->sequences, tokens, heads, cache->heads, (int64_t)batch->table_width * cache->page_size);
-  const size_t room = workspace ? workspace_bytes : 0;
-  while (a.splits > 1 && attn_part_bytes(a.splits, tokens, heads, cache->dim) > room) a.splits--;
+  const AttnPlan p = attn_plan(batch->sequences, tokens, heads, cache->heads, cache->dim,
+                               (int64_t)batch->table_width * cache->page_size, workspace ? workspace_bytes : 0);
+  a.rows = p.rows;
+  a.slots = p.slots;
+  a.whole = p.whole;
+  a.parts = p.parts;
   a.part = static_cast<float*>(workspace);
   return map_launch(launch_attn(a, static_cast<hipStream_t>(stream)));
 }
@@ -173,10 +177,10 @@ svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_
 size_t svdq_tree_attention_workspace_bytes(int sequences, int tokens, int heads, int kv_heads, int dim, int table_width,
                                            int page_size) {
   if (sequences < 1 || tokens < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || heads > kMaxHeads ||
-      tokens > kMaxDim || dim < 8 || dim > kMaxHeadDim || table_width < 0 || page_size < 1)
+      tokens > kMaxDim || sequences > kMaxDim || dim < 8 || dim > kMaxHeadDim || table_width < 0 || page_size < 1 ||
+      (int64_t)tokens * heads >= (int64_t)1 << 31)
     return 0;
-  const int splits = attn_splits(sequences, tokens, heads, kv_heads, (int64_t)table_width * page_size);
-  return attn_part_bytes(splits, tokens, heads, dim);
+  return attn_plan(sequences, tokens, heads, kv_heads, dim, (int64_t)table_width * page_size, ~(size_t)0).bytes;
 }
 
 svdq_status svdq_cache_keep(const svdq_paged_cache* cache, const svdq_paged_batch* batch, const int* path,

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
   if (!find_work<16 * NT>(a, w)) return;     // the whole workgroup
   const int kmax = w.last_key(a, w.row0 + 16 * NT - 1);
   int begin, end;
-  w.part(a, kmax, 32 * NW, &begin, &end);
+  w.part(kmax, 32 * NW, &begin, &end);
   const int dim = a.c.dim;
 
   // rows and their queries
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
       if (valid[n] && d < dim) __builtin_memcpy(&qf[n][s], q + d, 16);
     }
     coef[n] = a.scale;
-    if (CK != C16 && a.qbf) coef[n] *= queries_to_f16<kSteps>(qf[n]);
+    if (CK != C16 && a.qbf) coef[n] *= queries_to_f16<kSteps, 16>(qf[n]);
   }
 
   v4f acc[NT][DP / 16];
@@ -81,14 +81,15 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
   const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + w.head * a.c.head * es;
   const int l32 = lane & 31;
 
-  auto page_at = [&](int base) {             // of key base + lane % 32
+  auto entry_at = [&](int base) {            // of key base + lane % 32
     const int key = base + l32;
-    return key < end ? page_of(a.b, a.c, w.seq, key) : -1;
+    return key < end ? entry_of(a.b, a.c, w.seq, key) : -1;
   };
   int base = begin + wave * 32;
-  int page = page_at(base);
+  int entry = entry_at(base);
   for (; base < end; base += 32 * NW) {
-    const int next = page_at(base + 32 * NW);
+    const int page = as_page(a.c, entry);
+    entry = entry_at(base + 32 * NW);
     const int key0 = base + l32;
     const int64_t in_page = key0 & ((1 << a.c.shift) - 1);
     const int64_t off = page < 0 ? -1 : (page * a.c.page + in_page * a.c.token) * es;
@@ -135,7 +136,6 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
         }
       }
     }
-    page = next;
 
     // S^T
     v4f st[NT][2];
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
         const float* at = reinterpret_cast<const float*>(lds_v[x]) + row * CH + ((piece ^ (row & 15)) & (kP - 1)) * 4;
         o += f * *reinterpret_cast<const v4f*>(at);
       }
-      put(a, w, row, d, o, mm, sum);
+      put<16 * NT>(a, w, row, d, o, mm, sum);
     }
   }
 }
@@ -348,8 +348,7 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
 template <bool BF, int CK, int DP>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
   constexpr int NT = 1, NW = 4;
-  const int64_t slots = (int64_t)a.tokens * a.group / (16 * NT) + a.b.n;
-  const int64_t blocks = slots * a.c.heads * a.splits;
+  const int64_t blocks = blocks_of(a);
   if (!launchable(blocks, 64 * NW)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_attn_few<BF, CK, DP, NT, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, a);
   return hipGetLastError();

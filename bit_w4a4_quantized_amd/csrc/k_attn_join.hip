@@ -1,71 +1,127 @@
-// The parts of a row's keys joined: o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, m the largest m_s, in the
-// parts' order whatever order they ended in.  And the choice of how many parts there are.
+// The parts of a row's keys joined: o = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s, m the largest m_s, in a fixed
+// order whatever order the parts ended in.  And the choice of kernel and parts.
 #include "paged_attn.h"
 
 namespace svdq {
 
 namespace {
 
-// A wave has a row; lanes over its values, two at a time.
-__global__ void __launch_bounds__(256) k_attn_join(AttnArgs a) {
-  const int64_t rows = (int64_t)a.tokens * a.heads, row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= rows) return;
-  const int t = (int)(row / a.heads), h = (int)(row - (int64_t)t * a.heads), lane = threadIdx.x & 63;
-  if (t < start_of(a.b, 0, a.tokens) || t >= start_of(a.b, a.b.n, a.tokens)) return;   // no sequence's: left as it is
-  const float* ml = a.part + a.splits * rows * a.c.dim + row * a.splits * 2;
-  float m = -INFINITY;
-  for (int s = 0; s < a.splits; s++) m = fmaxf(m, ml[2 * s]);
-  const int dim = a.c.dim;
-  float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; s++) {
-    const float f = ml[2 * s] == m ? 1.f : __builtin_amdgcn_exp2f(ml[2 * s] - m);
-    sum += f * ml[2 * s + 1];
-    const float* p = a.part + (s * rows + row) * dim;
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-      const int d = x * 128 + 2 * lane;
-      if (d < dim) {
-        o[2 * x] += f * p[d];
-        o[2 * x + 1] += f * p[d + 1];
-      }
+using namespace attn;
+
+// A row's values are P lanes' pieces of four; `deep` such groups share a row's parts (part s goes to group
+// s % deep), joined through LDS: with few rows of many parts one group would wait for one load after another.
+template <int R, int P>
+__global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
+  __shared__ __attribute__((aligned(16))) float lds[256][4];
+  __shared__ float lds_ml[256 / P][2];
+  const int per = 256 / P / deep;            // rows a workgroup
+  const int g = threadIdx.x / P, lane = threadIdx.x % P, row_in = g / deep, way = g % deep;
+  const int chunks = R / per, cut = blockIdx.x / chunks, row = (int)(blockIdx.x % chunks) * per + row_in;
+  Work w;
+  if (!find_tile<R>(a, a.whole + cut, w)) return;                 // the whole workgroup
+  const int dim = a.c.dim, d = lane * 4, parts = a.parts;
+  const bool valid = w.row0 + row < w.rows && d < dim;
+  const int64_t cuts = (int64_t)a.slots * a.c.heads - a.whole;
+  const float* ml = a.part + cuts * parts * R * dim + (cut * (int64_t)R + row) * parts * 2;
+  const float* o = a.part + (cut * (int64_t)parts * R + row) * dim + d;
+  float m = -INFINITY, l = 0.f;
+  v4f sum{0.f, 0.f, 0.f, 0.f};
+  if (valid) {
+    for (int s = way; s < parts; s += deep) m = fmaxf(m, ml[2 * s]);
+#pragma unroll 4
+    for (int s = way; s < parts; s += deep) {
+      const float f = ml[2 * s] == m ? 1.f : __builtin_amdgcn_exp2f(ml[2 * s] - m);
+      l += f * ml[2 * s + 1];
+      sum += f * *reinterpret_cast<const v4f*>(o + (int64_t)s * R * dim);
     }
   }
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* to = static_cast<uint16_t*>(a.o) + (int64_t)t * a.o_token + (int64_t)h * a.o_head;
-#pragma unroll
-  for (int x = 0; x < 2; x++) {
-    const int d = x * 128 + 2 * lane;
-    if (d < dim) {
-      const uint32_t v = pack16(o[2 * x] * f, o[2 * x + 1] * f, a.qbf);
-      __builtin_memcpy(to + d, &v, 4);
+  if (deep > 1) {
+    *reinterpret_cast<v4f*>(lds[threadIdx.x]) = sum;
+    if (lane == 0) {
+      lds_ml[g][0] = m;
+      lds_ml[g][1] = l;
+    }
+    __syncthreads();
+    if (way) return;
+    float top = -INFINITY;
+    for (int x = 0; x < deep; x++) top = fmaxf(top, lds_ml[g + x][0]);
+    l = 0.f;
+    sum = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < deep; x++) {
+      const float f = lds_ml[g + x][0] == top ? 1.f : __builtin_amdgcn_exp2f(lds_ml[g + x][0] - top);
+      l += f * lds_ml[g + x][1];
+      sum += f * *reinterpret_cast<const v4f*>(lds[threadIdx.x + x * P]);
     }
   }
+  if (!valid) return;
+  w.parts = 1;
+  put<R>(a, w, row, d, sum, m, l);
 }
+
+template <int R, int P>
+hipError_t join(const AttnArgs& a, hipStream_t s) {
+  const int64_t cuts = (int64_t)a.slots * a.c.heads - a.whole;
+  int deep = 1;                              // ways: four parts or more for each
+  while (deep < 256 / P && deep * 8 <= a.parts) deep *= 2;
+  const int64_t blocks = cuts * (R / (256 / P / deep));
+  if (!launchable(blocks, 256)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((k_attn_join<R, P>), dim3((unsigned)blocks), dim3(256), 0, s, a, deep);
+  return hipGetLastError();
+}
+
+template <int R>
+hipError_t join_dim(const AttnArgs& a, hipStream_t s) {
+  return a.c.dim <= 64 ? join<R, 16>(a, s) : a.c.dim <= 128 ? join<R, 32>(a, s) : join<R, 64>(a, s);
+}
+
+constexpr int kManyRows = 128, kFewRows = 16;
 
 }  // namespace
 
-int attn_splits(int sequences, int tokens, int heads, int kv_heads, int64_t reach) {
-  if (sequences <= 0 || tokens <= 0) return 1;
+AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, int64_t reach, size_t room) {
+  AttnPlan p{};
   const int group = heads / kv_heads;
   const int64_t each = ((int64_t)tokens * group + sequences - 1) / sequences;    // rows of a sequence and cache head
-  const int64_t tiles = (each + 15) / 16 * sequences * kv_heads;
-  int64_t s = 1024 / tiles;
-  const int64_t most = reach / 256;
-  s = s < most ? s : most;
-  return s < 1 ? 1 : s > 128 ? 128 : (int)s;
-}
-
-size_t attn_part_bytes(int splits, int tokens, int heads, int dim) {
-  return splits <= 1 ? 0 : (size_t)splits * tokens * heads * (dim + 2) * sizeof(float);
+  p.rows = each <= 32 ? kFewRows : kManyRows;
+  p.slots = (int)((int64_t)tokens * group / p.rows + sequences);
+  const int64_t all = (int64_t)p.slots * kv_heads;
+  const int64_t tiles = (each + p.rows - 1) / p.rows * sequences * kv_heads;     // not empty, for sequences alike
+  p.whole = (int)(all < 1 << 30 ? all : 1 << 30);
+  p.parts = 1;
+  const int64_t most = reach / (p.rows == kFewRows ? 256 : 128);
+  if (p.rows == kFewRows) {
+    const int64_t s = 1024 / tiles;
+    p.parts = (int)(s < most ? s : most);
+    if (p.parts > 128) p.parts = 128;
+    if (p.parts > 1) p.whole = 0;
+  } else {
+    // two workgroups a CU: the tiles of the last, partial round are cut so that it fills the chip
+    const int64_t round = 512, rest = tiles % round;
+    double best = 1.0;
+    for (int s = 2; s <= 16 && s <= most && rest; s++) {
+      const double t = (double)((rest * s + round - 1) / round) / s + 0.01 * s;
+      if (t < 0.95 * best) {
+        best = t;
+        p.parts = s;
+      }
+    }
+    if (p.parts > 1) p.whole = (int)(tiles - rest);
+  }
+  if (p.parts < 2) {
+    p.parts = 1;
+    p.whole = (int)(all < 1 << 30 ? all : 1 << 30);
+  }
+  for (;; p.parts--) {
+    p.bytes = p.parts > 1 ? (size_t)(all - p.whole) * p.parts * p.rows * (dim + 2) * sizeof(float) : 0;
+    if (p.bytes <= room) break;
+  }
+  return p;
 }
 
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
-  const hipError_t e = attn::launch_few(a, s);
-  if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t blocks = ((int64_t)a.tokens * a.heads + 3) / 4;
-  if (!launchable(blocks, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(k_attn_join, dim3((unsigned)blocks), dim3(256), 0, s, a);
-  return hipGetLastError();
+  const hipError_t e = a.rows == kFewRows ? attn::launch_few(a, s) : attn::launch_many(a, s);
+  if (e != hipSuccess || a.parts == 1) return e;
+  return a.rows == kFewRows ? join_dim<kFewRows>(a, s) : join_dim<kManyRows>(a, s);
 }
 
 }  // namespace svdq

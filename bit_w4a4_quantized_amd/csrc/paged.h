@@ -28,12 +28,17 @@ struct AttnArgs {
   int tokens, heads, group, qbf;             // group: query heads a cache head; qbf: q and o are bf16
   float scale;                               // times log2(e)
   const uint8_t* tree; int64_t tree_stride; int tree_width;
-  int splits;                                // of each sequence's keys
-  float* part;                               // fp32 [splits][tokens * heads][dim] sums, then [tokens * heads][splits][2]
+  // A tile is `rows` rows of a sequence and cache head; its number is slot * cache heads + head.  The first
+  // `whole` tiles take all their keys at once, the others are cut into `parts` each, joined afterwards.
+  int rows, slots, whole, parts;
+  float* part;                               // fp32 [cut tiles][parts][rows][dim] sums, then [cut tiles][rows][parts][2]
 };
-// Parts that the keys are split into when the workspace has room for them, and its bytes.
-int attn_splits(int sequences, int tokens, int heads, int kv_heads, int64_t reach);
-size_t attn_part_bytes(int splits, int tokens, int heads, int dim);
+// How a step's tiles are cut, for workspaces of at most `room` bytes.  reach: keys that the table can hold.
+struct AttnPlan {
+  int rows, slots, whole, parts;
+  size_t bytes;
+};
+AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, int64_t reach, size_t room);
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s);
 
 // The last i in [0, n) with f(i) <= target, for f that never falls; -1 if there is none.  The wave looks

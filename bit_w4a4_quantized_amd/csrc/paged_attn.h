@@ -62,10 +62,10 @@ __device__ __forceinline__ bool not_finite(const v4u& u) {
   return r;
 }
 
-// A row of bf16 queries (its pieces lie in lanes c, c + 16, c + 32, c + 48, or c and c + 32) as fp16, divided by
+// A row of bf16 queries (its pieces lie in every NEAR-th lane: 16 or 32) as fp16, divided by
 // a power of two that brings its largest into [1, 2): exact for values down to 2^-14 of the largest and
 // within 2^-25 of it below.  Returns the power.
-template <int N>
+template <int N, int NEAR>
 __device__ __forceinline__ float queries_to_f16(v4u* q) {
   float top = 0.f;
 #pragma unroll
@@ -73,7 +73,7 @@ __device__ __forceinline__ float queries_to_f16(v4u* q) {
 #pragma unroll
     for (int i = 0; i < 4; i++)
       top = fmaxf(top, fmaxf(__builtin_fabsf(bf16_f32(q[s][i] & 0xFFFFu)), __builtin_fabsf(bf16_f32(q[s][i] >> 16))));
-  top = fmaxf(top, __shfl_xor(top, 16));
+  if (NEAR == 16) top = fmaxf(top, __shfl_xor(top, 16));
   top = fmaxf(top, __shfl_xor(top, 32));
   const int e = top > 0.f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;
 #pragma unroll
@@ -96,15 +96,16 @@ __device__ __forceinline__ v4u transposed(const uint16_t* x, const uint16_t* y) 
 // A workgroup's share: rows row0 ... of a sequence (token * group + query head of the group), a cache head
 // and a part of the keys.
 struct Work {
-  int seq, head, split, s0, n, ctx, keys;    // s0: first token; n: tokens; keys: context and tokens that have a slot
+  int seq, head, split, parts, cut;          // cut: the tile's number among those that are cut
+  int s0, n, ctx, keys;                      // s0: first token; n: tokens; keys: context and tokens that have a slot
   int row0, rows;
 
   // One past the last key that any row up to `row` sees.
   __device__ __forceinline__ int last_key(const AttnArgs& a, int row) const {
     return a.tree ? keys : min(keys, ctx + min(row / a.group, n - 1) + 1);
   }
-  __device__ __forceinline__ void part(const AttnArgs& a, int kmax, int unit, int* begin, int* end) const {
-    int each = (kmax + a.splits - 1) / a.splits;
+  __device__ __forceinline__ void part(int kmax, int unit, int* begin, int* end) const {
+    int each = (kmax + parts - 1) / parts;
     each = (each + unit - 1) / unit * unit;
     *begin = (int)min((int64_t)kmax, (int64_t)split * each);
     *end = min(kmax, *begin + each);
@@ -118,16 +119,14 @@ struct Work {
   }
 };
 
-// Workgroups are numbered heads first (those of a cache head on one XCD, which share rows of the cache where a
-// sequence has several row tiles), then parts, then slots of rows.  Sequence i has the slots from
-// floor(starts[i] group / R) + i on: one more than it may need, found without a sum over the sequences.
+// The rows of a tile.  Tiles are numbered heads first (those of a cache head on one XCD, which share rows of the
+// cache where a sequence has several), then slots of rows, the last first: a chunk's last rows see the most keys.
+// Sequence i has the slots from floor(starts[i] group / R) + i on: one more than it may need, found without a
+// sum over the sequences.
 template <int R>
-__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
-  int id = blockIdx.x;
-  w.head = id % a.c.heads;
-  id /= a.c.heads;
-  w.split = id % a.splits;
-  const int slot = id / a.splits;
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) {
+  w.head = tile % a.c.heads;
+  const int slot = a.slots - 1 - tile / a.c.heads;
   auto first = [&](int i) { return (int64_t)start_of(a.b, i, a.tokens) * a.group / R + i; };
   w.seq = __builtin_amdgcn_readfirstlane(last_below(a.b.n, slot, first));
   if (w.seq < 0) return false;
@@ -137,6 +136,22 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
   const int64_t row0 = (slot - first(w.seq)) * R;
   if (row0 >= w.rows) return false;
   w.row0 = (int)row0;
+  return true;
+}
+template <int R>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
+  const int id = blockIdx.x;
+  int tile = id;
+  w.split = w.cut = 0;
+  w.parts = 1;
+  if (id >= a.whole) {
+    const int cut = a.slots * a.c.heads - a.whole, u = id - a.whole;
+    w.split = u / cut;
+    w.cut = u - w.split * cut;
+    w.parts = a.parts;
+    tile = a.whole + w.cut;
+  }
+  if (!find_tile<R>(a, tile, w)) return false;
   w.ctx = context_of(a.b, w.seq);
   const int64_t reach = (int64_t)a.b.width << a.c.shift;
   w.keys = (int)min((int64_t)w.ctx + w.n, reach);
@@ -144,25 +159,31 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
 }
 
 // Four values of a row's result: the output where the keys are whole, else this part's sums.
+template <int R>
 __device__ __forceinline__ void put(const AttnArgs& a, const Work& w, int row, int d, const v4f& o, float m, float sum) {
-  const int r = w.row0 + row, i = r / a.group, t = w.s0 + i, h = w.head * a.group + r - i * a.group;
-  if (a.splits == 1) {
+  if (w.parts == 1) {
+    const int r = w.row0 + row, i = r / a.group, t = w.s0 + i, h = w.head * a.group + r - i * a.group;
     const float f = sum == 0.f ? 0.f : 1.f / sum;      // a row that sees nothing is zeros
     uint16_t* to = static_cast<uint16_t*>(a.o) + (int64_t)t * a.o_token + (int64_t)h * a.o_head + d;
     const uint32_t x[2] = {pack16(o[0] * f, o[1] * f, a.qbf), pack16(o[2] * f, o[3] * f, a.qbf)};
     __builtin_memcpy(to, x, 8);
     return;
   }
-  const int64_t rows = (int64_t)a.tokens * a.heads, at = (int64_t)t * a.heads + h;
-  *reinterpret_cast<v4f*>(a.part + (w.split * rows + at) * a.c.dim + d) = o;
+  const int64_t cuts = a.slots * a.c.heads - a.whole;
+  *reinterpret_cast<v4f*>(a.part + ((w.cut * (int64_t)w.parts + w.split) * R + row) * a.c.dim + d) = o;
   if (d == 0) {
-    float* ml = a.part + a.splits * rows * a.c.dim + (at * a.splits + w.split) * 2;
+    float* ml = a.part + cuts * w.parts * R * a.c.dim + ((w.cut * (int64_t)R + row) * w.parts + w.split) * 2;
     ml[0] = m;
     ml[1] = sum;
   }
 }
 
+inline int64_t blocks_of(const AttnArgs& a) {
+  const int64_t tiles = (int64_t)a.slots * a.c.heads;
+  return a.whole + (tiles - a.whole) * a.parts;
+}
 hipError_t launch_few(const AttnArgs& a, hipStream_t s);
+hipError_t launch_many(const AttnArgs& a, hipStream_t s);
 
 }  // namespace attn
 }  // namespace svdq

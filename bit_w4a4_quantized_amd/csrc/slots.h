@@ -31,12 +31,15 @@ SVDQ_BOTH inline int within(int v, int most) { return v < 0 ? 0 : v > most ? mos
 SVDQ_BOTH inline int start_of(const PagedBatch& b, int i, int tokens) { return within(b.starts[i], tokens); }
 SVDQ_BOTH inline int context_of(const PagedBatch& b, int i) { return within(b.context[i], kMaxContext); }
 
-// The page of a sequence's slot, -1 if it has none.
-SVDQ_BOTH inline int page_of(const PagedBatch& b, const PagedCache& c, int seq, int slot) {
+// What the table says of a sequence's slot, -1 past its width; and that as a page, -1 where it is none.  Apart, so
+// that a kernel can look a tile ahead without waiting for the answer.
+SVDQ_BOTH inline int entry_of(const PagedBatch& b, const PagedCache& c, int seq, int slot) {
   const int col = slot >> c.shift;
-  if (col >= b.width) return -1;
-  const int id = b.table[seq * b.stride + col];
-  return (unsigned)id < (unsigned)c.pages ? id : -1;
+  return col < b.width ? b.table[seq * b.stride + col] : -1;
+}
+SVDQ_BOTH inline int as_page(const PagedCache& c, int entry) { return (unsigned)entry < (unsigned)c.pages ? entry : -1; }
+SVDQ_BOTH inline int page_of(const PagedBatch& b, const PagedCache& c, int seq, int slot) {
+  return as_page(c, entry_of(b, c, seq, slot));
 }
 
 }  // namespace svdq
