@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
   constexpr int kLoads = kPieces / 2;        // of a lane, for 32 rows of V
   constexpr int kRows = 64 / kPieces;        // of V a load instruction
   __shared__ __attribute__((aligned(16))) uint16_t lds_v[NW][32 * kV];
-  __shared__ __attribute__((aligned(16))) float lds_s[CK == C16 ? 1 : NW][3][32];    // scales of K and V, V's as they are
+  __shared__ __attribute__((aligned(16))) float lds_s[CK == C16 ? 1 : NW][2][32];    // scales of K and V
   __shared__ float lds_ml[NW][16 * NT][2];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, quad = lane >> 4;
 
@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
   }
 
   v4f acc[NT][DP / 16];
+  bool sick = false;                         // the lane has taken an infinity or NaN out of V
   float m[NT], l[NT], ref = 0.f;             // ref: what V's scales are taken relative to (8-bit caches)
 #pragma unroll
   for (int n = 0; n < NT; n++) {
@@ -150,36 +151,24 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
         for (int n = 0; n < NT; n++) st[n][t] = mfma16<BF>(kk, qf[n][s], st[n][t]);
       }
 
-    // rows of V that hold an infinity or NaN and are hidden from some row: taken out of the product below
-    uint32_t bad = 0;
-    if (masked) {
-#pragma unroll
-      for (int i = 0; i < kLoads; i++) {
-        const uint64_t b = __ballot(not_finite<BF, CK>(vr[i]));
-        if (b) {
-#pragma unroll
-          for (int r = 0; r < kRows; r++)
-            if (b >> (r * kPieces) & ((1ull << (kPieces - 1) << 1) - 1)) bad |= 1u << (i * kRows + r);
-        }
-      }
-      if (CK != C16) bad |= (uint32_t)__ballot(lane < 32 && !(__builtin_fabsf(vs) < INFINITY));
-    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();         // the last tile's reads of LDS are done
     if (CK != C16 && lane < 32) {
       lds_s[wave][0][lane] = ks;
-      lds_s[wave][1][lane] = bad >> lane & 1 ? 0.f : vs;
-      lds_s[wave][2][lane] = vs;
+      const bool off = masked && !(__builtin_fabsf(vs) < INFINITY);
+      lds_s[wave][1][lane] = off ? 0.f : vs;
+      sick = sick || off;
     }
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
       uint16_t* to = vt + (i * kRows + lane / kPieces) * kV + lane % kPieces * (CK == C16 ? 8 : 16);
-      if (CK == C16) {
-        *reinterpret_cast<v4u*>(to) = vr[i];
-      } else {
-        *reinterpret_cast<v4u*>(to) = widen<CK>(vr[i], 0);
-        *reinterpret_cast<v4u*>(to + 8) = widen<CK>(vr[i], 1);
+      v4u x[2] = {CK == C16 ? vr[i] : widen<CK>(vr[i], 0), CK == C16 ? vr[i] : widen<CK>(vr[i], 1)};
+      if (masked && CK != CI8) {             // rows that see an infinity or NaN get it at the end
+        sick = make_finite<BF>(x[0]) || sick;
+        if (CK != C16) sick = make_finite<BF>(x[1]) || sick;
       }
+      *reinterpret_cast<v4u*>(to) = x[0];
+      if (CK != C16) *reinterpret_cast<v4u*>(to + 8) = x[1];
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -265,41 +254,34 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
         pf[n][e] = CK == C16 ? pack16(z[n][2 * e], z[n][2 * e + 1], BF)
                              : pack_f16(z[n][2 * e] * (vsc[2 * e] * inv), z[n][2 * e + 1] * (vsc[2 * e + 1] * inv));
     }
-    if (bad) {                               // hidden rows keep out what 0 * infinity would bring in
-      for (uint32_t rest = bad; rest; rest &= rest - 1) {
-        const int k = __builtin_ctz(rest), e = (k >> 4) * 4 + (k & 3), from = (k >> 2 & 3) * 16 + c;
-        const float vscale = CK == C16 ? 1.f : lds_s[wave][2][k] * inv;
-#pragma unroll
-        for (int n = 0; n < NT; n++) {
-          float p = 0.f;
-          uint32_t sn = 0;
-#pragma unroll
-          for (int x = 0; x < 8; x++)
-            if (x == e) p = z[n][x], sn = seen[n] >> x & 1;
-          p = __shfl(p, from);
-          sn = __shfl((int)sn, from);
-#pragma unroll
-          for (int dt = 0; dt < DP / 16; dt++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              const uint32_t b = vt[k * kV + dt * 16 + quad * 4 + i];
-              if (sn) acc[n][dt][i] += p * ((BF ? bf16_f32(b) : f16_f32(b)) * vscale);
-            }
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      for (uint32_t rest = bad; rest; rest &= rest - 1)
-        for (int d = lane; d < DP; d += 64) vt[__builtin_ctz(rest) * kV + d] = 0;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
 #pragma unroll
     for (int dt = 0; dt < DP / 16; dt++) {
       const uint16_t* at = vt + (quad * 4 + (c >> 2)) * kV + dt * 16 + (c & 3) * 4;
       const v4u vv = transposed(at, at + 16 * kV);
 #pragma unroll
       for (int n = 0; n < NT; n++) acc[n][dt] = mfma16<BF>(vv, pf[n], acc[n][dt]);
+    }
+  }
+
+  if (__any(sick)) {                         // rare: the wave's keys one by one, each row those that it sees
+#pragma unroll 1
+    for (int key = begin; key < end; key++) {
+      if ((key - begin) / 32 % NW != wave) continue;
+      const int page = page_of(a.b, a.c, w.seq, key);
+      if (page < 0) continue;
+#pragma unroll
+      for (int n = 0; n < NT; n++) {
+        const bool sees = valid[n] && w.sees(a, tok[n], key);
+#pragma unroll
+        for (int dt = 0; dt < DP / 16; dt++) {
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const float x = infinite_value<BF, CK>(a, w, page, key, min(dt * 16 + quad * 4 + i, dim - 1));
+            acc[n][dt][i] += sees ? x : 0.f;
+          }
+          asm volatile("" ::: "memory");     // few loads at once
+        }
+      }
     }
   }
 
@@ -340,7 +322,7 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
         const float* at = reinterpret_cast<const float*>(lds_v[x]) + row * CH + ((piece ^ (row & 15)) & (kP - 1)) * 4;
         o += f * *reinterpret_cast<const v4f*>(at);
       }
-      put<16 * NT>(a, w, row, d, o, mm, sum);
+      put(dest_of<16 * NT>(a, w, row), a.qbf, d, o, mm, sum);
     }
   }
 }

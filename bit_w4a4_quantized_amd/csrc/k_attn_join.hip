@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
   }
   if (!valid) return;
   w.parts = 1;
-  put<R>(a, w, row, d, sum, m, l);
+  put(dest_of<R>(a, w, row), a.qbf, d, sum, m, l);
 }
 
 template <int R, int P>

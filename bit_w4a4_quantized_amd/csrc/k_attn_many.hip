@@ -25,6 +25,10 @@ __device__ __forceinline__ int turn_v(int row) { return DP == 64 ? (row >> 1 & 1
 
 __device__ const uint4 kNothing[1] = {};     // 16 bytes of zeros that loads of absent keys read
 
+__device__ __forceinline__ uint64_t same_in_wave(uint64_t x) {
+  return ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(x >> 32)) << 32) | (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)x);
+}
+
 // Lane l's 16 bytes at `from` to LDS at `to` + 16 l; `to` is the wave's.  Written out, because the compiler cannot
 // tell which of the two tiles a transposed read takes and would wait for the other's loads in front of it.  It has no
 // results in registers; ready() below waits for it.  Nothing else here keeps a value in m0.
@@ -33,6 +37,10 @@ __device__ const uint4 kNothing[1] = {};     // 16 bytes of zeros that loads of 
 __device__ __forceinline__ void to_lds(uint64_t from, uint16_t* to) {
   const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)to;
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(at) : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint16_t* to) {      // base: the wave's
+  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)to;
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(at) : "memory", "m0");
 }
 #pragma clang diagnostic pop
 
@@ -49,11 +57,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   constexpr uint64_t kAll = ~0ull >> (64 - BN);
   constexpr int kSteps = DP / 16;            // of the first product's contraction
   constexpr int kBlocks = DP / 32;           // results of the second
+  constexpr int kAhead = 4;
   constexpr int kPieces = CK == C16 ? DP / 8 : DP / 16;   // 16-byte pieces a row of the cache
   constexpr int kRows = 64 / kPieces;        // rows that a wave's load takes
   constexpr int kLoads = BN / 4 / kRows;     // of a wave, for its share of a tile's K, or V
   __shared__ __attribute__((aligned(16))) uint16_t k0[BN * DP], k1[BN * DP], v0[BN * DP], v1[BN * DP];
   __shared__ __attribute__((aligned(16))) float s0[2][CK == C16 ? 4 : BN], s1[2][CK == C16 ? 4 : BN];   // scales of K and V
+  __shared__ int sick;                       // some tile of V held an infinity or NaN
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, half = lane >> 5;
 
@@ -98,6 +108,24 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   // addresses as numbers: chosen without a branch
   const uint64_t kaddr = reinterpret_cast<uint64_t>(kbase), vaddr = reinterpret_cast<uint64_t>(vbase);
   const uint64_t nothing = reinterpret_cast<uint64_t>(kNothing);
+  // A tile that one page holds whole: the lane's places in it, from its first row on.  (Strides that 32 bits do not
+  // hold go the other way.)
+  const bool paged = 1 << a.c.shift >= BN && a.c.token < 1 << 24;
+  uint32_t kat[kLoads], vat[kLoads];
+  constexpr uint32_t kSkip = 0x80000000u;    // values past the head's end
+#pragma unroll
+  for (int i = 0; i < kLoads; i++) {
+    const int row = (i * 4 + wave) * kRows + lane / kPieces, p = lane % kPieces;
+    const int pk = CK == C16 ? p ^ turn_k<DP>(row) : p, pv = CK == C16 ? p ^ turn_v<DP>(row) : p;
+    const uint32_t at = (uint32_t)row * (uint32_t)a.c.token * es;
+    kat[i] = pk * (16 / es) < dim ? at + pk * 16 : kSkip;
+    vat[i] = pv * (16 / es) < dim ? at + pv * 16 : kSkip;
+  }
+  if (dim < DP) {                            // places past the head's end are never loaded: zeros for good
+    for (int i = threadIdx.x; i < BN * DP / 8; i += 256)
+      for (uint16_t* t : {k0, k1, v0, v1}) *reinterpret_cast<v4u*>(t + i * 8) = v4u{0, 0, 0, 0};
+    __syncthreads();
+  }
 
   // One tile: the lane's own key (base + lane) says where its row is; the others' come by exchange.
   auto entry_at = [&](int base) {
@@ -106,25 +134,42 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   };
   v4u kr[CK == C16 ? 1 : kLoads], vr[CK == C16 ? 1 : kLoads];      // codes on their way
   float ksr = 0.f, vsr = 0.f;
-  auto fetch = [&](int base, int page, uint16_t* kt, uint16_t* vt) {
-    const int64_t in_page = (base + lane) & ((1 << a.c.shift) - 1);
-    const int64_t off = page < 0 ? -1 : (page * a.c.page + in_page * a.c.token) * es;
-    const int lo = (int)off, hi = (int)(off >> 32);
+  auto fetch = [&](int base, int page, uint64_t live, uint16_t* kt, uint16_t* vt) {
+    const int in_page = (base + lane) & ((1 << a.c.shift) - 1);
+    if (paged && live == kAll) {
+      const int id = __builtin_amdgcn_readfirstlane(page);
+      const int64_t off = (id * a.c.page + (int64_t)(base & ((1 << a.c.shift) - 1)) * a.c.token) * es;
+      const uint64_t ktile = same_in_wave(kaddr + off), vtile = same_in_wave(vaddr + off);
 #pragma unroll
-    for (int i = 0; i < kLoads; i++) {
-      const int first = (i * 4 + wave) * kRows, row = first + lane / kPieces;
-      const int64_t o = ((int64_t)__shfl(hi, row) << 32) | (uint32_t)__shfl(lo, row);
-      if (CK == C16) {
-        const int pk = (lane % kPieces) ^ turn_k<DP>(row), pv = (lane % kPieces) ^ turn_v<DP>(row);
-        const bool there = o >= 0;
-        to_lds(there && pk * 8 < dim ? kaddr + o + pk * 16 : nothing, kt + first * DP);
-        to_lds(there && pv * 8 < dim ? vaddr + o + pv * 16 : nothing, vt + first * DP);
-      } else {
-        const int p = lane % kPieces;
-        kr[i] = vr[i] = v4u{0, 0, 0, 0};
-        if (o >= 0 && p * 16 < dim) {
-          kr[i] = *reinterpret_cast<const v4u*>(kbase + o + p * 16);
-          vr[i] = *reinterpret_cast<const v4u*>(vbase + o + p * 16);
+      for (int i = 0; i < kLoads; i++) {
+        const int first = (i * 4 + wave) * kRows;
+        if (CK == C16) {
+          if (dim == DP || kat[i] != kSkip) to_lds(ktile, kat[i], kt + first * DP);
+          if (dim == DP || vat[i] != kSkip) to_lds(vtile, vat[i], vt + first * DP);
+        } else {
+          kr[i] = vr[i] = v4u{0, 0, 0, 0};
+          if (dim == DP || kat[i] != kSkip) {
+            kr[i] = *reinterpret_cast<const v4u*>(ktile + kat[i]);
+            vr[i] = *reinterpret_cast<const v4u*>(vtile + vat[i]);
+          }
+        }
+      }
+    } else {
+      const int64_t off = page < 0 ? -1 : (page * a.c.page + in_page * a.c.token) * es;
+      const int lo = (int)off, hi = (int)(off >> 32);
+#pragma unroll
+      for (int i = 0; i < kLoads; i++) {
+        const int first = (i * 4 + wave) * kRows, row = first + lane / kPieces, p = lane % kPieces;
+        const int64_t o = ((int64_t)__shfl(hi, row) << 32) | (uint32_t)__shfl(lo, row);
+        if (CK == C16) {
+          if (kat[i] != kSkip) to_lds(o >= 0 ? kaddr + o + (p ^ turn_k<DP>(row)) * 16 : nothing, kt + first * DP);
+          if (vat[i] != kSkip) to_lds(o >= 0 ? vaddr + o + (p ^ turn_v<DP>(row)) * 16 : nothing, vt + first * DP);
+        } else {
+          kr[i] = vr[i] = v4u{0, 0, 0, 0};
+          if (o >= 0 && kat[i] != kSkip) {
+            kr[i] = *reinterpret_cast<const v4u*>(kbase + o + p * 16);
+            vr[i] = *reinterpret_cast<const v4u*>(vbase + o + p * 16);
+          }
         }
       }
     }
@@ -153,21 +198,69 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       sc[1][lane] = vsr;
     }
   };
+  // Tiles that some row does not see whole: V without infinities and NaN (rows that see one get it at the end).
+  auto clean = [&](uint16_t* vt, float (*sc)[CK == C16 ? 4 : BN]) {
+    bool found = false;
+    if (CK != CI8) {
+#pragma unroll 1
+      for (int i = threadIdx.x; i < BN * DP / 8; i += 256) {
+        v4u x = *reinterpret_cast<const v4u*>(vt + i * 8);
+        if (make_finite<BF>(x)) {
+          *reinterpret_cast<v4u*>(vt + i * 8) = x;
+          found = true;
+        }
+      }
+    }
+    if (CK != C16 && threadIdx.x < BN && !(__builtin_fabsf(sc[1][CK == C16 ? 0 : threadIdx.x]) < INFINITY)) {
+      sc[1][CK == C16 ? 0 : threadIdx.x] = 0.f;
+      found = true;
+    }
+    if (found) sick = 1;
+    __syncthreads();
+  };
+  // The lane's places in a tile: the first product's piece of row c in each step (32 rows on the same turn), and the
+  // second's rows of V, 4 * half + (lane % 16) / 4 and so on (every 4 rows the same).
+  int kof[kSteps], vof[kBlocks];
+#pragma unroll
+  for (int s = 0; s < kSteps; s++) kof[s] = c * DP + ((2 * s + half) ^ turn_k<DP>(c)) * 8;
+#pragma unroll
+  for (int d = 0; d < kBlocks; d++) {
+    const int row = 4 * half + ((lane & 15) >> 2), at = d * 32 + (lane >> 4 & 1) * 16 + (lane & 3) * 4;
+    vof[d] = row * DP + ((at >> 3) ^ turn_v<DP>(row)) * 8 + (at & 7);
+  }
 
-  auto compute = [&](int base, uint64_t live, const uint16_t* kt, const uint16_t* vt, const float (*sc)[CK == C16 ? 4 : BN]) {
+  auto compute = [&](int base, uint64_t live, const uint16_t* kt, const uint16_t* vt,
+                     const float (*sc)[CK == C16 ? 4 : BN]) {
     v16f st[NB];
 #pragma unroll
     for (int b = 0; b < NB; b++)
 #pragma unroll
       for (int i = 0; i < 16; i++) st[b][i] = 0.f;
+    // The order is written out (the compiler's own waits for each read in front of the product that takes it): reads
+    // of K run kAhead steps ahead, the first sixteen rows of V are on their way while the powers' reference is found.
+    auto read_k = [&](int s, int b) { return *reinterpret_cast<const v4u*>(kt + kof[s] + b * 32 * DP); };
+    auto read_v = [&](int u, int d) {
+      const uint16_t* x = vt + vof[d] + u * 16 * DP;
+      return transposed(x, x + 8 * DP);
+    };
+    v4u kf[kAhead][NB], vf[2][kBlocks], pf[2];
 #pragma unroll
-    for (int s = 0; s < kSteps; s++)
+    for (int s = 0; s < kAhead; s++)
 #pragma unroll
-      for (int b = 0; b < NB; b++) {
-        const int row = 32 * b + c;
-        const v4u kk = *reinterpret_cast<const v4u*>(kt + row * DP + ((2 * s + half) ^ turn_k<DP>(row)) * 8);
-        st[b] = mfma32<BF>(kk, qf[s], st[b]);
+      for (int b = 0; b < NB; b++) kf[s][b] = read_k(s, b);
+#pragma unroll
+    for (int s = 0; s < kSteps; s++) {
+#pragma unroll
+      for (int b = 0; b < NB; b++) st[b] = mfma32<BF>(kf[s % kAhead][b], qf[s], st[b]);
+      if (s + kAhead < kSteps) {
+#pragma unroll
+        for (int b = 0; b < NB; b++) kf[s % kAhead][b] = read_k(s + kAhead, b);
       }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int d = 0; d < kBlocks; d++) vf[0][d] = read_v(0, d);
+    __builtin_amdgcn_sched_barrier(0);
     // logits in powers of two
     if (CK != C16) {
 #pragma unroll
@@ -180,11 +273,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
         }
     }
     const int sure = a.tree ? w.ctx : w.ctx + wave_first + 1;      // keys below it are seen by all of the wave's rows
-    const bool masked = base + BN > sure || live != kAll;          // the same in every lane
-    uint32_t seen = ~0u;
-    uint64_t bad = 0;
-    if (masked) {
-      seen = 0;
+    if (base + BN > sure || live != kAll) {  // the same in every lane
+      uint32_t seen = 0;
 #pragma unroll 1
       for (int e = 0; e < 16 * NB; e++) {
         const int k = (e >> 2) * 8 + 4 * half + (e & 3);
@@ -192,17 +282,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       }
 #pragma unroll
       for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = seen >> e & 1 ? st[e >> 4][e & 15] : -INFINITY;
-      // rows of V that hold an infinity or NaN: the product below would bring 0 * infinity to rows that do not see them
-      bool sick = CK != C16 && !(__builtin_fabsf(sc[1][lane & (CK == C16 ? 3 : BN - 1)]) < INFINITY);
-      if (CK != CI8)
-#pragma unroll 1
-        for (int p = 0; p < DP / 8; p++) sick = sick || not_finite<BF, C16>(*reinterpret_cast<const v4u*>(vt + (lane & (BN - 1)) * DP + p * 8));
-      bad = __ballot(sick);
     }
-    auto scale_v = [&](int e) {              // of the lane's e-th key
-      const float x = sc[1][(e >> 2) * 8 + 4 * half + (e & 3)];
-      return masked && !(__builtin_fabsf(x) < INFINITY) ? 0.f : x;
-    };
+    auto scale_v = [&](int e) { return sc[1][(e >> 2) * 8 + 4 * half + (e & 3)]; };      // of the lane's e-th key
     // the row's reference moves only when a logit passes it by kSlack (k_attn_few)
     float top = -INFINITY, vtop = 0.f;
 #pragma unroll
@@ -231,53 +312,37 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       for (int d = 0; d < kBlocks; d++) acc[d] *= f * back;
     }
     const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int e = 0; e < 16 * NB; e++) {
-      const float z = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], coef, -mu));
-      st[e >> 4][e & 15] = z;
-      l += z;
-    }
     const float inv = CK != C16 && ref > 0.f ? 1.f / ref : 0.f;
-    if (bad == 0) {
-      // rounded to 16 bits, with V's scales relative to ref, as in k_attn_few
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+    // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to ref, as in k_attn_few.
+    auto power = [&](int u, int x) {
+      const int e = 8 * u + 2 * x;
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], coef, -mu));
+      const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][(e & 15) + 1], coef, -mu));
+      part[x] += p + q;
+      pf[u & 1][x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (scale_v(e) * inv), q * (scale_v(e + 1) * inv));
+    };
 #pragma unroll
-      for (int u = 0; u < 2 * NB; u++) {
-        v4u pf;
+    for (int x = 0; x < 4; x++) power(0, x);
+    // the next sixteen keys' powers and rows of V between the products of these
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-          const int e = 8 * u + 2 * x;
-          const float p = st[e >> 4][e & 15], q = st[e >> 4][(e & 15) + 1];
-          pf[x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (scale_v(e) * inv), q * (scale_v(e + 1) * inv));
-        }
+    for (int u = 0; u < 2 * NB; u++) {
+      if (u + 1 < 2 * NB) {
 #pragma unroll
-        for (int d = 0; d < kBlocks; d++) {
-          const int row = 16 * u + 4 * half + ((lane & 15) >> 2);
-          const int at = d * 32 + (lane >> 4 & 1) * 16 + (lane & 3) * 4;
-          const uint16_t* x = vt + row * DP + ((at >> 3) ^ turn_v<DP>(row)) * 8 + (at & 7);
-          acc[d] = mfma32<BF>(transposed(x, x + 8 * DP), pf, acc[d]);      // 8 rows on: the same turn
-        }
+        for (int d = 0; d < kBlocks; d++) vf[(u + 1) & 1][d] = read_v(u + 1, d);
       }
-    } else {                                 // key by key, each row those that it sees
-#pragma unroll 1
-      for (int k = 0; k < BN; k++) {
-        const int e = (k >> 3) * 4 + (k & 3), from = (k >> 2 & 1) * 32 + c;
-        float p = 0.f;
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int x = 0; x < 16 * NB; x++)
-          if (x == e) p = st[x >> 4][x & 15];
-        p = __shfl(p, from);
-        const bool sees = __shfl((int)(seen >> e & 1), from);
-        const float vs = CK == C16 ? 1.f : sc[1][k] * inv;
+      for (int d = 0; d < kBlocks; d++) {
+        acc[d] = mfma32<BF>(vf[u & 1][d], pf[u & 1], acc[d]);
+        if (u + 1 < 2 * NB) {
 #pragma unroll
-        for (int d = 0; d < kBlocks; d++)
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            const int at = d * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
-            const uint32_t b = vt[k * DP + ((at >> 3) ^ turn_v<DP>(k)) * 8 + (at & 7)];
-            if (sees) acc[d][i] += p * ((BF ? bf16_f32(b) : f16_f32(b)) * vs);
-          }
+          for (int x = 4 * d / kBlocks; x < 4 * (d + 1) / kBlocks; x++) power(u + 1, x);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+    l += (part[0] + part[1]) + (part[2] + part[3]);
   };
 
   // ring of two tiles
@@ -287,10 +352,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  // keys below it are seen by all of the workgroup's rows
+  const int all_see = a.tree ? w.ctx : w.ctx + w.row0 / a.group + 1;
+  if (threadIdx.x == 0) sick = 0;            // before the first tile's barrier
   if (begin < end) {
     const int page = as_page(a.c, entry_at(begin));
     uint64_t live = __ballot(page >= 0);
-    fetch(begin, page, k0, v0);
+    fetch(begin, page, live, k0, v0);
     int entry = entry_at(begin + BN);
     auto turn = [&](int base, uint16_t* kt, uint16_t* vt, auto* st, uint16_t* kn, uint16_t* vn) {
       settle(kt, vt, st);
@@ -298,9 +366,10 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       const int page = as_page(a.c, entry);
       const uint64_t next = __ballot(page >= 0);
       if (base + BN < end) {
-        fetch(base + BN, page, kn, vn);
+        fetch(base + BN, page, next, kn, vn);
         entry = entry_at(base + 2 * BN);
       }
+      if (base + BN > all_see) clean(vt, st);            // the same in every wave
       // a wave whose rows see none of the tile has nothing to do (a chunk's later keys)
       if (a.tree || base <= w.ctx + wave_last) compute(base, live, kt, vt, st);
       live = next;
@@ -313,14 +382,36 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
 
   l += __shfl_xor(l, 32);
   const float unit = CK == C16 ? 1.f : ref;
+  if (begin < end) {
+    __syncthreads();
+    if (sick) {                              // rare: key by key, each row those that it sees
+#pragma unroll 1
+      for (int key = max(begin, all_see / BN * BN); key < end; key++) {
+        const int page = page_of(a.b, a.c, w.seq, key);
+        if (page < 0) continue;
+        const bool sees = valid && w.sees(a, tok, key);
+#pragma unroll
+        for (int d = 0; d < kBlocks; d++) {
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            const int at = d * 32 + 8 * (i >> 2) + 4 * half + (i & 3);
+            const float x = infinite_value<BF, CK>(a, w, page, key, min(at, dim - 1));
+            acc[d][i] += sees ? x : 0.f;
+          }
+          asm volatile("" ::: "memory");     // few loads at once
+        }
+      }
+    }
+  }
   if (!valid) return;
+  const Dest to = dest_of<128>(a, w, 32 * wave + c);
 #pragma unroll
   for (int d = 0; d < kBlocks; d++)
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const int at = d * 32 + 8 * g + 4 * half;
       if (at < dim)
-        put<128>(a, w, 32 * wave + c, at, v4f{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]} * unit, m, l);
+        put(to, a.qbf, at, v4f{acc[d][4 * g], acc[d][4 * g + 1], acc[d][4 * g + 2], acc[d][4 * g + 3]} * unit, m, l);
     }
 }
 

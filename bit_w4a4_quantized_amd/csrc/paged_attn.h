@@ -44,22 +44,28 @@ __device__ __forceinline__ v4u widen(const v4u& u, int second) {
   return r;
 }
 
-// Whether a piece of the cache holds an infinity or NaN.
-template <bool BF, int CK>
-__device__ __forceinline__ bool not_finite(const v4u& u) {
-  if (CK == CI8) return false;
+// A piece of V (16-bit values) without its infinities and NaN, which 0 * infinity would bring to rows that do not
+// see them; whether there were any.
+template <bool BF>
+__device__ __forceinline__ bool make_finite(v4u& u) {
+  constexpr uint32_t e = BF ? 0x7F80u : 0x7C00u;
   bool r = false;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    if (CK == CE4) {
-#pragma unroll
-      for (int b = 0; b < 4; b++) r = r || (u[i] >> (8 * b) & 0x7Fu) == 0x7Fu;
-    } else {
-      constexpr uint32_t e = BF ? 0x7F80u : 0x7C00u;
-      r = r || (u[i] & e) == e || (u[i] >> 16 & e) == e;
-    }
+    const bool lo = (u[i] & e) == e, hi = (u[i] >> 16 & e) == e;
+    u[i] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+    r = r || lo || hi;
   }
   return r;
+}
+
+// A value of a row of the cache, without its scale.
+template <bool BF, int CK>
+__device__ __forceinline__ float one_value(const uint8_t* row, int at) {
+  if (CK == CI8) return (float)reinterpret_cast<const int8_t*>(row)[at];
+  if (CK == CE4) return __builtin_amdgcn_cvt_f32_fp8((int)row[at], 0);
+  const uint32_t b = reinterpret_cast<const uint16_t*>(row)[at];
+  return BF ? bf16_f32(b) : f16_f32(b);
 }
 
 // A row of bf16 queries (its pieces lie in every NEAR-th lane: 16 or 32) as fp16, divided by
@@ -158,23 +164,45 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
   return true;
 }
 
-// Four values of a row's result: the output where the keys are whole, else this part's sums.
+// A value of V of an existing slot, where it is an infinity or NaN (with its scale), else 0: what make_finite took
+// from the rows that do see it.
+template <bool BF, int CK>
+__device__ __forceinline__ float infinite_value(const AttnArgs& a, const Work& w, int page, int slot, int d) {
+  const int64_t in_page = slot & ((1 << a.c.shift) - 1);
+  const int64_t at = page * a.c.page + in_page * a.c.token + w.head * a.c.head;
+  float x = one_value<BF, CK>(static_cast<const uint8_t*>(a.c.v) + at * (CK == C16 ? 2 : 1), d);
+  if (CK != C16) x *= a.c.vs[page * a.c.spage + in_page * a.c.stoken + w.head * a.c.shead];
+  return __builtin_fabsf(x) < INFINITY ? 0.f : x;
+}
+
+// Where a row's result goes: the output where the tile has all its keys, else this part's sums.
+struct Dest {
+  uint16_t* out;
+  float* sums;
+  float* ml;
+};
 template <int R>
-__device__ __forceinline__ void put(const AttnArgs& a, const Work& w, int row, int d, const v4f& o, float m, float sum) {
+__device__ __forceinline__ Dest dest_of(const AttnArgs& a, const Work& w, int row) {
   if (w.parts == 1) {
     const int r = w.row0 + row, i = r / a.group, t = w.s0 + i, h = w.head * a.group + r - i * a.group;
+    return {static_cast<uint16_t*>(a.o) + (int64_t)t * a.o_token + (int64_t)h * a.o_head, nullptr, nullptr};
+  }
+  const int64_t cuts = (int64_t)a.slots * a.c.heads - a.whole;
+  return {nullptr, a.part + ((w.cut * (int64_t)w.parts + w.split) * R + row) * a.c.dim,
+          a.part + cuts * w.parts * R * a.c.dim + ((w.cut * (int64_t)R + row) * w.parts + w.split) * 2};
+}
+// Four of its values, from d on, with the row's maximum and sum.
+__device__ __forceinline__ void put(const Dest& to, bool bf, int d, const v4f& o, float m, float sum) {
+  if (to.out) {
     const float f = sum == 0.f ? 0.f : 1.f / sum;      // a row that sees nothing is zeros
-    uint16_t* to = static_cast<uint16_t*>(a.o) + (int64_t)t * a.o_token + (int64_t)h * a.o_head + d;
-    const uint32_t x[2] = {pack16(o[0] * f, o[1] * f, a.qbf), pack16(o[2] * f, o[3] * f, a.qbf)};
-    __builtin_memcpy(to, x, 8);
+    const uint32_t x[2] = {pack16(o[0] * f, o[1] * f, bf), pack16(o[2] * f, o[3] * f, bf)};
+    __builtin_memcpy(to.out + d, x, 8);
     return;
   }
-  const int64_t cuts = a.slots * a.c.heads - a.whole;
-  *reinterpret_cast<v4f*>(a.part + ((w.cut * (int64_t)w.parts + w.split) * R + row) * a.c.dim + d) = o;
+  *reinterpret_cast<v4f*>(to.sums + d) = o;
   if (d == 0) {
-    float* ml = a.part + cuts * w.parts * R * a.c.dim + ((w.cut * (int64_t)R + row) * w.parts + w.split) * 2;
-    ml[0] = m;
-    ml[1] = sum;
+    to.ml[0] = m;
+    to.ml[1] = sum;
   }
 }
 
