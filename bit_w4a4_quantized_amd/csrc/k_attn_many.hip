@@ -19,7 +19,7 @@ using namespace attn;
 
 // Where the piece p of a row lies in its row.
 template <int DP>
-__device__ __forceinline__ int turn_k(int row) { return DP == 64 ? (row >> 1) & 7 : row & 15; }
+__device__ __forceinline__ int turn_k(int row) { return DP == 64 ? (row >> 1) & 7 : DP == 128 ? row & 15 : row & 7; }
 template <int DP>
 __device__ __forceinline__ int turn_v(int row) { return DP == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
 
@@ -38,8 +38,7 @@ __device__ __forceinline__ void to_lds(uint64_t from, uint16_t* to) {
   const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)to;
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(at) : "memory", "m0");
 }
-__device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint16_t* to) {      // base: the wave's
-  const uint32_t at = (uint32_t)(uintptr_t)(lds_void*)to;
+__device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at) {       // base: the wave's
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(at) : "memory", "m0");
 }
 #pragma clang diagnostic pop
@@ -61,7 +60,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   constexpr int kPieces = CK == C16 ? DP / 8 : DP / 16;   // 16-byte pieces a row of the cache
   constexpr int kRows = 64 / kPieces;        // rows that a wave's load takes
   constexpr int kLoads = BN / 4 / kRows;     // of a wave, for its share of a tile's K, or V
-  __shared__ __attribute__((aligned(16))) uint16_t k0[BN * DP], k1[BN * DP], v0[BN * DP], v1[BN * DP];
+  __shared__ __attribute__((aligned(16))) uint16_t tiles[4 * BN * DP];     // K, V and the other tile's
   __shared__ __attribute__((aligned(16))) float s0[2][CK == C16 ? 4 : BN], s1[2][CK == C16 ? 4 : BN];   // scales of K and V
   __shared__ int sick;                       // some tile of V held an infinity or NaN
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -108,85 +107,127 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   // addresses as numbers: chosen without a branch
   const uint64_t kaddr = reinterpret_cast<uint64_t>(kbase), vaddr = reinterpret_cast<uint64_t>(vbase);
   const uint64_t nothing = reinterpret_cast<uint64_t>(kNothing);
-  // A tile that one page holds whole: the lane's places in it, from its first row on.  (Strides that 32 bits do not
-  // hold go the other way.)
-  const bool paged = 1 << a.c.shift >= BN && a.c.token < 1 << 24;
-  uint32_t kat[kLoads], vat[kLoads];
-  constexpr uint32_t kSkip = 0x80000000u;    // values past the head's end
-#pragma unroll
-  for (int i = 0; i < kLoads; i++) {
-    const int row = (i * 4 + wave) * kRows + lane / kPieces, p = lane % kPieces;
-    const int pk = CK == C16 ? p ^ turn_k<DP>(row) : p, pv = CK == C16 ? p ^ turn_v<DP>(row) : p;
-    const uint32_t at = (uint32_t)row * (uint32_t)a.c.token * es;
-    kat[i] = pk * (16 / es) < dim ? at + pk * 16 : kSkip;
-    vat[i] = pv * (16 / es) < dim ? at + pv * 16 : kSkip;
-  }
+  // A load's rows are first_row(i) + lane / kPieces.  Their turns do not depend on i, so that where one page holds a
+  // load's rows the lane's place behind the first of them is the same for all loads and tiles.  (Strides past
+  // 32 bits, and pages of fewer rows, go the slow way.)
+  auto first_row = [&](int i) { return (i * 4 + wave) * kRows; };
+  const int row_in = lane / kPieces, piece = lane % kPieces;
+  const int pk = CK == C16 ? piece ^ turn_k<DP>(first_row(0) + row_in) : piece;
+  const int pv = CK == C16 ? piece ^ turn_v<DP>(first_row(0) + row_in) : piece;
+  const bool in_k = pk * (16 / es) < dim, in_v = pv * (16 / es) < dim;     // not past the head's end
+  const uint32_t page_bytes = (uint32_t)(a.c.page * es), token_bytes = (uint32_t)(a.c.token * es);
+  const uint32_t kat = row_in * token_bytes + pk * 16, vat = row_in * token_bytes + pv * 16;
+  const int page_size = 1 << a.c.shift, page_mask = page_size - 1;
+  const bool steady = page_size >= kRows && a.c.page < (int64_t)1 << 31 && a.c.token < 1 << 24;
   if (dim < DP) {                            // places past the head's end are never loaded: zeros for good
-    for (int i = threadIdx.x; i < BN * DP / 8; i += 256)
-      for (uint16_t* t : {k0, k1, v0, v1}) *reinterpret_cast<v4u*>(t + i * 8) = v4u{0, 0, 0, 0};
+    for (int i = threadIdx.x; i < 4 * BN * DP / 8; i += 256) *reinterpret_cast<v4u*>(tiles + i * 8) = v4u{0, 0, 0, 0};
     __syncthreads();
   }
 
-  // One tile: the lane's own key (base + lane) says where its row is; the others' come by exchange.
-  auto entry_at = [&](int base) {
-    const int key = base + lane;
-    return lane < BN && key < end ? entry_of(a.b, a.c, w.seq, key) : -1;
-  };
   v4u kr[CK == C16 ? 1 : kLoads], vr[CK == C16 ? 1 : kLoads];      // codes on their way
   float ksr = 0.f, vsr = 0.f;
-  auto fetch = [&](int base, int page, uint64_t live, uint16_t* kt, uint16_t* vt) {
-    const int in_page = (base + lane) & ((1 << a.c.shift) - 1);
-    if (paged && live == kAll) {
-      const int id = __builtin_amdgcn_readfirstlane(page);
-      const int64_t off = (id * a.c.page + (int64_t)(base & ((1 << a.c.shift) - 1)) * a.c.token) * es;
-      const uint64_t ktile = same_in_wave(kaddr + off), vtile = same_in_wave(vaddr + off);
+  // The pages of a tile's loads, asked for a tile ahead: all of its keys are there, and the wave's loads have one
+  // page each.  The table does not change while a kernel runs.
+  typedef __attribute__((address_space(4))) const int const_int;
+  const_int* table = (const_int*)(uintptr_t)(a.b.table + w.seq * a.b.stride);
+  int ids[kLoads];
+  auto look = [&](int base) {
+    if (!steady || base + BN > end) return;
+    if (page_size >= BN) {
+      const int id = table[base >> a.c.shift];
 #pragma unroll
-      for (int i = 0; i < kLoads; i++) {
-        const int first = (i * 4 + wave) * kRows;
-        if (CK == C16) {
-          if (dim == DP || kat[i] != kSkip) to_lds(ktile, kat[i], kt + first * DP);
-          if (dim == DP || vat[i] != kSkip) to_lds(vtile, vat[i], vt + first * DP);
-        } else {
-          kr[i] = vr[i] = v4u{0, 0, 0, 0};
-          if (dim == DP || kat[i] != kSkip) {
-            kr[i] = *reinterpret_cast<const v4u*>(ktile + kat[i]);
-            vr[i] = *reinterpret_cast<const v4u*>(vtile + vat[i]);
-          }
-        }
-      }
+      for (int i = 0; i < kLoads; i++) ids[i] = id;
     } else {
-      const int64_t off = page < 0 ? -1 : (page * a.c.page + in_page * a.c.token) * es;
-      const int lo = (int)off, hi = (int)(off >> 32);
 #pragma unroll
-      for (int i = 0; i < kLoads; i++) {
-        const int first = (i * 4 + wave) * kRows, row = first + lane / kPieces, p = lane % kPieces;
-        const int64_t o = ((int64_t)__shfl(hi, row) << 32) | (uint32_t)__shfl(lo, row);
-        if (CK == C16) {
-          if (kat[i] != kSkip) to_lds(o >= 0 ? kaddr + o + (p ^ turn_k<DP>(row)) * 16 : nothing, kt + first * DP);
-          if (vat[i] != kSkip) to_lds(o >= 0 ? vaddr + o + (p ^ turn_v<DP>(row)) * 16 : nothing, vt + first * DP);
-        } else {
-          kr[i] = vr[i] = v4u{0, 0, 0, 0};
-          if (o >= 0 && kat[i] != kSkip) {
-            kr[i] = *reinterpret_cast<const v4u*>(kbase + o + p * 16);
-            vr[i] = *reinterpret_cast<const v4u*>(vbase + o + p * 16);
-          }
-        }
-      }
+      for (int i = 0; i < kLoads; i++) ids[i] = table[(base + first_row(i)) >> a.c.shift];
     }
+  };
+  auto fetch_scales = [&](int base, int page) {      // of the lane's key
     if (CK != C16 && wave == 0) {
       ksr = vsr = 0.f;
-      if (page >= 0) {
-        const int64_t so = page * a.c.spage + in_page * a.c.stoken + w.head * a.c.shead;
+      if (lane < BN && page >= 0) {
+        const int64_t so = page * a.c.spage + (int64_t)((base + lane) & page_mask) * a.c.stoken + w.head * a.c.shead;
         ksr = a.c.ks[so];
         vsr = a.c.vs[so];
       }
     }
   };
+  // Whether `look` has found a page for each of the wave's loads, and the offsets of their first rows.
+  uint64_t at[kLoads];
+  auto easy = [&](int base) {
+    if (!steady || base + BN > end) return false;
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) all = all && (uint32_t)ids[i] < (uint32_t)a.c.pages;
+    if (page_size >= BN) {
+      at[0] = (uint64_t)(uint32_t)ids[0] * page_bytes + (uint64_t)(uint32_t)((base + first_row(0)) & page_mask) * token_bytes;
+#pragma unroll
+      for (int i = 1; i < kLoads; i++) at[i] = at[i - 1] + (uint64_t)4 * kRows * token_bytes;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; i++)
+        at[i] = (uint64_t)(uint32_t)ids[i] * page_bytes + (uint64_t)(uint32_t)((base + first_row(i)) & page_mask) * token_bytes;
+    }
+    return all;
+  };
+  const uint32_t wave_lds = (uint32_t)(uintptr_t)(lds_void*)(tiles + first_row(0) * DP);
+  auto load_k = [&](int i, int off) { to_lds(same_in_wave(kaddr + at[i]), kat, wave_lds + (off + i * 4 * kRows * DP) * 2); };
+  auto load_v = [&](int i, int off) { to_lds(same_in_wave(vaddr + at[i]), vat, wave_lds + (off + i * 4 * kRows * DP) * 2); };
+  // Loads a tile; which of its keys there are.
+  auto fetch = [&](int base, bool is_easy, int k_off, int v_off) -> uint64_t {
+    if (is_easy) {
+      if (CK == C16) {
+        if (in_k) {
+#pragma unroll
+          for (int i = 0; i < kLoads; i++) load_k(i, k_off);
+        }
+        if (in_v) {
+#pragma unroll
+          for (int i = 0; i < kLoads; i++) load_v(i, v_off);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; i++) {
+          kr[i] = vr[i] = v4u{0, 0, 0, 0};
+          if (in_k) {
+            kr[i] = *reinterpret_cast<const v4u*>(kbase + at[i] + kat);
+            vr[i] = *reinterpret_cast<const v4u*>(vbase + at[i] + vat);
+          }
+        }
+        int page = ids[0];
+        if (page_size < BN) page = page_of(a.b, a.c, w.seq, min(base + lane, end - 1));
+        fetch_scales(base, page);
+      }
+      return kAll;
+    }
+    uint16_t *kt = tiles + k_off, *vt = tiles + v_off;
+    // the lane's own key (base + lane) says where its row is; the others' come by exchange
+    const int key = base + lane, page = lane < BN && key < end ? page_of(a.b, a.c, w.seq, key) : -1;
+    const int64_t off = page < 0 ? -1 : (page * a.c.page + (int64_t)(key & page_mask) * a.c.token) * es;
+    const int lo = (int)off, hi = (int)(off >> 32);
+#pragma unroll
+    for (int i = 0; i < kLoads; i++) {
+      const int row = first_row(i) + row_in;
+      const int64_t o = ((int64_t)__shfl(hi, row) << 32) | (uint32_t)__shfl(lo, row);
+      if (CK == C16) {
+        if (in_k) to_lds(o >= 0 ? kaddr + o + pk * 16 : nothing, kt + first_row(i) * DP);
+        if (in_v) to_lds(o >= 0 ? vaddr + o + pv * 16 : nothing, vt + first_row(i) * DP);
+      } else {
+        kr[i] = vr[i] = v4u{0, 0, 0, 0};
+        if (o >= 0 && in_k) {
+          kr[i] = *reinterpret_cast<const v4u*>(kbase + o + piece * 16);
+          vr[i] = *reinterpret_cast<const v4u*>(vbase + o + piece * 16);
+        }
+      }
+    }
+    fetch_scales(base, page);
+    return __ballot(page >= 0);
+  };
   auto settle = [&](uint16_t* kt, uint16_t* vt, float (*sc)[CK == C16 ? 4 : BN]) {      // codes to LDS
     if (CK == C16) return;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
-      const int row = (i * 4 + wave) * kRows + lane / kPieces, p = 2 * (lane % kPieces);
+      const int row = first_row(i) + row_in, p = 2 * piece;
 #pragma unroll
       for (int x = 0; x < 2; x++) {
         *reinterpret_cast<v4u*>(kt + row * DP + ((p + x) ^ turn_k<DP>(row)) * 8) = widen<CK>(kr[i], x);
@@ -229,7 +270,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     vof[d] = row * DP + ((at >> 3) ^ turn_v<DP>(row)) * 8 + (at & 7);
   }
 
-  auto compute = [&](int base, uint64_t live, const uint16_t* kt, const uint16_t* vt,
+  auto compute = [&](int base, uint64_t live, const uint16_t* kt, const uint16_t* vt, bool loads, int then,
                      const float (*sc)[CK == C16 ? 4 : BN]) {
     v16f st[NB];
 #pragma unroll
@@ -243,20 +284,35 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       const uint16_t* x = vt + vof[d] + u * 16 * DP;
       return transposed(x, x + 8 * DP);
     };
-    v4u kf[kAhead][NB], vf[2][kBlocks], pf[2];
+    v4u vf[2][kBlocks], pf[2];
+    auto first_product = [&](auto between) {
+      v4u kf[kAhead][NB];
 #pragma unroll
-    for (int s = 0; s < kAhead; s++)
+      for (int s = 0; s < kAhead; s++)
 #pragma unroll
-      for (int b = 0; b < NB; b++) kf[s][b] = read_k(s, b);
+        for (int b = 0; b < NB; b++) kf[s][b] = read_k(s, b);
 #pragma unroll
-    for (int s = 0; s < kSteps; s++) {
+      for (int s = 0; s < kSteps; s++) {
 #pragma unroll
-      for (int b = 0; b < NB; b++) st[b] = mfma32<BF>(kf[s % kAhead][b], qf[s], st[b]);
-      if (s + kAhead < kSteps) {
+        for (int b = 0; b < NB; b++) st[b] = mfma32<BF>(kf[s % kAhead][b], qf[s], st[b]);
+        if (s + kAhead < kSteps) {
 #pragma unroll
-        for (int b = 0; b < NB; b++) kf[s % kAhead][b] = read_k(s + kAhead, b);
+          for (int b = 0; b < NB; b++) kf[s % kAhead][b] = read_k(s + kAhead, b);
+        }
+        between(s);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr int kEach = kSteps / (2 * kLoads) > 0 ? kSteps / (2 * kLoads) : 1;
+    if (CK == C16 && loads) {                // the next tile's loads go out between the products
+      first_product([&](int s) {
+        if (s % kEach == 0 && s / kEach < 2 * kLoads) {
+          if (s / kEach % 2 == 0) load_k(s / kEach / 2, then);
+          else load_v(s / kEach / 2, then + BN * DP);
+        }
+      });
+    } else {
+      first_product([](int) {});
     }
 #pragma unroll
     for (int d = 0; d < kBlocks; d++) vf[0][d] = read_v(0, d);
@@ -356,27 +412,28 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   const int all_see = a.tree ? w.ctx : w.ctx + w.row0 / a.group + 1;
   if (threadIdx.x == 0) sick = 0;            // before the first tile's barrier
   if (begin < end) {
-    const int page = as_page(a.c, entry_at(begin));
-    uint64_t live = __ballot(page >= 0);
-    fetch(begin, page, live, k0, v0);
-    int entry = entry_at(begin + BN);
-    auto turn = [&](int base, uint16_t* kt, uint16_t* vt, auto* st, uint16_t* kn, uint16_t* vn) {
+    constexpr int kTile = BN * DP;
+    look(begin);
+    uint64_t live = fetch(begin, easy(begin), 0, kTile);
+    look(begin + BN);
+    auto turn = [&](int base, int now, int then, auto* st) {     // places of this tile and of the next
+      uint16_t *kt = tiles + now, *vt = tiles + now + kTile;
       settle(kt, vt, st);
       ready();
-      const int page = as_page(a.c, entry);
-      const uint64_t next = __ballot(page >= 0);
-      if (base + BN < end) {
-        fetch(base + BN, page, next, kn, vn);
-        entry = entry_at(base + 2 * BN);
-      }
-      if (base + BN > all_see) clean(vt, st);            // the same in every wave
+      const bool more = base + BN < end, next_easy = more && easy(base + BN);
       // a wave whose rows see none of the tile has nothing to do (a chunk's later keys)
-      if (a.tree || base <= w.ctx + wave_last) compute(base, live, kt, vt, st);
+      const bool works = a.tree || base <= w.ctx + wave_last, checks = base + BN > all_see;
+      const bool loads = CK == C16 && dim == DP && next_easy && works && !checks;
+      uint64_t next = kAll;
+      if (more && !loads) next = fetch(base + BN, next_easy, then, then + kTile);
+      if (checks) clean(vt, st);             // the same in every wave
+      if (works) compute(base, live, kt, vt, loads, then, st);
+      if (more) look(base + 2 * BN);
       live = next;
     };
     for (int base = begin; base < end; base += 2 * BN) {
-      turn(base, k0, v0, s0, k1, v1);
-      if (base + BN < end) turn(base + BN, k1, v1, s1, k0, v0);
+      turn(base, 0, 2 * kTile, s0);
+      if (base + BN < end) turn(base + BN, 2 * kTile, 0, s1);
     }
   }
 
