@@ -17,23 +17,43 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
   const int per = 256 / P / deep;            // rows a workgroup
   const int g = threadIdx.x / P, lane = threadIdx.x % P, row_in = g / deep, way = g % deep;
   const int chunks = R / per, cut = blockIdx.x / chunks, row = (int)(blockIdx.x % chunks) * per + row_in;
-  Work w;
-  if (!find_tile<R>(a, a.whole + cut, w)) return;                 // the whole workgroup
   const int dim = a.c.dim, d = lane * 4, parts = a.parts;
-  const bool valid = w.row0 + row < w.rows && d < dim;
   const int64_t cuts = (int64_t)a.slots * a.c.heads - a.whole;
   const float* ml = a.part + cuts * parts * R * dim + (cut * (int64_t)R + row) * parts * 2;
-  const float* o = a.part + (cut * (int64_t)parts * R + row) * dim + d;
+  const float* o = a.part + (cut * (int64_t)parts * R + row) * dim + min(d, dim - 4);
+  // the first parts' sums are on their way while the tile's sequence is looked up (what lies there of rows that a
+  // tile has not is not used)
+  constexpr int kFirst = 4;
+  float m4[kFirst], l4[kFirst];
+  v4f o4[kFirst];
+#pragma unroll
+  for (int i = 0; i < kFirst; i++) {
+    const int s = min(way + i * deep, parts - 1);
+    m4[i] = ml[2 * s];
+    l4[i] = ml[2 * s + 1];
+    o4[i] = *reinterpret_cast<const v4f*>(o + (int64_t)s * R * dim);
+  }
+  Work w;
+  if (!find_tile<R>(a, a.whole + cut, w)) return;                 // the whole workgroup
+  const bool valid = w.row0 + row < w.rows && d < dim;
   float m = -INFINITY, l = 0.f;
   v4f sum{0.f, 0.f, 0.f, 0.f};
+  auto add = [&](float ms, float ls, const v4f& os) {
+    const float f = ms == m ? 1.f : __builtin_amdgcn_exp2f(ms - m);
+    l += f * ls;
+    sum += f * os;
+  };
   if (valid) {
-    for (int s = way; s < parts; s += deep) m = fmaxf(m, ml[2 * s]);
+#pragma unroll
+    for (int i = 0; i < kFirst; i++)
+      if (way + i * deep < parts) m = fmaxf(m, m4[i]);
+    for (int s = way + kFirst * deep; s < parts; s += deep) m = fmaxf(m, ml[2 * s]);
+#pragma unroll
+    for (int i = 0; i < kFirst; i++)
+      if (way + i * deep < parts) add(m4[i], l4[i], o4[i]);
 #pragma unroll 4
-    for (int s = way; s < parts; s += deep) {
-      const float f = ml[2 * s] == m ? 1.f : __builtin_amdgcn_exp2f(ml[2 * s] - m);
-      l += f * ml[2 * s + 1];
-      sum += f * *reinterpret_cast<const v4f*>(o + (int64_t)s * R * dim);
-    }
+    for (int s = way + kFirst * deep; s < parts; s += deep)
+      add(ml[2 * s], ml[2 * s + 1], *reinterpret_cast<const v4f*>(o + (int64_t)s * R * dim));
   }
   if (deep > 1) {
     *reinterpret_cast<v4f*>(lds[threadIdx.x]) = sum;
@@ -97,9 +117,11 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   } else {
     // two workgroups a CU: the tiles of the last, partial round are cut so that it fills the chip
     const int64_t round = 512, rest = tiles % round;
-    double best = 1.0;
+    // (in rounds of whole tiles: the parts' own, half a part for the workgroups that end early, and the join)
+    const double early = tiles > round ? 0.5 : 0.0;
+    double best = 1.0 + early;
     for (int s = 2; s <= 16 && s <= most && rest; s++) {
-      const double t = (double)((rest * s + round - 1) / round) / s + 0.01 * s;
+      const double t = (double)((rest * s + round - 1) / round) / s + early / s + 0.02 * s;
       if (t < 0.95 * best) {
         best = t;
         p.parts = s;

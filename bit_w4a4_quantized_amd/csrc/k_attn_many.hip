@@ -127,20 +127,14 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   v4u kr[CK == C16 ? 1 : kLoads], vr[CK == C16 ? 1 : kLoads];      // codes on their way
   float ksr = 0.f, vsr = 0.f;
   // The pages of a tile's loads, asked for a tile ahead: all of its keys are there, and the wave's loads have one
-  // page each.  The table does not change while a kernel runs.
-  typedef __attribute__((address_space(4))) const int const_int;
-  const_int* table = (const_int*)(uintptr_t)(a.b.table + w.seq * a.b.stride);
+  // page each.  (By the vector unit: the scalar one's loads would be waited for with the reads of LDS.)
+  const int* table = a.b.table + w.seq * a.b.stride;
   int ids[kLoads];
   auto look = [&](int base) {
     if (!steady || base + BN > end) return;
-    if (page_size >= BN) {
-      const int id = table[base >> a.c.shift];
 #pragma unroll
-      for (int i = 0; i < kLoads; i++) ids[i] = id;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; i++) ids[i] = table[(base + first_row(i)) >> a.c.shift];
-    }
+    for (int i = 0; i < kLoads; i++)
+      if (i == 0 || page_size < BN) ids[i] = table[(base + first_row(i)) >> a.c.shift];
   };
   auto fetch_scales = [&](int base, int page) {      // of the lane's key
     if (CK != C16 && wave == 0) {
@@ -156,17 +150,19 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   uint64_t at[kLoads];
   auto easy = [&](int base) {
     if (!steady || base + BN > end) return false;
-    bool all = true;
-#pragma unroll
-    for (int i = 0; i < kLoads; i++) all = all && (uint32_t)ids[i] < (uint32_t)a.c.pages;
+    uint32_t id = (uint32_t)__builtin_amdgcn_readfirstlane(ids[0]);
+    bool all = id < (uint32_t)a.c.pages;
+    at[0] = (uint64_t)id * page_bytes + (uint64_t)(uint32_t)((base + first_row(0)) & page_mask) * token_bytes;
     if (page_size >= BN) {
-      at[0] = (uint64_t)(uint32_t)ids[0] * page_bytes + (uint64_t)(uint32_t)((base + first_row(0)) & page_mask) * token_bytes;
 #pragma unroll
       for (int i = 1; i < kLoads; i++) at[i] = at[i - 1] + (uint64_t)4 * kRows * token_bytes;
     } else {
 #pragma unroll
-      for (int i = 0; i < kLoads; i++)
-        at[i] = (uint64_t)(uint32_t)ids[i] * page_bytes + (uint64_t)(uint32_t)((base + first_row(i)) & page_mask) * token_bytes;
+      for (int i = 1; i < kLoads; i++) {
+        id = (uint32_t)__builtin_amdgcn_readfirstlane(ids[i]);
+        all = all && id < (uint32_t)a.c.pages;
+        at[i] = (uint64_t)id * page_bytes + (uint64_t)(uint32_t)((base + first_row(i)) & page_mask) * token_bytes;
+      }
     }
     return all;
   };
@@ -427,8 +423,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       uint64_t next = kAll;
       if (more && !loads) next = fetch(base + BN, next_easy, then, then + kTile);
       if (checks) clean(vt, st);             // the same in every wave
-      if (works) compute(base, live, kt, vt, loads, then, st);
       if (more) look(base + 2 * BN);
+      if (works) compute(base, live, kt, vt, loads, then, st);
       live = next;
     };
     for (int base = begin; base < end; base += 2 * BN) {
