@@ -24,8 +24,11 @@ namespace {
 
 using namespace attn;
 
+// Waves a SIMD that the registers are kept to.
+constexpr int few_waves(int CK, int DP, int NT) { return DP == 256 ? 1 : NT == 2 ? 2 : DP == 64 ? 3 : CK == C16 ? 2 : 3; }
+
 template <bool BF, int CK, int DP, int NT, int NW>
-__global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
+__global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(AttnArgs a) {
   constexpr int kV = DP + 16;                // halves a row of V in LDS: eight rows side by side reach every bank
   constexpr int kSteps = DP / 32;            // of the contraction over the head's values
   constexpr int kPieces = CK == C16 ? DP / 8 : DP / 16;   // 16-byte pieces a row of the cache
@@ -77,53 +80,91 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
     for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] = v4f{0.f, 0.f, 0.f, 0.f};
   }
   uint16_t* vt = lds_v[wave];
-  const int es = CK == C16 ? 2 : 1;
+  constexpr int es = CK == C16 ? 2 : 1;
+  constexpr int kKLoads = CK == C16 ? kSteps : kSteps / 2;         // of a lane, for one row of K
   const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + w.head * a.c.head * es;
   const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + w.head * a.c.head * es;
-  const int l32 = lane & 31;
+  const int l32 = lane & 31, page_mask = (1 << a.c.shift) - 1;
 
+  // A tile's keys, in flight: K as a lane's operands straight from memory (rows c and 16 + c), V as whole rows.
+  v4u kf[2][kKLoads], vr[kLoads];
+  float ks = 0.f, vs = 0.f;
+  uint32_t live = 0;                         // which of its keys there are
+  int64_t off = 0;                           // of the row of the lane's key; with a page of its own the tile's first
+  bool easy = false;                         // one page holds the tile, and all of its keys are there
+  const bool steady = page_mask >= 31 && a.c.page < (int64_t)1 << 31 && a.c.token < 1 << 24;
+  const uint32_t page_bytes = (uint32_t)(a.c.page * es), token_bytes = (uint32_t)(a.c.token * es);
+  const uint32_t kat = c * token_bytes + quad * 16, vat = lane / kPieces * token_bytes + lane % kPieces * 16;
   auto entry_at = [&](int base) {            // of key base + lane % 32
     const int key = base + l32;
     return key < end ? entry_of(a.b, a.c, w.seq, key) : -1;
   };
-  int base = begin + wave * 32;
-  int entry = entry_at(base);
-  for (; base < end; base += 32 * NW) {
+  auto find = [&](int base, int entry) {
     const int page = as_page(a.c, entry);
-    entry = entry_at(base + 32 * NW);
-    const int key0 = base + l32;
-    const int64_t in_page = key0 & ((1 << a.c.shift) - 1);
-    const int64_t off = page < 0 ? -1 : (page * a.c.page + in_page * a.c.token) * es;
-    const uint32_t live = (uint32_t)__ballot(page >= 0);
-    const int lo = (int)off, hi = (int)(off >> 32);
-    auto row_at = [&](int row) {             // byte offset of a row of the tile, below 0: absent
-      return ((int64_t)__shfl(hi, row) << 32) | (uint32_t)__shfl(lo, row);
-    };
-    // K: a lane's operands straight from memory; V: whole rows
-    v4u kf[2][CK == C16 ? kSteps : kSteps / 2], vr[kLoads];
-#pragma unroll
-    for (int t = 0; t < 2; t++) {
-      const int64_t o = row_at(16 * t + c);
-#pragma unroll
-      for (int s = 0; s < (CK == C16 ? kSteps : kSteps / 2); s++) {
-        const int d = CK == C16 ? s * 32 + quad * 8 : s * 64 + quad * 16;
-        kf[t][s] = v4u{0, 0, 0, 0};
-        if (o >= 0 && d < dim) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + o + d * es);
+    live = (uint32_t)__ballot(page >= 0);
+    easy = steady && live == 0xFFFFFFFFu;
+    const int64_t in_page = (base + l32) & page_mask;
+    if (easy) {
+      const uint32_t id = (uint32_t)__builtin_amdgcn_readfirstlane(page);
+      off = (int64_t)((uint64_t)id * page_bytes + (uint64_t)(uint32_t)(base & page_mask) * token_bytes);
+    } else {
+      off = page < 0 ? -1 : (page * a.c.page + in_page * a.c.token) * es;
+    }
+    if (CK != C16) {
+      ks = vs = 0.f;
+      if (page >= 0) {
+        const int64_t so = page * a.c.spage + in_page * a.c.stoken + w.head * a.c.shead;
+        ks = a.c.ks[so];
+        vs = a.c.vs[so];
       }
     }
+  };
+  auto row_at = [&](int row) {               // byte offset of a row of the tile, below 0: absent
+    return ((int64_t)__shfl((int)(off >> 32), row) << 32) | (uint32_t)__shfl((int)off, row);
+  };
+  auto load_k = [&]() {
+    if (easy) {
+#pragma unroll
+      for (int t = 0; t < 2; t++)
+#pragma unroll
+        for (int s = 0; s < kKLoads; s++) {
+          kf[t][s] = v4u{0, 0, 0, 0};
+          if ((s * 64 + quad * 16) / es < dim) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + off + 16 * t * token_bytes + kat + s * 64);
+        }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const int64_t o = row_at(16 * t + c);
+#pragma unroll
+        for (int s = 0; s < kKLoads; s++) {
+          kf[t][s] = v4u{0, 0, 0, 0};
+          if (o >= 0 && (s * 64 + quad * 16) / es < dim) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + o + s * 64 + quad * 16);
+        }
+      }
+    }
+  };
+  auto load_v = [&]() {
+    const bool in = lane % kPieces * (16 / es) < dim;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
-      const int64_t o = row_at(i * kRows + lane / kPieces);
-      const int piece = lane % kPieces;
       vr[i] = v4u{0, 0, 0, 0};
-      if (o >= 0 && piece * (16 / es) < dim) vr[i] = *reinterpret_cast<const v4u*>(vbase + o + piece * 16);
+      if (easy) {
+        if (in) vr[i] = *reinterpret_cast<const v4u*>(vbase + off + i * kRows * token_bytes + vat);
+      } else {
+        const int64_t o = row_at(i * kRows + lane / kPieces);
+        if (o >= 0 && in) vr[i] = *reinterpret_cast<const v4u*>(vbase + o + lane % kPieces * 16);
+      }
     }
-    float ks = 0.f, vs = 0.f;
-    if (CK != C16 && page >= 0) {
-      const int64_t so = page * a.c.spage + in_page * a.c.stoken + w.head * a.c.shead;
-      ks = a.c.ks[so];
-      vs = a.c.vs[so];
-    }
+  };
+
+  int base = begin + wave * 32, entry = entry_at(base);
+  if (base < end) {
+    find(base, entry);
+    load_k();
+    load_v();
+    entry = entry_at(base + 32 * NW);
+  }
+  for (; base < end; base += 32 * NW) {
     const bool masked = base + 32 > w.ctx || live != 0xFFFFFFFFu;   // the same in every lane
     uint32_t seen[NT];
     if (masked) {
@@ -169,6 +210,12 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
       }
       *reinterpret_cast<v4u*>(to) = x[0];
       if (CK != C16) *reinterpret_cast<v4u*>(to + 8) = x[1];
+    }
+    if (base + 32 * NW < end) {              // the next tile's loads, into the registers that are free now
+      find(base + 32 * NW, entry);
+      load_k();
+      load_v();
+      entry = entry_at(base + 64 * NW);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -327,9 +374,9 @@ __global__ void __launch_bounds__(64 * NW) k_attn_few(AttnArgs a) {
   }
 }
 
-template <bool BF, int CK, int DP>
+template <bool BF, int CK, int DP, int NT>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
-  constexpr int NT = 1, NW = 4;
+  constexpr int NW = 4;
   const int64_t blocks = blocks_of(a);
   if (!launchable(blocks, 64 * NW)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_attn_few<BF, CK, DP, NT, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, a);
@@ -338,7 +385,9 @@ hipError_t launch(const AttnArgs& a, hipStream_t s) {
 
 template <bool BF, int CK>
 hipError_t launch_dim(const AttnArgs& a, hipStream_t s) {
-  return a.c.dim <= 64 ? launch<BF, CK, 64>(a, s) : a.c.dim <= 128 ? launch<BF, CK, 128>(a, s) : launch<BF, CK, 256>(a, s);
+  if (a.rows == 16)
+    return a.c.dim <= 64 ? launch<BF, CK, 64, 1>(a, s) : a.c.dim <= 128 ? launch<BF, CK, 128, 1>(a, s) : launch<BF, CK, 256, 1>(a, s);
+  return a.c.dim <= 64 ? launch<BF, CK, 64, 2>(a, s) : launch<BF, CK, 128, 2>(a, s);
 }
 
 }  // namespace

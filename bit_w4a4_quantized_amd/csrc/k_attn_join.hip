@@ -94,7 +94,7 @@ hipError_t join_dim(const AttnArgs& a, hipStream_t s) {
   return a.c.dim <= 64 ? join<R, 16>(a, s) : a.c.dim <= 128 ? join<R, 32>(a, s) : join<R, 64>(a, s);
 }
 
-constexpr int kManyRows = 128, kFewRows = 16;
+constexpr int kManyRows = 128, kFewRows = 32;   // 16 or 32 where there are no more (32 of heads up to 128: registers)
 
 }  // namespace
 
@@ -102,15 +102,15 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   AttnPlan p{};
   const int group = heads / kv_heads;
   const int64_t each = ((int64_t)tokens * group + sequences - 1) / sequences;    // rows of a sequence and cache head
-  p.rows = each <= 32 ? kFewRows : kManyRows;
+  p.rows = each > kFewRows ? kManyRows : each > 16 && dim <= 128 ? kFewRows : 16;
   p.slots = (int)((int64_t)tokens * group / p.rows + sequences);
   const int64_t all = (int64_t)p.slots * kv_heads;
   const int64_t tiles = (each + p.rows - 1) / p.rows * sequences * kv_heads;     // not empty, for sequences alike
   p.whole = (int)(all < 1 << 30 ? all : 1 << 30);
   p.parts = 1;
-  const int64_t most = reach / (p.rows == kFewRows ? 256 : 128);
-  if (p.rows == kFewRows) {
-    const int64_t s = 1024 / tiles;
+  const int64_t most = reach / (p.rows <= kFewRows ? 256 : 128);
+  if (p.rows <= kFewRows) {
+    const int64_t s = 2048 / tiles;
     p.parts = (int)(s < most ? s : most);
     if (p.parts > 128) p.parts = 128;
     if (p.parts > 1) p.whole = 0;
@@ -141,9 +141,9 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
 }
 
 hipError_t launch_attn(const AttnArgs& a, hipStream_t s) {
-  const hipError_t e = a.rows == kFewRows ? attn::launch_few(a, s) : attn::launch_many(a, s);
+  const hipError_t e = a.rows <= kFewRows ? attn::launch_few(a, s) : attn::launch_many(a, s);
   if (e != hipSuccess || a.parts == 1) return e;
-  return a.rows == kFewRows ? join_dim<kFewRows>(a, s) : join_dim<kManyRows>(a, s);
+  return a.rows == 16 ? join_dim<16>(a, s) : a.rows == kFewRows ? join_dim<kFewRows>(a, s) : join_dim<kManyRows>(a, s);
 }
 
 }  // namespace svdq
