@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
   bool easy = false;                         // one page holds the tile, and all of its keys are there
   const bool steady = page_mask >= 31 && a.c.page < (int64_t)1 << 31 && a.c.token < 1 << 24;
   const uint32_t page_bytes = (uint32_t)(a.c.page * es), token_bytes = (uint32_t)(a.c.token * es);
-  const uint32_t kat = c * token_bytes + quad * 16, vat = lane / kPieces * token_bytes + lane % kPieces * 16;
+  const uint32_t crow = c * token_bytes, vrow = lane / kPieces * token_bytes;
   auto entry_at = [&](int base) {            // of key base + lane % 32
     const int key = base + l32;
     return key < end ? entry_of(a.b, a.c, w.seq, key) : -1;
@@ -122,15 +122,20 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
   auto row_at = [&](int row) {               // byte offset of a row of the tile, below 0: absent
     return ((int64_t)__shfl((int)(off >> 32), row) << 32) | (uint32_t)__shfl((int)off, row);
   };
+  // Places past the head's end read its first piece instead: in K they meet zeros of the queries, and have to be
+  // finite; in V they make results that nothing takes.
+  const bool whole = dim == DP;
+  int kcol[kKLoads];                         // byte offset of the lane's pieces in a row
+#pragma unroll
+  for (int s = 0; s < kKLoads; s++) kcol[s] = (s * 64 + quad * 16) / es < dim ? s * 64 + quad * 16 : 0;
+  const int vcol = lane % kPieces * (16 / es) < dim ? lane % kPieces * 16 : 0;
   auto load_k = [&]() {
     if (easy) {
 #pragma unroll
       for (int t = 0; t < 2; t++)
 #pragma unroll
-        for (int s = 0; s < kKLoads; s++) {
-          kf[t][s] = v4u{0, 0, 0, 0};
-          if ((s * 64 + quad * 16) / es < dim) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + off + 16 * t * token_bytes + kat + s * 64);
-        }
+        for (int s = 0; s < kKLoads; s++)
+          kf[t][s] = *reinterpret_cast<const v4u*>(kbase + off + (16 * t * token_bytes + crow) + (whole ? s * 64 + quad * 16 : kcol[s]));
     } else {
 #pragma unroll
       for (int t = 0; t < 2; t++) {
@@ -138,21 +143,25 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
 #pragma unroll
         for (int s = 0; s < kKLoads; s++) {
           kf[t][s] = v4u{0, 0, 0, 0};
-          if (o >= 0 && (s * 64 + quad * 16) / es < dim) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + o + s * 64 + quad * 16);
+          if (o >= 0) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + o + kcol[s]);
         }
       }
     }
+    if (!whole) {
+#pragma unroll
+      for (int s = 0; s < kKLoads; s++)
+        if ((s * 64 + quad * 16) / es >= dim) kf[0][s] = kf[1][s] = v4u{0, 0, 0, 0};
+    }
   };
   auto load_v = [&]() {
-    const bool in = lane % kPieces * (16 / es) < dim;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
-      vr[i] = v4u{0, 0, 0, 0};
       if (easy) {
-        if (in) vr[i] = *reinterpret_cast<const v4u*>(vbase + off + i * kRows * token_bytes + vat);
+        vr[i] = *reinterpret_cast<const v4u*>(vbase + off + i * kRows * token_bytes + (vrow + vcol));
       } else {
         const int64_t o = row_at(i * kRows + lane / kPieces);
-        if (o >= 0 && in) vr[i] = *reinterpret_cast<const v4u*>(vbase + o + lane % kPieces * 16);
+        vr[i] = v4u{0, 0, 0, 0};
+        if (o >= 0) vr[i] = *reinterpret_cast<const v4u*>(vbase + o + vcol);
       }
     }
   };
@@ -171,7 +180,7 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
 #pragma unroll
       for (int n = 0; n < NT; n++) {
         seen[n] = 0;
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < 8; e++) {
           const int k = (e >> 2) * 16 + quad * 4 + (e & 3);
           if (valid[n] && (live >> k & 1) && w.sees(a, tok[n], base + k)) seen[n] |= 1u << e;

@@ -108,11 +108,14 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   const int64_t tiles = (each + p.rows - 1) / p.rows * sequences * kv_heads;     // not empty, for sequences alike
   p.whole = (int)(all < 1 << 30 ? all : 1 << 30);
   p.parts = 1;
-  const int64_t most = reach / (p.rows <= kFewRows ? 256 : 128);
+  const int64_t most = reach / 128;
   if (p.rows <= kFewRows) {
-    const int64_t s = 2048 / tiles;
-    p.parts = (int)(s < most ? s : most);
-    if (p.parts > 128) p.parts = 128;
+    // one round of workgroups (two or three a CU), and more of them while a part is longer than its fixed costs
+    const int64_t round = (p.rows == 16 ? 768 : 384) / tiles;
+    int64_t s = round < 1 ? 1 : round;
+    while (reach / s > 1500 && 2 * s * tiles <= 3072) s *= 2;
+    s = s < most ? s : most;
+    p.parts = s > 128 ? 128 : (int)s;
     if (p.parts > 1) p.whole = 0;
   } else {
     // two workgroups a CU: the tiles of the last, partial round are cut so that it fills the chip

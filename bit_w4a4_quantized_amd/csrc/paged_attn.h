@@ -133,13 +133,29 @@ template <int R>
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) {
   w.head = tile % a.c.heads;
   const int slot = a.slots - 1 - tile / a.c.heads;
-  auto first = [&](int i) { return (int64_t)start_of(a.b, i, a.tokens) * a.group / R + i; };
-  w.seq = __builtin_amdgcn_readfirstlane(last_below(a.b.n, slot, first));
-  if (w.seq < 0) return false;
-  w.s0 = start_of(a.b, w.seq, a.tokens);
-  w.n = max(0, start_of(a.b, w.seq + 1, a.tokens) - w.s0);
+  int s1;
+  if (a.b.n <= 64) {                         // one look, at all that is asked of the sequence
+    const int i = min(__lane_id(), a.b.n - 1);
+    const int from = start_of(a.b, i, a.tokens), to = start_of(a.b, i + 1, a.tokens), ctx = context_of(a.b, i);
+    const int64_t first = (int64_t)from * a.group / R + i;
+    const int count = __popcll(__ballot((int)__lane_id() < a.b.n && first <= slot));
+    if (count == 0) return false;
+    w.seq = __builtin_amdgcn_readfirstlane(count - 1);
+    w.s0 = __builtin_amdgcn_readlane(from, w.seq);
+    s1 = __builtin_amdgcn_readlane(to, w.seq);
+    w.ctx = __builtin_amdgcn_readlane(ctx, w.seq);
+  } else {
+    w.seq = __builtin_amdgcn_readfirstlane(
+        last_below(a.b.n, slot, [&](int i) { return (int64_t)start_of(a.b, i, a.tokens) * a.group / R + i; }));
+    if (w.seq < 0) return false;
+    w.s0 = start_of(a.b, w.seq, a.tokens);
+    s1 = start_of(a.b, w.seq + 1, a.tokens);
+    w.ctx = context_of(a.b, w.seq);
+  }
+  const int64_t first = (int64_t)w.s0 * a.group / R + w.seq;
+  w.n = max(0, s1 - w.s0);
   w.rows = w.n * a.group;
-  const int64_t row0 = (slot - first(w.seq)) * R;
+  const int64_t row0 = (slot - first) * R;
   if (row0 >= w.rows) return false;
   w.row0 = (int)row0;
   return true;
@@ -158,7 +174,6 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
     tile = a.whole + w.cut;
   }
   if (!find_tile<R>(a, tile, w)) return false;
-  w.ctx = context_of(a.b, w.seq);
   const int64_t reach = (int64_t)a.b.width << a.c.shift;
   w.keys = (int)min((int64_t)w.ctx + w.n, reach);
   return true;
