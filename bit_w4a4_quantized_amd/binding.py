@@ -85,7 +85,7 @@ _SIGS = {
                                   _c_int, _c_float, _vp]),
     "svdq_tree_attention": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp, _c_i64, _c_int,
                                      _vp, _c_i64, _c_i64, _vp, _c_size, _vp]),
-    "svdq_tree_attention_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "svdq_tree_attention_workspace_bytes": (_c_size, [_c_int] * 7),
     "svdq_cache_keep": (_c_int, [_vp, _vp, _vp, _c_i64, _c_int, _vp]),
     "svdq_status_string": (ctypes.c_char_p, [_c_int]),
     "svdq_version": (ctypes.c_char_p, []),

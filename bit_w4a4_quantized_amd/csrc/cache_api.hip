@@ -168,6 +168,8 @@ svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_
                                (int64_t)batch->table_width * cache->page_size, workspace ? workspace_bytes : 0);
   a.rows = p.rows;
   a.slots = p.slots;
+  a.unit = p.unit;
+  a.ids = p.ids;
   a.whole = p.whole;
   a.parts = p.parts;
   a.part = static_cast<float*>(workspace);

@@ -27,24 +27,27 @@ using namespace attn;
 // Waves a SIMD that the registers are kept to.
 constexpr int few_waves(int CK, int DP, int NT) { return DP == 256 ? 1 : NT == 2 ? 2 : DP == 64 ? 3 : CK == C16 ? 2 : 3; }
 
+template <int CK, int DP, int NT, int NW>
+struct FewLds {
+  // V's rows of 2 DP bytes and 32 more: eight of them side by side reach every bank
+  __attribute__((aligned(16))) uint16_t v[NW][32 * (DP + 16)];
+  __attribute__((aligned(16))) float s[CK == C16 ? 1 : NW][2][32];   // scales of K and V
+  float ml[NW][16 * NT][2];
+};
+
 template <bool BF, int CK, int DP, int NT, int NW>
-__global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(AttnArgs a) {
-  constexpr int kV = DP + 16;                // halves a row of V in LDS: eight rows side by side reach every bank
+__device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<CK, DP, NT, NW>& lds) {
+  constexpr int kV = DP + 16;                // halves a row of V in LDS
   constexpr int kSteps = DP / 32;            // of the contraction over the head's values
   constexpr int kPieces = CK == C16 ? DP / 8 : DP / 16;   // 16-byte pieces a row of the cache
   constexpr int kLoads = kPieces / 2;        // of a lane, for 32 rows of V
   constexpr int kRows = 64 / kPieces;        // of V a load instruction
-  __shared__ __attribute__((aligned(16))) uint16_t lds_v[NW][32 * kV];
-  __shared__ __attribute__((aligned(16))) float lds_s[CK == C16 ? 1 : NW][2][32];    // scales of K and V
-  __shared__ float lds_ml[NW][16 * NT][2];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, c = lane & 15, quad = lane >> 4;
+  auto& lds_v = lds.v;
+  auto& lds_s = lds.s;
+  auto& lds_ml = lds.ml;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, quad = lane >> 4;
 
-  Work w;
-  if (!find_work<16 * NT>(a, w)) return;     // the whole workgroup
-  const int kmax = w.last_key(a, w.row0 + 16 * NT - 1);
-  int begin, end;
-  w.part(kmax, 32 * NW, &begin, &end);
-  const int dim = a.c.dim;
+  const int begin = w.begin, end = w.end, dim = a.c.dim;
 
   // rows and their queries
   int tok[NT];
@@ -81,20 +84,21 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
   }
   uint16_t* vt = lds_v[wave];
   constexpr int es = CK == C16 ? 2 : 1;
-  constexpr int kKLoads = CK == C16 ? kSteps : kSteps / 2;         // of a lane, for one row of K
+  constexpr int kKLoads = CK == C16 ? kSteps : kSteps / 2;         // pieces of a row of K that a lane takes
   const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + w.head * a.c.head * es;
   const uint8_t* vbase = static_cast<const uint8_t*>(a.c.v) + w.head * a.c.head * es;
   const int l32 = lane & 31, page_mask = (1 << a.c.shift) - 1;
 
-  // A tile's keys, in flight: K as a lane's operands straight from memory (rows c and 16 + c), V as whole rows.
-  v4u kf[2][kKLoads], vr[kLoads];
+  // A tile's keys in flight, K and V as whole rows (a lane's operands of K straight from memory, 64 bytes of 16 rows
+  // an instruction, came at 4.4 TB/s where whole lines come at 5.4).
+  v4u kr[kLoads], vr[kLoads];
   float ks = 0.f, vs = 0.f;
   uint32_t live = 0;                         // which of its keys there are
   int64_t off = 0;                           // of the row of the lane's key; with a page of its own the tile's first
   bool easy = false;                         // one page holds the tile, and all of its keys are there
   const bool steady = page_mask >= 31 && a.c.page < (int64_t)1 << 31 && a.c.token < 1 << 24;
   const uint32_t page_bytes = (uint32_t)(a.c.page * es), token_bytes = (uint32_t)(a.c.token * es);
-  const uint32_t crow = c * token_bytes, vrow = lane / kPieces * token_bytes;
+  const int row_in = lane / kPieces, piece = lane % kPieces;
   auto entry_at = [&](int base) {            // of key base + lane % 32
     const int key = base + l32;
     return key < end ? entry_of(a.b, a.c, w.seq, key) : -1;
@@ -119,62 +123,35 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
       }
     }
   };
-  auto row_at = [&](int row) {               // byte offset of a row of the tile, below 0: absent
-    return ((int64_t)__shfl((int)(off >> 32), row) << 32) | (uint32_t)__shfl((int)off, row);
-  };
-  // Places past the head's end read its first piece instead: in K they meet zeros of the queries, and have to be
-  // finite; in V they make results that nothing takes.
-  const bool whole = dim == DP;
-  int kcol[kKLoads];                         // byte offset of the lane's pieces in a row
-#pragma unroll
-  for (int s = 0; s < kKLoads; s++) kcol[s] = (s * 64 + quad * 16) / es < dim ? s * 64 + quad * 16 : 0;
-  const int vcol = lane % kPieces * (16 / es) < dim ? lane % kPieces * 16 : 0;
-  auto load_k = [&]() {
-    if (easy) {
-#pragma unroll
-      for (int t = 0; t < 2; t++)
-#pragma unroll
-        for (int s = 0; s < kKLoads; s++)
-          kf[t][s] = *reinterpret_cast<const v4u*>(kbase + off + (16 * t * token_bytes + crow) + (whole ? s * 64 + quad * 16 : kcol[s]));
-    } else {
-#pragma unroll
-      for (int t = 0; t < 2; t++) {
-        const int64_t o = row_at(16 * t + c);
-#pragma unroll
-        for (int s = 0; s < kKLoads; s++) {
-          kf[t][s] = v4u{0, 0, 0, 0};
-          if (o >= 0) kf[t][s] = *reinterpret_cast<const v4u*>(kbase + o + kcol[s]);
-        }
-      }
-    }
-    if (!whole) {
-#pragma unroll
-      for (int s = 0; s < kKLoads; s++)
-        if ((s * 64 + quad * 16) / es >= dim) kf[0][s] = kf[1][s] = v4u{0, 0, 0, 0};
-    }
-  };
-  auto load_v = [&]() {
+  // Places past the head's end read its first piece instead (in V they make results that nothing takes; in K they
+  // are made zeros on the way to LDS, to meet those of the queries).
+  const bool in = piece * (16 / es) < dim;
+  const uint32_t place = row_in * token_bytes + (in ? piece * 16 : 0);
+  auto load = [&](const uint8_t* from, v4u (&r)[kLoads]) {
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
       if (easy) {
-        vr[i] = *reinterpret_cast<const v4u*>(vbase + off + i * kRows * token_bytes + (vrow + vcol));
+        r[i] = *reinterpret_cast<const v4u*>(from + off + i * kRows * token_bytes + place);
       } else {
-        const int64_t o = row_at(i * kRows + lane / kPieces);
-        vr[i] = v4u{0, 0, 0, 0};
-        if (o >= 0) vr[i] = *reinterpret_cast<const v4u*>(vbase + o + vcol);
+        const int row = i * kRows + row_in;
+        const int64_t o = ((int64_t)__shfl((int)(off >> 32), row) << 32) | (uint32_t)__shfl((int)off, row);
+        r[i] = v4u{0, 0, 0, 0};
+        if (o >= 0) r[i] = *reinterpret_cast<const v4u*>(from + o + (in ? piece * 16 : 0));
       }
     }
   };
+  constexpr int kK = CK == C16 ? 2 * kV : DP + 16;       // bytes a row of K in LDS, where V comes after it
+  uint8_t* kt = reinterpret_cast<uint8_t*>(vt);
 
   int base = begin + wave * 32, entry = entry_at(base);
   if (base < end) {
     find(base, entry);
-    load_k();
-    load_v();
+    load(kbase, kr);
+    load(vbase, vr);
     entry = entry_at(base + 32 * NW);
   }
   for (; base < end; base += 32 * NW) {
-    const bool masked = base + 32 > w.ctx || live != 0xFFFFFFFFu;   // the same in every lane
+    const bool masked = base + 32 > w.ctx || live != 0xFFFFFFFFu, more = base + 32 * NW < end;   // the same in every lane
     uint32_t seen[NT];
     if (masked) {
 #pragma unroll
@@ -187,6 +164,24 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
         }
       }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();         // the last tile's reads of LDS are done
+    if (CK != C16 && lane < 32) {
+      lds_s[wave][0][lane] = ks;
+      const bool infinite = masked && !(__builtin_fabsf(vs) < INFINITY);
+      lds_s[wave][1][lane] = infinite ? 0.f : vs;
+      sick = sick || infinite;
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; i++)
+      *reinterpret_cast<v4u*>(kt + (i * kRows + row_in) * kK + piece * 16) = in ? kr[i] : v4u{0, 0, 0, 0};
+    if (more) {                              // the next tile's loads, into registers that are free now
+      find(base + 32 * NW, entry);
+      load(kbase, kr);
+      entry = entry_at(base + 64 * NW);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 
     // S^T
     v4f st[NT][2];
@@ -195,23 +190,20 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
 #pragma unroll
     for (int t = 0; t < 2; t++)
 #pragma unroll
-      for (int s = 0; s < kSteps; s++) {
-        const v4u kk = CK == C16 ? kf[t][s] : widen<CK>(kf[t][s >> 1], s & 1);
+      for (int s = 0; s < kKLoads; s++) {
+        const v4u x = *reinterpret_cast<const v4u*>(kt + (16 * t + c) * kK + s * 64 + quad * 16);
 #pragma unroll
-        for (int n = 0; n < NT; n++) st[n][t] = mfma16<BF>(kk, qf[n][s], st[n][t]);
+        for (int h = 0; h < (CK == C16 ? 1 : 2); h++) {
+          const v4u kk = CK == C16 ? x : widen<CK>(x, h);
+#pragma unroll
+          for (int n = 0; n < NT; n++) st[n][t] = mfma16<BF>(kk, qf[n][CK == C16 ? s : 2 * s + h], st[n][t]);
+        }
       }
-
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();         // the last tile's reads of LDS are done
-    if (CK != C16 && lane < 32) {
-      lds_s[wave][0][lane] = ks;
-      const bool off = masked && !(__builtin_fabsf(vs) < INFINITY);
-      lds_s[wave][1][lane] = off ? 0.f : vs;
-      sick = sick || off;
-    }
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
-      uint16_t* to = vt + (i * kRows + lane / kPieces) * kV + lane % kPieces * (CK == C16 ? 8 : 16);
+      uint16_t* to = vt + (i * kRows + row_in) * kV + piece * (CK == C16 ? 8 : 16);
       v4u x[2] = {CK == C16 ? vr[i] : widen<CK>(vr[i], 0), CK == C16 ? vr[i] : widen<CK>(vr[i], 1)};
       if (masked && CK != CI8) {             // rows that see an infinity or NaN get it at the end
         sick = make_finite<BF>(x[0]) || sick;
@@ -219,13 +211,9 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
       }
       *reinterpret_cast<v4u*>(to) = x[0];
       if (CK != C16) *reinterpret_cast<v4u*>(to + 8) = x[1];
+      if (CK != C16) __builtin_amdgcn_sched_barrier(0);      // few pieces as fp16 at once
     }
-    if (base + 32 * NW < end) {              // the next tile's loads, into the registers that are free now
-      find(base + 32 * NW, entry);
-      load_k();
-      load_v();
-      entry = entry_at(base + 64 * NW);
-    }
+    if (more) load(vbase, vr);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 
@@ -366,7 +354,7 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
         *reinterpret_cast<v4f*>(mine + (16 * n + c) * CH + (((x * 4 + quad) ^ c) & (kP - 1)) * 4) = v;
       }
     __syncthreads();
-    for (int u = threadIdx.x; u < 16 * NT * kP; u += 64 * NW) {
+    for (int u = tid; u < 16 * NT * kP; u += 64 * NW) {
       const int row = u / kP, piece = u % kP, d = turn * CH + piece * 4;
       if (w.row0 + row >= w.rows || d >= dim) continue;
       float mm = -INFINITY, sum = 0.f;
@@ -381,6 +369,13 @@ __global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(Att
       put(dest_of<16 * NT>(a, w, row), a.qbf, d, o, mm, sum);
     }
   }
+}
+
+template <bool BF, int CK, int DP, int NT, int NW>
+__global__ void __launch_bounds__(64 * NW, few_waves(CK, DP, NT)) k_attn_few(AttnArgs a) {
+  __shared__ FewLds<CK, DP, NT, NW> lds;
+  Work w;
+  if (cut_work<16 * NT>(a, w)) attend<BF, CK, DP, NT, NW>(a, w, lds);        // the whole workgroup
 }
 
 template <bool BF, int CK, int DP, int NT>

@@ -16,11 +16,12 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
   __shared__ float lds_ml[256 / P][2];
   const int per = 256 / P / deep;            // rows a workgroup
   const int g = threadIdx.x / P, lane = threadIdx.x % P, row_in = g / deep, way = g % deep;
-  const int chunks = R / per, cut = blockIdx.x / chunks, row = (int)(blockIdx.x % chunks) * per + row_in;
-  const int dim = a.c.dim, d = lane * 4, parts = a.parts;
-  const int64_t cuts = (int64_t)a.slots * a.c.heads - a.whole;
-  const float* ml = a.part + cuts * parts * R * dim + (cut * (int64_t)R + row) * parts * 2;
-  const float* o = a.part + (cut * (int64_t)parts * R + row) * dim + min(d, dim - 4);
+  const int chunks = R / per, tile = a.whole + blockIdx.x / chunks, row = (int)(blockIdx.x % chunks) * per + row_in;
+  const int dim = a.c.dim, d = lane * 4;
+  const int parts = a.parts;
+  const int64_t id = (int64_t)(tile - a.whole) * parts;      // of the first part; the others follow
+  const float* ml = a.part + a.ids * R * dim + (id * R + row) * 2;
+  const float* o = a.part + (id * R + row) * dim + min(d, dim - 4);
   // the first parts' sums are on their way while the tile's sequence is looked up (what lies there of rows that a
   // tile has not is not used)
   constexpr int kFirst = 4;
@@ -28,13 +29,14 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
   v4f o4[kFirst];
 #pragma unroll
   for (int i = 0; i < kFirst; i++) {
-    const int s = min(way + i * deep, parts - 1);
+    const int64_t s = min(way + i * deep, parts - 1) * (int64_t)R;
     m4[i] = ml[2 * s];
     l4[i] = ml[2 * s + 1];
-    o4[i] = *reinterpret_cast<const v4f*>(o + (int64_t)s * R * dim);
+    o4[i] = *reinterpret_cast<const v4f*>(o + s * dim);
   }
   Work w;
-  if (!find_tile<R>(a, a.whole + cut, w)) return;                 // the whole workgroup
+  w.id = -1;
+  if (!find_tile<R>(a, tile, w)) return;     // the whole workgroup
   const bool valid = w.row0 + row < w.rows && d < dim;
   float m = -INFINITY, l = 0.f;
   v4f sum{0.f, 0.f, 0.f, 0.f};
@@ -47,13 +49,15 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
 #pragma unroll
     for (int i = 0; i < kFirst; i++)
       if (way + i * deep < parts) m = fmaxf(m, m4[i]);
-    for (int s = way + kFirst * deep; s < parts; s += deep) m = fmaxf(m, ml[2 * s]);
+    for (int s = way + kFirst * deep; s < parts; s += deep) m = fmaxf(m, ml[(int64_t)s * R * 2]);
 #pragma unroll
     for (int i = 0; i < kFirst; i++)
       if (way + i * deep < parts) add(m4[i], l4[i], o4[i]);
 #pragma unroll 4
-    for (int s = way + kFirst * deep; s < parts; s += deep)
-      add(ml[2 * s], ml[2 * s + 1], *reinterpret_cast<const v4f*>(o + (int64_t)s * R * dim));
+    for (int s = way + kFirst * deep; s < parts; s += deep) {
+      const int64_t x = (int64_t)s * R;
+      add(ml[2 * x], ml[2 * x + 1], *reinterpret_cast<const v4f*>(o + x * dim));
+    }
   }
   if (deep > 1) {
     *reinterpret_cast<v4f*>(lds[threadIdx.x]) = sum;
@@ -74,7 +78,6 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
     }
   }
   if (!valid) return;
-  w.parts = 1;
   put(dest_of<R>(a, w, row), a.qbf, d, sum, m, l);
 }
 
@@ -103,28 +106,32 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   const int group = heads / kv_heads;
   const int64_t each = ((int64_t)tokens * group + sequences - 1) / sequences;    // rows of a sequence and cache head
   p.rows = each > kFewRows ? kManyRows : each > 16 && dim <= 128 ? kFewRows : 16;
+  p.unit = p.rows <= kFewRows ? 128 : dim > 128 ? 32 : 64;
   p.slots = (int)((int64_t)tokens * group / p.rows + sequences);
   const int64_t all = (int64_t)p.slots * kv_heads;
   const int64_t tiles = (each + p.rows - 1) / p.rows * sequences * kv_heads;     // not empty, for sequences alike
-  p.whole = (int)(all < 1 << 30 ? all : 1 << 30);
-  p.parts = 1;
   const int64_t most = reach / 128;
+  p.whole = (int)all;
+  p.parts = 1;
+  const size_t id_bytes = (size_t)p.rows * (dim + 2) * sizeof(float);
+  // workgroups that are on the chip at once: two a CU, three of the 16-row kernel
+  const int64_t resident = p.rows == 16 ? 768 : 512;
   if (p.rows <= kFewRows) {
-    // one round of workgroups (two or three a CU), and more of them while a part is longer than its fixed costs
-    const int64_t round = (p.rows == 16 ? 768 : 384) / tiles;
+    // one round of workgroups, and more of them while a part is longer than its fixed costs
+    const int64_t round = (p.rows == 16 ? resident : 384) / tiles;
     int64_t s = round < 1 ? 1 : round;
     while (reach / s > 1500 && 2 * s * tiles <= 3072) s *= 2;
     s = s < most ? s : most;
     p.parts = s > 128 ? 128 : (int)s;
     if (p.parts > 1) p.whole = 0;
   } else {
-    // two workgroups a CU: the tiles of the last, partial round are cut so that it fills the chip
-    const int64_t round = 512, rest = tiles % round;
-    // (in rounds of whole tiles: the parts' own, half a part for the workgroups that end early, and the join)
-    const double early = tiles > round ? 0.5 : 0.0;
+    // The tiles of the last, partial round are cut so that it fills the chip (in rounds of whole tiles: the parts'
+    // own, half a part for the workgroups that end early, and the join).
+    const int64_t rest = tiles % resident;
+    const double early = tiles > resident ? 0.5 : 0.0;
     double best = 1.0 + early;
     for (int s = 2; s <= 16 && s <= most && rest; s++) {
-      const double t = (double)((rest * s + round - 1) / round) / s + early / s + 0.02 * s;
+      const double t = (double)((rest * s + resident - 1) / resident) / s + early / s + 0.02 * s;
       if (t < 0.95 * best) {
         best = t;
         p.parts = s;
@@ -134,10 +141,11 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   }
   if (p.parts < 2) {
     p.parts = 1;
-    p.whole = (int)(all < 1 << 30 ? all : 1 << 30);
+    p.whole = (int)all;
   }
   for (;; p.parts--) {
-    p.bytes = p.parts > 1 ? (size_t)(all - p.whole) * p.parts * p.rows * (dim + 2) * sizeof(float) : 0;
+    p.ids = (all - p.whole) * p.parts;
+    p.bytes = p.parts > 1 ? p.ids * id_bytes : 0;
     if (p.bytes <= room) break;
   }
   return p;

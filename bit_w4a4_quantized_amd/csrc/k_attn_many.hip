@@ -67,11 +67,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   const int c = lane & 31, half = lane >> 5;
 
   Work w;
-  if (!find_work<128>(a, w)) return;         // the whole workgroup
-  const int kmax = w.last_key(a, w.row0 + 127);
-  int begin, end;
-  w.part(kmax, BN, &begin, &end);
-  const int dim = a.c.dim;
+  if (!cut_work<128>(a, w)) return;          // the whole workgroup
+  const int begin = w.begin, end = w.end, dim = a.c.dim;
 
   // the lane's row and its queries
   const int r = w.row0 + 32 * wave + c;

@@ -29,13 +29,16 @@ struct AttnArgs {
   float scale;                               // times log2(e)
   const uint8_t* tree; int64_t tree_stride; int tree_width;
   // A tile is `rows` rows of a sequence and cache head; its number is slot * cache heads + head.  The first
-  // `whole` tiles take all their keys at once, the others are cut into `parts` each, joined afterwards.
-  int rows, slots, whole, parts;
-  float* part;                               // fp32 [cut tiles][parts][rows][dim] sums, then [cut tiles][rows][parts][2]
+  // `whole` tiles take all their keys at once, the others are cut into `parts` each, of whole units of `unit` keys, and
+  // joined afterwards.
+  int rows, slots, unit, whole, parts;
+  int64_t ids;                               // of parts
+  float* part;                               // fp32 [ids][rows][dim] sums, then [ids][rows][2]
 };
 // How a step's tiles are cut, for workspaces of at most `room` bytes.  reach: keys that the table can hold.
 struct AttnPlan {
-  int rows, slots, whole, parts;
+  int rows, slots, unit, whole, parts;
+  int64_t ids;
   size_t bytes;
 };
 AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, int64_t reach, size_t room);

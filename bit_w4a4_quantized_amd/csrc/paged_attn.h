@@ -100,22 +100,13 @@ __device__ __forceinline__ v4u transposed(const uint16_t* x, const uint16_t* y) 
 }
 
 // A workgroup's share: rows row0 ... of a sequence (token * group + query head of the group), a cache head
-// and a part of the keys.
+// and keys begin ... end - 1.
 struct Work {
-  int seq, head, split, parts, cut;          // cut: the tile's number among those that are cut
+  int seq, head;
   int s0, n, ctx, keys;                      // s0: first token; n: tokens; keys: context and tokens that have a slot
-  int row0, rows;
+  int row0, rows, begin, end;
+  int64_t id;                                // of its sums among all parts'; below 0: the tile has all its keys here
 
-  // One past the last key that any row up to `row` sees.
-  __device__ __forceinline__ int last_key(const AttnArgs& a, int row) const {
-    return a.tree ? keys : min(keys, ctx + min(row / a.group, n - 1) + 1);
-  }
-  __device__ __forceinline__ void part(int kmax, int unit, int* begin, int* end) const {
-    int each = (kmax + parts - 1) / parts;
-    each = (each + unit - 1) / unit * unit;
-    *begin = (int)min((int64_t)kmax, (int64_t)split * each);
-    *end = min(kmax, *begin + each);
-  }
   // Whether token i of the sequence sees an existing key.
   __device__ __forceinline__ bool sees(const AttnArgs& a, int i, int key) const {
     const int j = key - ctx;
@@ -125,14 +116,14 @@ struct Work {
   }
 };
 
-// The rows of a tile.  Tiles are numbered heads first (those of a cache head on one XCD, which share rows of the
-// cache where a sequence has several), then slots of rows, the last first: a chunk's last rows see the most keys.
-// Sequence i has the slots from floor(starts[i] group / R) + i on: one more than it may need, found without a
-// sum over the sequences.
+__device__ __forceinline__ int keys_of(const AttnArgs& a, int ctx, int n) {
+  return (int)min((int64_t)ctx + n, (int64_t)a.b.width << a.c.shift);
+}
+
+// The rows of a slot.  Sequence i has the slots from floor(starts[i] group / R) + i on: one more than it may need,
+// found without a sum over the sequences.
 template <int R>
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) {
-  w.head = tile % a.c.heads;
-  const int slot = a.slots - 1 - tile / a.c.heads;
+__device__ __forceinline__ bool find_rows(const AttnArgs& a, int slot, Work& w) {
   int s1;
   if (a.b.n <= 64) {                         // one look, at all that is asked of the sequence
     const int i = min(__lane_id(), a.b.n - 1);
@@ -158,24 +149,36 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) 
   const int64_t row0 = (slot - first) * R;
   if (row0 >= w.rows) return false;
   w.row0 = (int)row0;
+  w.keys = keys_of(a, w.ctx, w.n);
   return true;
 }
+// Tiles are numbered heads first (those of a cache head on one XCD, which share rows of the cache where a
+// sequence has several), then slots of rows, the last first: a chunk's last rows see the most keys.
 template <int R>
-__device__ __forceinline__ bool find_work(const AttnArgs& a, Work& w) {
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) {
+  w.head = tile % a.c.heads;
+  return find_rows<R>(a, a.slots - 1 - tile / a.c.heads, w);
+}
+
+// The workgroup's tile, or part of one.
+template <int R>
+__device__ __forceinline__ bool cut_work(const AttnArgs& a, Work& w) {
   const int id = blockIdx.x;
-  int tile = id;
-  w.split = w.cut = 0;
-  w.parts = 1;
+  int tile = id, split = 0, parts = 1;
+  w.id = -1;
   if (id >= a.whole) {
     const int cut = a.slots * a.c.heads - a.whole, u = id - a.whole;
-    w.split = u / cut;
-    w.cut = u - w.split * cut;
-    w.parts = a.parts;
-    tile = a.whole + w.cut;
+    split = u / cut;
+    parts = a.parts;
+    tile = a.whole + u - split * cut;
+    if (parts > 1) w.id = (int64_t)(tile - a.whole) * parts + split;
   }
   if (!find_tile<R>(a, tile, w)) return false;
-  const int64_t reach = (int64_t)a.b.width << a.c.shift;
-  w.keys = (int)min((int64_t)w.ctx + w.n, reach);
+  const int last = a.tree ? w.keys : min(w.keys, w.ctx + min((w.row0 + R - 1) / a.group, w.n - 1) + 1);
+  int each = (last + parts - 1) / parts;
+  each = (each + a.unit - 1) / a.unit * a.unit;
+  w.begin = (int)min((int64_t)last, (int64_t)split * each);
+  w.end = min(last, w.begin + each);
   return true;
 }
 
@@ -198,13 +201,11 @@ struct Dest {
 };
 template <int R>
 __device__ __forceinline__ Dest dest_of(const AttnArgs& a, const Work& w, int row) {
-  if (w.parts == 1) {
+  if (w.id < 0) {
     const int r = w.row0 + row, i = r / a.group, t = w.s0 + i, h = w.head * a.group + r - i * a.group;
     return {static_cast<uint16_t*>(a.o) + (int64_t)t * a.o_token + (int64_t)h * a.o_head, nullptr, nullptr};
   }
-  const int64_t cuts = (int64_t)a.slots * a.c.heads - a.whole;
-  return {nullptr, a.part + ((w.cut * (int64_t)w.parts + w.split) * R + row) * a.c.dim,
-          a.part + cuts * w.parts * R * a.c.dim + ((w.cut * (int64_t)R + row) * w.parts + w.split) * 2};
+  return {nullptr, a.part + (w.id * R + row) * a.c.dim, a.part + a.ids * R * a.c.dim + (w.id * R + row) * 2};
 }
 // Four of its values, from d on, with the row's maximum and sum.
 __device__ __forceinline__ void put(const Dest& to, bool bf, int d, const v4f& o, float m, float sum) {
