@@ -97,8 +97,6 @@ hipError_t join_dim(const AttnArgs& a, hipStream_t s) {
   return a.c.dim <= 64 ? join<R, 16>(a, s) : a.c.dim <= 128 ? join<R, 32>(a, s) : join<R, 64>(a, s);
 }
 
-constexpr int kManyRows = 128, kFewRows = 32;   // 16 or 32 where there are no more (32 of heads up to 128: registers)
-
 }  // namespace
 
 AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, int64_t reach, size_t room) {

@@ -99,6 +99,13 @@ __device__ __forceinline__ v4u transposed(const uint16_t* x, const uint16_t* y) 
   return v4u{p[0], p[1], q[0], q[1]};
 }
 
+constexpr int kManyRows = 128, kFewRows = 32;   // 16 or 32 where there are no more (32 of heads up to 128: registers)
+
+__host__ __device__ inline int64_t blocks_of(const AttnArgs& a) {
+  const int64_t tiles = (int64_t)a.slots * a.c.heads;
+  return a.whole + (tiles - a.whole) * a.parts;
+}
+
 // A workgroup's share: rows row0 ... of a sequence (token * group + query head of the group), a cache head
 // and keys begin ... end - 1.
 struct Work {
@@ -163,7 +170,14 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) 
 // The workgroup's tile, or part of one.
 template <int R>
 __device__ __forceinline__ bool cut_work(const AttnArgs& a, Work& w) {
-  const int id = blockIdx.x;
+  int id = blockIdx.x;
+  if (R <= kFewRows) {
+    // Eight slots' parts at a time, a head after the other: workgroups go round the eight XCDs, so that the heads of a
+    // part meet on one of them.  They share the cache lines of scales (and of short rows).
+    const int all = (int)blocks_of(a) / a.c.heads, g = id / (8 * a.c.heads), in = id - g * 8 * a.c.heads, m = min(8, all - 8 * g);
+    const int head = in / m;
+    id = (8 * g + in - head * m) * a.c.heads + head;
+  }
   int tile = id, split = 0, parts = 1;
   w.id = -1;
   if (id >= a.whole) {
@@ -222,10 +236,6 @@ __device__ __forceinline__ void put(const Dest& to, bool bf, int d, const v4f& o
   }
 }
 
-inline int64_t blocks_of(const AttnArgs& a) {
-  const int64_t tiles = (int64_t)a.slots * a.c.heads;
-  return a.whole + (tiles - a.whole) * a.parts;
-}
 hipError_t launch_few(const AttnArgs& a, hipStream_t s);
 hipError_t launch_many(const AttnArgs& a, hipStream_t s);
 
