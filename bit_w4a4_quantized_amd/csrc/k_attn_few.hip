@@ -157,10 +157,10 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
 #pragma unroll
       for (int n = 0; n < NT; n++) {
         seen[n] = 0;
-#pragma unroll 1
-        for (int e = 0; e < 8; e++) {
-          const int k = (e >> 2) * 16 + quad * 4 + (e & 3);
-          if (valid[n] && (live >> k & 1) && w.sees(a, tok[n], base + k)) seen[n] |= 1u << e;
+#pragma unroll 1                             // (unrolled, 64 x 8000 int8 took 207 us for 169)
+        for (int t = 0; t < 2; t++) {
+          const int k = 16 * t + 4 * quad;
+          seen[n] |= (w.sees4(a, tok[n], base + k) & (live >> k)) << (4 * t);
         }
       }
     }

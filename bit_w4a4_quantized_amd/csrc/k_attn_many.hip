@@ -324,10 +324,10 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     const int sure = a.tree ? w.ctx : w.ctx + wave_first + 1;      // keys below it are seen by all of the wave's rows
     if (base + BN > sure || live != kAll) {  // the same in every lane
       uint32_t seen = 0;
-#pragma unroll 1
-      for (int e = 0; e < 16 * NB; e++) {
-        const int k = (e >> 2) * 8 + 4 * half + (e & 3);
-        if (valid && (live >> k & 1) && w.sees(a, tok, base + k)) seen |= 1u << e;
+#pragma unroll
+      for (int g = 0; g < 4 * NB; g++) {
+        const int k = 8 * g + 4 * half;
+        seen |= (w.sees4(a, tok, base + k) & (uint32_t)(live >> k)) << (4 * g);
       }
 #pragma unroll
       for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = seen >> e & 1 ? st[e >> 4][e & 15] : -INFINITY;

@@ -121,6 +121,28 @@ struct Work {
     if (!a.tree) return j <= i;
     return j < a.tree_width && a.tree[(int64_t)(s0 + i) * a.tree_stride + j];
   }
+  // The same of keys key ... key + 3, a bit each.  Of a tree's row one load of four marks, moved to where it lies
+  // within the row, and no branches: the loads of a lane's keys are in flight together.
+  __device__ __forceinline__ uint32_t sees4(const AttnArgs& a, int i, int key) const {
+    const int j = key - ctx;
+    if (!a.tree) return (1u << min(max(i - j + 1, 0), 4)) - 1;
+    uint32_t bits = 0;
+    if (a.tree_width >= 4) {
+      const int at = min(max(j, 0), a.tree_width - 4), by = 8 * min(max(j - at, -4), 4);
+      uint32_t x;
+      __builtin_memcpy(&x, a.tree + (int64_t)(s0 + i) * a.tree_stride + at, 4);
+      x = (uint32_t)(by < 0 ? (uint64_t)x << -by : (uint64_t)x >> by);
+      x |= x >> 4;                           // a mark is any value but 0
+      x |= x >> 2;
+      x |= x >> 1;
+      x &= 0x01010101u;
+      bits = (x | x >> 7 | x >> 14 | x >> 21) & 0xFu;
+    } else {
+      for (int e = 0; e < 4; e++)
+        if (j + e >= 0 && j + e < a.tree_width && a.tree[(int64_t)(s0 + i) * a.tree_stride + j + e]) bits |= 1u << e;
+    }
+    return bits | ((1u << min(max(-j, 0), 4)) - 1);    // the context's
+  }
 };
 
 __device__ __forceinline__ int keys_of(const AttnArgs& a, int ctx, int n) {
