@@ -21,6 +21,11 @@ inline bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 inline bool eps_ok(float e) { return isfinite(e) && e > 0.f; }
 inline bool power_of_two(int n) { return n > 0 && (n & (n - 1)) == 0; }
 
+// Tiles of at least 16 rows: what 32-bit numbers of tiles and of their parts hold.
+inline bool tiles_ok(int tokens, int heads, int kv_heads, int sequences) {
+  return ((int64_t)tokens * (heads / kv_heads) / 16 + sequences) * kv_heads <= 1 << 24;
+}
+
 svdq_status map_launch(hipError_t e) {
   if (e == hipSuccess) return SVDQ_OK;
   if (e == hipErrorInvalidConfiguration) return SVDQ_ERR_SHAPE;   // !launchable
@@ -138,7 +143,7 @@ svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_
   if (st != SVDQ_OK) return st;
   if (tokens < 0 || tokens > kMaxDim || heads < 1 || heads > kMaxHeads || heads % cache->heads) return SVDQ_ERR_SHAPE;
   if ((int64_t)tokens * heads >= (int64_t)1 << 31 || !isfinite(scale) || scale <= 0.f) return SVDQ_ERR_SHAPE;
-  if (((int64_t)tokens * (heads / cache->heads) / 16 + batch->sequences) * cache->heads > 1 << 24) return SVDQ_ERR_SHAPE;
+  if (!tiles_ok(tokens, heads, cache->heads, batch->sequences)) return SVDQ_ERR_SHAPE;
   for (const int64_t s : {q_token, q_head, out_token, out_head})
     if (!stride_ok(s)) return SVDQ_ERR_SHAPE;
   if (tree && (!stride_ok(tree_stride) || tree_width < 0)) return SVDQ_ERR_SHAPE;
@@ -180,7 +185,8 @@ size_t svdq_tree_attention_workspace_bytes(int sequences, int tokens, int heads,
                                            int page_size) {
   if (sequences < 1 || tokens < 1 || kv_heads < 1 || heads < kv_heads || heads % kv_heads || heads > kMaxHeads ||
       tokens > kMaxDim || sequences > kMaxDim || dim < 8 || dim > kMaxHeadDim || table_width < 0 || page_size < 1 ||
-      (int64_t)tokens * heads >= (int64_t)1 << 31)
+      (int64_t)tokens * heads >= (int64_t)1 << 31 || (int64_t)table_width * page_size > (int64_t)1 << 30 ||
+      !tiles_ok(tokens, heads, kv_heads, sequences))
     return 0;
   return attn_plan(sequences, tokens, heads, kv_heads, dim, (int64_t)table_width * page_size, ~(size_t)0).bytes;
 }

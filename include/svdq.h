@@ -555,15 +555,19 @@ svdq_status svdq_rope_append(const svdq_paged_cache* cache, const svdq_paged_bat
  * the slots below the sequence's context, and of the step's own tokens the j-th where
  *   tree[t, j] != 0 (a byte; j >= tree_width: not seen)    with a tree,
  *   j <= i                                                 without (a chain: one token, or a chunk of a prompt).
- * A row that sees nothing is zeros.  What a token does not see has no effect on it, infinities and NaN included.
+ * A row that sees nothing is zeros (and so is one whose logits are all minus infinity).  What a token does not see
+ * has no effect on it, infinities and NaN included.
  *   q, out : [tokens, heads, dim] of `type` by their strides; heads a multiple of the cache's.  out may be q with
  *            the same strides.  Rows of tokens that belong to no sequence are left as they were.
+ *   tokens * heads < 2^31, and (tokens * (heads / cache heads) / 16 + sequences) * cache heads <= 2^24.
  *   scale  : finite, > 0.
  *   tree   : bytes [tokens, tree_width], rows tree_stride apart, or NULL.
  * Logits, the softmax's statistics and sums are fp32; probabilities are rounded to 16 bits for the matrix
- * cores (to fp16 with an 8-bit cache, whose scales of values join them there).
+ * cores (to fp16 with an 8-bit cache, whose scales of values join them there).  They are taken relative to a
+ * maximum that may lag by 2^8: sums of values of a bf16 cache from 2^119 on can leave fp32's range.
  *   workspace, workspace_bytes : caller-owned device scratch, 16-byte aligned, for the sums of the keys' parts
- *            where there are few rows (svdq_tree_attention_workspace_bytes); rules as for svdq_gemm_act_residual's.
+ *            where rows alone do not fill the chip (svdq_tree_attention_workspace_bytes); rules as for
+ *            svdq_gemm_act_residual's.
  */
 svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_batch* batch, const void* q,
                                 int64_t q_token, int64_t q_head, int heads, int tokens, svdq_type type, float scale,
