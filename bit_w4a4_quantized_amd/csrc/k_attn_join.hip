@@ -84,8 +84,10 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
 template <int R, int P>
 hipError_t join(const AttnArgs& a, hipStream_t s) {
   const int64_t cuts = (int64_t)a.slots * a.c.heads - a.whole;
-  int deep = 1;                              // ways: four parts or more for each
-  while (deep < 256 / P && deep * 8 <= a.parts) deep *= 2;
+  // Ways: so many that each one's parts are on their way before it looks for its tile, or, where the workgroups fill
+  // the chip, has eight or more (8 tiles of 16 parts: 5.7 us with 2, 3.3 with 4; 512 tiles of 6: 6.1 with 1, 8.9 with 2).
+  int deep = 1;
+  while (deep < 256 / P && deep * 4 <= a.parts && (deep * 8 <= a.parts || cuts * R * P * deep < 256 * 256)) deep *= 2;
   const int64_t blocks = cuts * (R / (256 / P / deep));
   if (!launchable(blocks, 256)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((k_attn_join<R, P>), dim3((unsigned)blocks), dim3(256), 0, s, a, deep);
@@ -104,11 +106,14 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   const int group = heads / kv_heads;
   const int64_t each = ((int64_t)tokens * group + sequences - 1) / sequences;    // rows of a sequence and cache head
   p.rows = each > kFewRows ? kManyRows : each > 16 && dim <= 128 ? kFewRows : 16;
-  p.unit = p.rows <= kFewRows ? 128 : dim > 128 ? 32 : 64;
+  p.unit = dim > 128 && p.rows > kFewRows ? 32 : 64;
   p.slots = (int)((int64_t)tokens * group / p.rows + sequences);
   const int64_t all = (int64_t)p.slots * kv_heads;
   const int64_t tiles = (each + p.rows - 1) / p.rows * sequences * kv_heads;     // not empty, for sequences alike
-  const int64_t most = reach / 128;
+  // A part has 64 keys or more, two turns of k_attn_few's four waves: a compute unit alone takes about six bytes a
+  // clock from beyond its L2, so that a short context comes faster to more of them (1000 keys of 8 heads 11.2 us in
+  // parts of 128, 8.6 of 64, 8.5 of 32).
+  const int64_t most = reach / (p.rows <= kFewRows ? 64 : 128);
   p.whole = (int)all;
   p.parts = 1;
   const size_t id_bytes = (size_t)p.rows * (dim + 2) * sizeof(float);
