@@ -8,9 +8,17 @@
     y        = fc2(gelu(fc1(h)))      svdq_linear_folded and svdq_linear, W4A4 with their low-rank branches
     x        = x + y                  the next block's svdq_add_rmsnorm
 
-The attention between is torch's: this library has none.  Weights are random.
+The attention between is torch's, of all tokens to all.  With a paged cache of keys and values the block
+takes a step's tokens of several sequences instead, each seeing what came before it:
+
+    q        = turn(norm(q)); k, v to the cache          svdq_rope_append
+    a        = attn(q, the sequence's cache)             svdq_tree_attention, a chain or a tree of drafted tokens
+    the tokens kept of a draft, moved together           svdq_cache_keep, once for all blocks' caches
+
+Weights are random.
 
     python examples/transformer_block.py            # sizes of a 3072-wide block, 4608 tokens
+    python examples/transformer_block.py --cached   # prompts, a drafted tree and its accepted path
 """
 from __future__ import annotations
 
@@ -50,18 +58,24 @@ class Block:
         # fc1's smoothing divides its input's channels: folded into the norm's weight
         self.n2 = (r["n2"] / torch.from_numpy(self.h1.lam)).cuda()
 
-    def __call__(self, x, y, positions):
-        """x fp16 [T, dim], the stream; y the previous block's MLP output (or None); returns (x, y)."""
+    def __call__(self, x, y, positions, cache=None, batch=None, tree=None):
+        """x fp16 [T, dim], the stream; y the previous block's MLP output (or None); returns (x, y).  With cache
+        and batch the tokens are a step's, appended to their sequences."""
         T, D, H = x.shape[0], self.dim, self.heads
         codes, scales, stream = binding.svdq_add_rmsnorm(x if y is None else y, self.n1, residual=None if y is None else x,
                                                          out_format=self.w8)
         x = x if stream is None else stream
         qkv = binding.svdq_gemm_act_residual(codes, self.wqkv, scales, self.wqkv_s, self.bqkv)
         heads = lambda i: qkv[:, i * D:(i + 1) * D].unflatten(-1, (H, D // H))  # noqa: E731
-        q, k = binding.svdq_rope_axes(heads(0), heads(1), positions, self.freq, self.axis_pairs, q_weight=self.qn,
-                                      k_weight=self.kn, heads_first=True)
-        a = torch.nn.functional.scaled_dot_product_attention(q[None], k[None], heads(2).transpose(0, 1)[None])
-        a = a[0].transpose(0, 1).reshape(T, D)
+        if cache is not None:
+            q = binding.svdq_rope_append(cache, batch, heads(0), heads(1), heads(2), positions, self.freq, self.axis_pairs,
+                                         q_weight=self.qn, k_weight=self.kn)
+            a = binding.svdq_tree_attention(cache, batch, q, tree=tree).view(T, D)
+        else:
+            q, k = binding.svdq_rope_axes(heads(0), heads(1), positions, self.freq, self.axis_pairs, q_weight=self.qn,
+                                          k_weight=self.kn, heads_first=True)
+            a = torch.nn.functional.scaled_dot_product_attention(q[None], k[None], heads(2).transpose(0, 1)[None])
+            a = a[0].transpose(0, 1).reshape(T, D)
         x = binding.svdq_gemm_act_residual(a, self.wo, bias=self.bo, residual=x)
         h, _, _ = binding.svdq_add_rmsnorm(x, self.n2, out_format="same")
         f1, f2 = self.fc1, self.fc2
@@ -118,5 +132,65 @@ def main(dim=3072, heads=24, ffn=12288, axis_pairs=(8, 28, 28), text=512, side=6
     return rel(x, px), rel(y, py)
 
 
+class Serving:
+    """A stack of blocks over paged caches, one a block, with a page table shared by all."""
+
+    def __init__(self, blocks, sequences, longest, page=64, kind=torch.float8_e4m3fn):
+        self.blocks, self.page = blocks, page
+        width = -(-longest // page)
+        self.caches = [binding.PagedCache.empty(sequences * width, page, b.heads, b.dim // b.heads, kind) for b in blocks]
+        # any page may serve any sequence
+        self.table = torch.randperm(sequences * width).view(sequences, width).to(torch.int32).cuda()
+        self.length = torch.zeros(sequences, dtype=torch.int32, device="cuda")
+
+    def step(self, x, counts, depth=None, tree=None):
+        """x fp16 [tokens, dim]: counts[b] tokens of each sequence b, one behind the other; the blocks' (x, y) and the
+        batch, for keep.  depth [tokens]: how far behind its sequence's context a token of a tree is (a chain: its
+        number)."""
+        starts = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+        batch = binding.PagedBatch(self.table, starts, self.length.clone())
+        of = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts)).cuda()
+        at = torch.arange(len(x), device="cuda") - starts[of] if depth is None else depth
+        axes = len(self.blocks[0].axis_pairs)
+        positions = (self.length[of] + at).to(torch.int32)[:, None].expand(-1, axes).contiguous()
+        y = None
+        for block, cache in zip(self.blocks, self.caches):
+            x, y = block(x, y, positions, cache, batch, tree)
+        self.length += torch.tensor(counts, dtype=torch.int32).cuda()
+        return x, y, batch
+
+    def keep(self, batch, path):
+        """Of the last step's tokens only a path's stay: int32 [sequences, width], negative behind a path's end."""
+        path = path.cuda()
+        for cache in self.caches:
+            binding.svdq_cache_keep(cache, batch, path)
+        self.length.copy_(batch.context + (path >= 0).sum(1).to(torch.int32))
+
+
+def cached(dim=3072, heads=24, ffn=12288, axis_pairs=(64,), prompts=(700, 64, 1300), blocks=2):
+    """Prompts, a tree of drafted tokens for each sequence, an accepted path of it and one more token; the last
+    token's output."""
+    torch.manual_seed(0)
+    net = Block(dim, heads, ffn, axis_pairs)
+    serving = Serving([net] * blocks, len(prompts), max(prompts) + 16)
+    rand = lambda n: torch.randn(n, dim).half().cuda()  # noqa: E731
+    serving.step(rand(sum(prompts)), list(prompts))
+    parent = [-1, 0, 0, 1, 1, 2, 4]
+    sees, depth = torch.eye(len(parent), dtype=torch.bool), [0] * len(parent)
+    for i, up in enumerate(parent):
+        if up >= 0:
+            sees[i] |= sees[up]
+            depth[i] = depth[up] + 1
+    n = len(prompts)
+    _, _, batch = serving.step(rand(n * len(parent)), [len(parent)] * n, torch.tensor(depth).cuda().repeat(n),
+                               sees.repeat(n, 1).cuda())
+    accepted = torch.tensor([[0, 1, 4, 6], [0, 2, -1, -1], [0, 2, 5, -1]])[torch.arange(n) % 3].to(torch.int32)
+    serving.keep(batch, accepted)
+    x, y, _ = serving.step(rand(n), [1] * n)
+    torch.cuda.synchronize()
+    print(f"lengths {serving.length.tolist()}, last outputs finite: {bool(torch.isfinite(x + y).all())}")
+    return x + y
+
+
 if __name__ == "__main__":
-    main()
+    cached() if "--cached" in sys.argv[1:] else main()
