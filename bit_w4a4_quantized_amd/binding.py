@@ -1064,7 +1064,7 @@ def svdq_rope_append(cache, batch, q, k, v, positions, inv_freq, axis_pairs, pai
             _vector(q_weight, d.f32, cache.dim, "q_weight")
             ops[0].weight = q_weight.data_ptr()
         if q_out is None:
-            q_out = torch.empty_like(q) if stream is None and q.is_contiguous() else _new(stream, q.shape, dtype, q.device)
+            q_out = _rope_out(q, q.shape, stream)
         ops[0].inp, ops[0].out = q.data_ptr(), q_out.data_ptr()
     _launch("svdq_rope_append",
             (cache._at, batch._at, None if q is None else at, at + _OPERAND_BYTES, v.data_ptr(), *v_step, tokens,
@@ -1130,7 +1130,7 @@ def svdq_tree_attention(cache, batch, q, tree=None, scale=None, out=None, worksp
         if room:
             workspace = _new_workspace(stream, room, q.device)
     if out is None:
-        out = torch.empty_like(q) if stream is None and q.is_contiguous() else _new(stream, q.shape, dtype, q.device)
+        out = _rope_out(q, q.shape, stream)
     _launch("svdq_tree_attention",
             (cache._at, batch._at, q.data_ptr(), q_step[0], q_step[1], heads, tokens, d.code[dtype], scale, at, t_step,
              t_width, out.data_ptr(), o_step[0], o_step[1], _p(workspace), room), given, stream)

@@ -5,8 +5,11 @@
 //   keys     turn(norm(k)) to slot context[b] + i of the token's sequence b, rounded once: to the cache's
 //            16-bit type, or to codes rnd(u * (qmax / a)) with the scale a / qmax, a = max(max|u|, 2^-100)
 //            over the head (qmax 127 or 448);  values the same way, neither normed nor turned.
-// HBM bounds it at many tokens (each value read once and written once), latency at few: everything is one
-// launch, and a wave loads its heads before it looks for their sequence and page.
+// Latency bounds few tokens: everything is one launch, and a wave loads its heads before it looks for their sequence
+// and page (64 tokens of 32 + 16 heads of 128 5.7 us).  Many are bound by HBM and the vector unit together: 16384 tokens
+// of 24 + 48 heads of 128 to E4M3 codes, 509 MB, take 130 us, 3.9 TB/s of the 4.9 that a large copy reaches, with the
+// vector unit busy for three quarters of it (the norm, the angles, codes).  Three heads a lane group instead of two: an
+// eighth fewer instructions, 135 us (four waves a SIMD for five).
 #include "paged.h"
 #include "rope.h"
 
@@ -324,8 +327,8 @@ bool wide(const AppendArgs& a) {
 // Each kept token to its place: slot context + i takes slot context + path[i].  A thread has one piece of a
 // head's keys or values (or a scale) over the whole path, in the path's order and kKeepAhead places at a time, so
 // that rising paths (path[i] >= i) need no other room: a place is read before it or a later turn writes it.
-// Latency bounds it: the path, the table, the values and the stores, each of a turn's places at once (256 paths of 8
-// tokens of 8 heads of 128 E4M3 codes, 8.6 MB each way: 7.0 us; one place after the other 12.5).
+// Latency bounds it: the path, the table, the values and the stores, each of a turn's places at once (256 paths of up
+// to 8 tokens of 8 heads of 128 E4M3 codes, 2 MB moved: 6.6 us; one place after the other 12.5).
 constexpr int kKeepAhead = 8;
 __device__ const uint4 kNothing[1] = {};     // what places that are left as they are read
 template <typename T, typename P>
