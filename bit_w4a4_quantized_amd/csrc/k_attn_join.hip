@@ -131,10 +131,10 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
     // The tiles of the last, partial round are cut so that it fills the chip (in rounds of whole tiles: the parts'
     // own, half a part for the workgroups that end early, and the join).
     const int64_t rest = tiles % resident;
-    const double early = tiles > resident ? 0.5 : 0.0;
+    const double early = tiles > resident ? 0.5 : 0.0, join = reach > 8192 ? 0.02 * 8192 / reach : 0.02;
     double best = 1.0 + early;
-    for (int s = 2; s <= 16 && s <= most && rest; s++) {
-      const double t = (double)((rest * s + resident - 1) / resident) / s + early / s + 0.02 * s;
+    for (int s = 2; (s <= 16 || rest * s <= resident) && s <= most && rest; s++) {
+      const double t = (double)((rest * s + resident - 1) / resident) / s + early / s + join * s;
       if (t < 0.95 * best) {
         best = t;
         p.parts = s;

@@ -236,14 +236,16 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   auto clean = [&](uint16_t* vt, float (*sc)[CK == C16 ? 4 : BN]) {
     bool found = false;
     if (CK != CI8) {
-#pragma unroll 1
-      for (int i = threadIdx.x; i < BN * DP / 8; i += 256) {
-        v4u x = *reinterpret_cast<const v4u*>(vt + i * 8);
-        if (make_finite<BF>(x)) {
-          *reinterpret_cast<v4u*>(vt + i * 8) = x;
+      constexpr int kMine = BN * DP / 8 / 256;
+      v4u x[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; i++) x[i] = *reinterpret_cast<const v4u*>(vt + (threadIdx.x + 256 * i) * 8);
+#pragma unroll
+      for (int i = 0; i < kMine; i++)
+        if (make_finite<BF>(x[i])) {
+          *reinterpret_cast<v4u*>(vt + (threadIdx.x + 256 * i) * 8) = x[i];
           found = true;
         }
-      }
     }
     if (CK != C16 && threadIdx.x < BN && !(__builtin_fabsf(sc[1][CK == C16 ? 0 : threadIdx.x]) < INFINITY)) {
       sc[1][CK == C16 ? 0 : threadIdx.x] = 0.f;
