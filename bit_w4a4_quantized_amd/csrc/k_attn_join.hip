@@ -131,7 +131,7 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
     // The tiles of the last, partial round are cut so that it fills the chip (in rounds of whole tiles: the parts'
     // own, half a part for the workgroups that end early, and the join).
     const int64_t rest = tiles % resident;
-    const double early = tiles > resident ? 0.5 : 0.0, join = reach > 8192 ? 0.02 * 8192 / reach : 0.02;
+    const double early = tiles > resident ? 0.5 : 0.0, join = 0.02 * 8192 / reach;
     double best = 1.0 + early;
     for (int s = 2; (s <= 16 || rest * s <= resident) && s <= most && rest; s++) {
       const double t = (double)((rest * s + resident - 1) / resident) / s + early / s + join * s;
