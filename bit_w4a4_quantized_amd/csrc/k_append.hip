@@ -66,7 +66,7 @@ __device__ __forceinline__ int slot_of(const AppendArgs& a, int seq, int t) {
 __device__ __forceinline__ float inv_qmax(int type) { return type == T_INT8 ? 1.f / 127.f : 1.f / 448.f; }
 __device__ __forceinline__ float qmax(int type) { return type == T_INT8 ? 127.f : 448.f; }
 
-enum Form { ADJACENT, PARTIAL, HALVES };     // as in k_rope.hip
+enum Form { ADJACENT, PARTIAL, HALVES, HALVES_PARTIAL };     // as in k_rope.hip, and halves of a part of the head
 
 struct Split {
   int tw, batches, waves, heads;             // tokens a wave; parts of a token's heads; waves; heads
@@ -90,7 +90,19 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a, int lanes, Splits 
   const RopeOperand& o = r.op[which];
   const int groups = 64 / lanes, j = lane % lanes, g = lane / lanes;
   const int nv = r.dim / 8, half = (nv + 1) / 2, pairs = r.dim / 2;
-  const bool in0 = j < half, in1 = j + half < nv;
+  // The lane's two pieces: half a head apart, of a part of the head that halves turn half of that apart, and behind it
+  // half of what is left.
+  int first_piece = j, second_piece = j + half;
+  if (FORM == HALVES_PARTIAL) {
+    const int apart = r.pairs / 8;
+    if (j < apart) {
+      second_piece = j + apart;
+    } else {
+      first_piece = j + apart;
+      second_piece = first_piece + (nv - 2 * apart + 1) / 2;
+    }
+  }
+  const bool in0 = j < half, in1 = j < half && second_piece < nv;
   const int part = id % w_.batches, t0 = id / w_.batches * w_.tw;
   const int nt = min(w_.tw, r.tokens - t0);
   const int first = part * U * groups, last = min(nt * w_.heads, first + U * groups);
@@ -110,8 +122,8 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a, int lanes, Splits 
       if (is_v[i]) hd[i] -= a.c.heads;
       const uint16_t* p = is_v[i] ? static_cast<const uint16_t*>(a.v) + t * a.v_token + hd[i] * a.v_head
                                   : static_cast<const uint16_t*>(o.in) + t * o.in_token + hd[i] * o.in_head;
-      if (in0) raw[i][0] = *reinterpret_cast<const uint4*>(p + j * 8);
-      if (in1) raw[i][1] = *reinterpret_cast<const uint4*>(p + (j + half) * 8);
+      if (in0) raw[i][0] = *reinterpret_cast<const uint4*>(p + first_piece * 8);
+      if (in1) raw[i][1] = *reinterpret_cast<const uint4*>(p + second_piece * 8);
     }
   }
   int seq = 0;
@@ -128,7 +140,7 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a, int lanes, Splits 
   float w[2][8];
   if (norm) {
 #pragma unroll
-    for (int v = 0; v < 2; v++) __builtin_memcpy(w[v], o.weight + min((j + v * half) * 8, r.dim - 8), 32);
+    for (int v = 0; v < 2; v++) __builtin_memcpy(w[v], o.weight + min((v ? second_piece : first_piece) * 8, r.dim - 8), 32);
   }
   Place place[U];
   if (which) {
@@ -178,11 +190,11 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a, int lanes, Splits 
       // the lane's eight pairs: of its two pieces (adjacent), or between them (half apart)
 #pragma unroll
       for (int v = 0; v < 2; v++) {
-        const int p = tl[i] * pairs + min(FORM == HALVES ? j * 8 + v * 4 : (j + v * half) * 4, pairs - 4);
+        const int p = tl[i] * pairs + min(FORM >= HALVES ? j * 8 + v * 4 : (j + v * half) * 4, pairs - 4);
         *reinterpret_cast<float4*>(c + 4 * v) = *reinterpret_cast<const float4*>(&table[wave][0][p]);
         *reinterpret_cast<float4*>(s + 4 * v) = *reinterpret_cast<const float4*>(&table[wave][1][p]);
       }
-      if (FORM == HALVES) {
+      if (FORM >= HALVES) {
 #pragma unroll
         for (int e = 0; e < 8; e++) {
           y[0][e] = u[0][e] * c[e] - u[1][e] * s[e];
@@ -206,18 +218,25 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a, int lanes, Splits 
           for (int e = 0; e < 8; e++)
             if ((j + v * half) * 4 + e / 2 >= r.pairs) y[v][e] = u[v][e];
       }
+      if (FORM == HALVES_PARTIAL) {
+#pragma unroll
+        for (int v = 0; v < 2; v++)
+#pragma unroll
+          for (int e = 0; e < 8; e++)
+            if (j >= r.pairs / 8) y[v][e] = u[v][e];
+      }
     }
     if (!which) {
       if (hd[i] < 0) continue;
       uint16_t* out = static_cast<uint16_t*>(o.out) + (int64_t)(t0 + tl[i]) * o.out_token + hd[i] * o.out_head;
-      if (in0) stream16(out + j * 8, pack8(y[0], BF));
-      if (in1) stream16(out + (j + half) * 8, pack8(y[1], BF));
+      if (in0) stream16(out + first_piece * 8, pack8(y[0], BF));
+      if (in1) stream16(out + second_piece * 8, pack8(y[1], BF));
     } else if (a.c.type == T_F16 || a.c.type == T_BF16) {
       if (place[i].at < 0) continue;
       uint16_t* out = static_cast<uint16_t*>(is_v[i] ? a.c.v : a.c.k) + place[i].at + hd[i] * a.c.head;
       // nontemporal as the queries' (k_rope.hip)
-      if (in0) stream16(out + j * 8, is_v[i] ? raw[i][0] : pack8(y[0], BF));
-      if (in1) stream16(out + (j + half) * 8, is_v[i] ? raw[i][1] : pack8(y[1], BF));
+      if (in0) stream16(out + first_piece * 8, is_v[i] ? raw[i][0] : pack8(y[0], BF));
+      if (in1) stream16(out + second_piece * 8, is_v[i] ? raw[i][1] : pack8(y[1], BF));
     } else {
       // lanes past a head's end hold zeros turned by the last pairs: zeros
       float top = 0.f;
@@ -230,8 +249,8 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a, int lanes, Splits 
       if (place[i].at < 0) continue;
       const float mul = qmax(a.c.type) / top;
       uint8_t* out = static_cast<uint8_t*>(is_v[i] ? a.c.v : a.c.k) + place[i].at + hd[i] * a.c.head;
-      if (in0) *reinterpret_cast<uint2*>(out + j * 8) = codes8(y[0], mul, a.c.type);
-      if (in1) *reinterpret_cast<uint2*>(out + (j + half) * 8) = codes8(y[1], mul, a.c.type);
+      if (in0) *reinterpret_cast<uint2*>(out + first_piece * 8) = codes8(y[0], mul, a.c.type);
+      if (in1) *reinterpret_cast<uint2*>(out + second_piece * 8) = codes8(y[1], mul, a.c.type);
       if (j == 0) (is_v[i] ? a.c.vs : a.c.ks)[place[i].sat + hd[i] * a.c.shead] = top * inv_qmax(a.c.type);
     }
   }
@@ -314,7 +333,7 @@ __global__ void __launch_bounds__(256) k_append_any(AppendArgs a, int64_t units)
 
 bool wide(const AppendArgs& a) {
   const RopeArgs& r = a.r;
-  if (r.halves && (2 * r.pairs != r.dim || r.dim % 16)) return false;
+  if (r.halves && r.pairs % 8) return false;
   uintptr_t p = reinterpret_cast<uintptr_t>(r.op[1].in) | reinterpret_cast<uintptr_t>(a.v);
   int64_t st = r.op[1].in_token | r.op[1].in_head | a.v_token | a.v_head;
   if (r.op[0].heads) {
@@ -423,7 +442,8 @@ hipError_t launch_append(const AppendArgs& a, hipStream_t s) {
     blocks += (waves + 3) / 4;
   }
   if (!launchable(blocks, 256)) return hipErrorInvalidConfiguration;
-  const auto k = r.halves                ? (bf ? k_append<true, HALVES, U> : k_append<false, HALVES, U>)
+  const auto k = r.halves && 2 * r.pairs < r.dim ? (bf ? k_append<true, HALVES_PARTIAL, U> : k_append<false, HALVES_PARTIAL, U>)
+                 : r.halves              ? (bf ? k_append<true, HALVES, U> : k_append<false, HALVES, U>)
                  : 2 * r.pairs < r.dim ? (bf ? k_append<true, PARTIAL, U> : k_append<false, PARTIAL, U>)
                                        : (bf ? k_append<true, ADJACENT, U> : k_append<false, ADJACENT, U>);
   hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(256), 0, s, a, lanes, sp);

@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 from bit_w4a4_quantized_amd import binding  # noqa: E402
 from test_gpu_block import BF16, E4M3, F16, U, check, gen, randn  # noqa: E402
-from test_gpu_cache import (I8, KINDS, QMAX, Pages, _gpu, attend, attention64, attention_case, random_tree,  # noqa: E402, F401
+from test_gpu_cache import (I8, KINDS, QMAX, Pages, _gpu, append_case, attend, attention64, attention_case, random_tree,  # noqa: E402, F401
                             raw)
 
 
@@ -202,3 +202,39 @@ def test_batches_that_hold_anything(cache):
         if t is not None:
             assert torch.equal(raw(p.dev[name]).cpu(), raw(t))
     assert torch.equal(attend(p, q.cpu(), None), before)
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("dim,pairs", [(64, 16), (64, 24), (80, 8), (80, 32), (96, 40), (128, 32), (128, 8), (256, 64), (256, 120),
+                                       (208, 56), (32, 8)])
+def test_append_halves_of_a_part(dim, pairs, dtype, cache):
+    """Pairs half of the turned part apart, the rest of the head as it is."""
+    append_case([1, 5, 0, 3], [40, 7, 9, 0], 5, 3, dim, dtype, cache, 8, (pairs // 2, pairs - pairs // 2), "halves", dim != 64)
+
+
+@pytest.mark.parametrize("dim,pairs", [(72, 8), (72, 24), (88, 40), (136, 8), (24, 8)])
+def test_append_halves_of_a_part_odd(dim, pairs):
+    append_case([2, 7], [5, 1], 3, 2, dim, BF16, BF16, 16, (pairs,), "halves", True)
+    append_case([2, 7], [5, 1], 3, 2, dim, F16, F16, 16, (pairs,), "halves", False)
+
+
+def test_append_halves_of_a_part_several_tokens_a_wave():
+    counts = [1 + (b * 7) % 5 for b in range(1500)]
+    append_case(counts, [b % 3 for b in range(1500)], 2, 1, 64, F16, E4M3, 4, (16,), "halves", True, behind=5)
+
+
+@pytest.mark.parametrize("pairs", ["adjacent", "halves"])
+def test_append_keeps_what_lies_behind_the_pairs(pairs):
+    """Infinities, NaN and minus zero behind the turned part stay where they are."""
+    g = gen(68)
+    p = Pages(g, [3], [2], 1, 64, F16, 8)
+    q, k, v = (randn(g, 3, h, 64).to(F16) for h in (2, 1, 1))
+    for t in (q, k):
+        t[..., 32:] = torch.tensor([float("inf"), float("nan"), -0.0, 7.0] * 8).to(F16)
+    pos, freq = torch.arange(3, dtype=torch.int32, device="cuda")[:, None].contiguous(), torch.full((16,), 0.3, device="cuda")
+    got = binding.svdq_rope_append(p.cache, p.batch, q.cuda(), k.cuda(), v.cuda(), pos, freq, (16,), pairs).cpu()
+    assert torch.equal(got[..., 32:].view(torch.int16), q[..., 32:].view(torch.int16)) and bool(torch.isfinite(got[..., :32]).all())
+    for t in range(3):
+        at = p.dev["k"][int(p.table[0, (2 + t) // 8]), (2 + t) % 8].cpu()
+        assert torch.equal(at[..., 32:].view(torch.int16), k[t, :, 32:].view(torch.int16))
+        assert bool(torch.isfinite(at[..., :32]).all())
