@@ -562,6 +562,7 @@ svdq_status svdq_rope_append(const svdq_paged_cache* cache, const svdq_paged_bat
  *   tokens * heads < 2^31, and (tokens * (heads / cache heads) / 16 + sequences) * cache heads <= 2^24.
  *   scale  : finite, > 0.
  *   tree   : bytes [tokens, tree_width], rows tree_stride apart, or NULL.
+ * The work is cut by the mean number of rows of a sequence: long chunks and single tokens are best in calls of their own.
  * Logits, the softmax's statistics and sums are fp32; probabilities are rounded to 16 bits for the matrix
  * cores (to fp16 with an 8-bit cache, whose scales of values join them there).  They are taken relative to a
  * maximum that may lag by 2^8: sums of values of a bf16 cache from 2^119 on can leave fp32's range.
