@@ -238,3 +238,33 @@ def test_append_keeps_what_lies_behind_the_pairs(pairs):
         at = p.dev["k"][int(p.table[0, (2 + t) // 8]), (2 + t) % 8].cpu()
         assert torch.equal(at[..., 32:].view(torch.int16), k[t, :, 32:].view(torch.int16))
         assert bool(torch.isfinite(at[..., :32]).all())
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 16, 32, 64])
+def test_absent_pages(page, dtype, cache):
+    """Absent pages anywhere in the tiles of every kernel, small ones that only some of a workgroup's waves load."""
+    for rows, dim in ((140, 64), (140, 128), (140, 256), (24, 128), (3, 64)):
+        g = gen(page + rows + dim)
+        p = Pages(g, [rows], [230], 1, dim, cache, page)
+        gone = torch.rand(p.table.shape, generator=g) < 0.15
+        gone[0, 0] = True
+        p.table[gone] = torch.where(torch.rand(p.table.shape, generator=g) < 0.5, -1, p.pages).to(torch.int32)[gone]
+        p.upload()
+        q = (2 * randn(g, rows, 1, dim)).to(dtype)
+        want, tol = attention64(p, q, None, dim ** -0.5, U[F16] if cache in QMAX else U[dtype])
+        check(attend(p, q, None), want, tol, f"absent pages of {page}, {rows} rows of {dim}")
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
+@pytest.mark.parametrize("page", [4, 8, 16, 64])
+def test_one_absent_page(page, dtype, cache):
+    """A single absent page, in each place of a tile in turn."""
+    for col in range(64 // page if page < 64 else 3):
+        g = gen(page + col)
+        p = Pages(g, [70], [200], 2, 128, cache, page)
+        p.table[0, 64 // page + col if page < 64 else col] = -1
+        p.upload()
+        q = (2 * randn(g, 70, 4, 128)).to(dtype)
+        want, tol = attention64(p, q, None, 128 ** -0.5, U[F16] if cache in QMAX else U[dtype])
+        check(attend(p, q, None), want, tol, f"absent page {col} of {page}")
