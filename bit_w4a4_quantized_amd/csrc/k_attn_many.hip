@@ -360,20 +360,28 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     const float mu = m == -INFINITY ? 0.f : m;
     const float inv = CK != C16 && ref > 0.f ? 1.f / ref : 0.f;
     float part[4] = {0.f, 0.f, 0.f, 0.f};
+    v4f sv[2];                               // scales of V of the lane's half of sixteen keys, read ahead of their powers
+    auto read_scales = [&](int u) {
+      if (CK == C16) return;
+#pragma unroll
+      for (int x = 0; x < 2; x++) sv[x] = *reinterpret_cast<const v4f*>(&sc[1][CK == C16 ? 0 : (2 * u + x) * 8 + 4 * half]);
+    };
     // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to ref, as in k_attn_few.
     auto power = [&](int u, int x) {
       const int e = 8 * u + 2 * x;
       const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], coef, -mu));
       const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][(e & 15) + 1], coef, -mu));
       part[x] += p + q;
-      pf[u & 1][x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (scale_v(e) * inv), q * (scale_v(e + 1) * inv));
+      pf[u & 1][x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (sv[x >> 1][2 * (x & 1)] * inv), q * (sv[x >> 1][2 * (x & 1) + 1] * inv));
     };
+    read_scales(0);
 #pragma unroll
     for (int x = 0; x < 4; x++) power(0, x);
     // the next sixteen keys' powers and rows of V between the products of these
 #pragma unroll
     for (int u = 0; u < 2 * NB; u++) {
       if (u + 1 < 2 * NB) {
+        read_scales(u + 1);
 #pragma unroll
         for (int d = 0; d < kBlocks; d++) vf[(u + 1) & 1][d] = read_v(u + 1, d);
       }
