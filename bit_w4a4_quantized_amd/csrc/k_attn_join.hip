@@ -120,10 +120,12 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   // workgroups that are on the chip at once: two a CU, three of the 16-row kernel
   const int64_t resident = p.rows == 16 ? 768 : 512;
   if (p.rows <= kFewRows) {
-    // one round of workgroups, and more of them while a part is longer than its fixed costs
+    // One round of workgroups, and up to twice that while a part is longer than its fixed costs (one sequence over 131072
+    // E4M3 keys: 96 parts a head 64 + 7 us, 192 to 256 parts 62 + 12; 5 trees of 37 in 32 rows: 18.4 us for 384
+    // workgroups, 18.7 for 320, 22 and more from 448 on, whose last ones wait for registers).
     const int64_t round = (p.rows == 16 ? resident : 384) / tiles;
     int64_t s = round < 1 ? 1 : round;
-    while (reach / s > 1500 && 2 * s * tiles <= 3072) s *= 2;
+    while (reach / s > 1500 && s * tiles <= 2 * 768) s *= 2;
     s = s < most ? s : most;
     p.parts = s > 128 ? 128 : (int)s;
     if (p.parts > 1) p.whole = 0;

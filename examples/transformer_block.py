@@ -167,7 +167,7 @@ class Serving:
         self.length.copy_(batch.context + (path >= 0).sum(1).to(torch.int32))
 
 
-def cached(dim=3072, heads=24, ffn=12288, axis_pairs=(64,), prompts=(700, 64, 1300), blocks=2):
+def cached(dim=2048, heads=16, ffn=8192, axis_pairs=(64,), prompts=(700, 64, 1300), blocks=2):
     """Prompts, a tree of drafted tokens for each sequence, an accepted path of it and one more token; the last
     token's output."""
     torch.manual_seed(0)
