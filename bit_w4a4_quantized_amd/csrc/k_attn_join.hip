@@ -105,6 +105,9 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   AttnPlan p{};
   const int group = heads / kv_heads;
   const int64_t each = ((int64_t)tokens * group + sequences - 1) / sequences;    // rows of a sequence and cache head
+  // Past 32 rows a tile of 128 reads the cache once where tiles of 32 read it again: 16 trees of 12 over 4000 (48 rows of
+  // 128 values, bf16) 80 us and 136, 64 of 9 over 2000 in E4M3 (36 rows) 125 and 125; int8 heads of 64 alone were
+  // better off in tiles of 32 (56 rows over 29044: 64 us and 37), and the type is not known here.
   p.rows = each > kFewRows ? kManyRows : each > 16 && dim <= 128 ? kFewRows : 16;
   p.unit = dim > 128 && p.rows > kFewRows ? 32 : 64;
   p.slots = (int)((int64_t)tokens * group / p.rows + sequences);
@@ -120,7 +123,7 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   // workgroups that are on the chip at once: two a CU, three of the 16-row kernel
   const int64_t resident = p.rows == 16 ? 768 : 512;
   if (p.rows <= kFewRows) {
-    // One round of workgroups, and up to twice that while a part is longer than its fixed costs (one sequence over 131072
+    // One round of workgroups, and up to four while a part is longer than its fixed costs (one sequence over 131072
     // E4M3 keys: 96 parts a head 64 + 7 us, 192 to 256 parts 62 + 12; 5 trees of 37 in 32 rows: 18.4 us for 384
     // workgroups, 18.7 for 320, 22 and more from 448 on, whose last ones wait for registers).
     const int64_t round = (p.rows == 16 ? resident : 384) / tiles;
