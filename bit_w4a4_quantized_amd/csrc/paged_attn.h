@@ -157,7 +157,7 @@ __device__ __forceinline__ bool find_rows(const AttnArgs& a, int slot, Work& w) 
   if (a.b.n <= 64) {                         // one look, at all that is asked of the sequence
     const int i = min(__lane_id(), a.b.n - 1);
     const int from = start_of(a.b, i, a.tokens), to = start_of(a.b, i + 1, a.tokens), ctx = context_of(a.b, i);
-    const int64_t first = (int64_t)from * a.group / R + i;
+    const int64_t first = first_slot(from, a.group, R, i);
     const int count = __popcll(__ballot((int)__lane_id() < a.b.n && first <= slot));
     if (count == 0) return false;
     w.seq = __builtin_amdgcn_readfirstlane(count - 1);
@@ -166,18 +166,16 @@ __device__ __forceinline__ bool find_rows(const AttnArgs& a, int slot, Work& w) 
     w.ctx = __builtin_amdgcn_readlane(ctx, w.seq);
   } else {
     w.seq = __builtin_amdgcn_readfirstlane(
-        last_below(a.b.n, slot, [&](int i) { return (int64_t)start_of(a.b, i, a.tokens) * a.group / R + i; }));
+        last_below(a.b.n, slot, [&](int i) { return first_slot(start_of(a.b, i, a.tokens), a.group, R, i); }));
     if (w.seq < 0) return false;
     w.s0 = start_of(a.b, w.seq, a.tokens);
     s1 = start_of(a.b, w.seq + 1, a.tokens);
     w.ctx = context_of(a.b, w.seq);
   }
-  const int64_t first = (int64_t)w.s0 * a.group / R + w.seq;
   w.n = max(0, s1 - w.s0);
   w.rows = w.n * a.group;
-  const int64_t row0 = (slot - first) * R;
-  if (row0 >= w.rows) return false;
-  w.row0 = (int)row0;
+  w.row0 = first_row_of(first_slot(w.s0, a.group, R, w.seq), slot, R, w.rows);
+  if (w.row0 < 0) return false;
   w.keys = keys_of(a, w.ctx, w.n);
   return true;
 }

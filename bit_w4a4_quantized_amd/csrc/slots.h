@@ -42,4 +42,13 @@ SVDQ_BOTH inline int page_of(const PagedBatch& b, const PagedCache& c, int seq, 
   return as_page(c, entry_of(b, c, seq, slot));
 }
 
+// Attention's rows (a token times `group` query heads) in slots of R.  Sequence i has the slots from first_slot on, one
+// more than it may need.  The row that a slot begins with, of a sequence of `rows` that was found for it: -1 where it has
+// none.  Starts that fall can find a sequence whose first slot lies behind this one.
+SVDQ_BOTH inline int64_t first_slot(int start, int group, int R, int i) { return (int64_t)start * group / R + i; }
+SVDQ_BOTH inline int first_row_of(int64_t first, int slot, int R, int rows) {
+  const int64_t row = (slot - first) * R;
+  return row < 0 || row >= rows ? -1 : (int)row;
+}
+
 }  // namespace svdq
