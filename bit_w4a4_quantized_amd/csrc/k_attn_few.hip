@@ -33,7 +33,7 @@ template <int CK, int DP, int NT, int NW>
 struct FewLds {
   // V's rows of 2 DP bytes and 32 more: eight of them side by side reach every bank
   __attribute__((aligned(16))) uint16_t v[NW][32 * (DP + 16)];
-  __attribute__((aligned(16))) float s[CK == C16 ? 1 : NW][2][32];   // scales of K and V
+  __attribute__((aligned(16))) float s[CK == C16 ? 1 : NW][3][32];   // scales of K and V, the latter's logarithms
   float ml[NW][16 * NT][2];
 };
 
@@ -76,11 +76,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
 
   v4f acc[NT][DP / 16];
   bool sick = false;                         // the lane has taken an infinity or NaN out of V
-  float m[NT], l[NT], ref = 0.f;             // ref: what V's scales are taken relative to (8-bit caches)
+  float m[NT], l[NT], mv[NT], g[NT];         // g: 2^(m - mv) (8-bit caches)
 #pragma unroll
   for (int n = 0; n < NT; n++) {
-    m[n] = -INFINITY;
-    l[n] = 0.f;
+    m[n] = mv[n] = -INFINITY;
+    l[n] = g[n] = 0.f;
 #pragma unroll
     for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] = v4f{0.f, 0.f, 0.f, 0.f};
   }
@@ -172,6 +172,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
       lds_s[wave][0][lane] = ks;
       const bool infinite = masked && !(__builtin_fabsf(vs) < INFINITY);
       lds_s[wave][1][lane] = infinite ? 0.f : vs;
+      lds_s[wave][2][lane] = __builtin_amdgcn_logf(infinite ? 0.f : __builtin_fabsf(vs));
       sick = sick || infinite;
     }
 #pragma unroll
@@ -245,45 +246,47 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
 #pragma unroll
         for (int e = 0; e < 8; e++) z[n][e] = seen[n] >> e & 1 ? z[n][e] : -INFINITY;
     }
-    // The reference that a row's powers are taken from moves only when a logit passes it by kSlack, so
-    // that most tiles need no exchange between lanes and no rescaling: powers stay below 2^kSlack.
-    float top[NT], vtop = 0.f;
+    // the references (move_powers)
+    float top[NT], vtop[NT];
     bool move = false;
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      top[n] = -INFINITY;
+      top[n] = vtop[n] = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 8; e++) top[n] = fmaxf(top[n], z[n][e]);
       move = move || top[n] > m[n] + kSlack;
     }
     if (CK != C16) {
 #pragma unroll
-      for (int e = 0; e < 8; e++) vtop = fmaxf(vtop, __builtin_fabsf(vsc[e]));
-      move = move || vtop > 8.f * ref;
-    }
-    if (__any(move)) {
-      float back = 1.f;
-      if (CK != C16) {
-        vtop = fmaxf(vtop, ref);
-        vtop = fmaxf(vtop, __shfl_xor(vtop, 16));
-        vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
-        back = vtop > 0.f ? ref / vtop : 1.f;
-        ref = vtop;
+      for (int t = 0; t < 2; t++) {
+        const v4f x = *reinterpret_cast<const v4f*>(&lds_s[wave][2][16 * t + 4 * quad]);
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) vtop[n] = fmaxf(vtop[n], z[n][4 * t + i] + x[i]);
       }
 #pragma unroll
-      for (int n = 0; n < NT; n++) {
-        float mn = fmaxf(top[n], m[n]);
-        mn = fmaxf(mn, __shfl_xor(mn, 16));
-        mn = fmaxf(mn, __shfl_xor(mn, 32));
-        const float f = mn == m[n] ? 1.f : __builtin_amdgcn_exp2f(m[n] - mn);
-        m[n] = mn;
-        l[n] *= f;
+      for (int n = 0; n < NT; n++) move = move || vtop[n] > mv[n] + kSlack;
+    }
+    if (__any(move)) {
 #pragma unroll
-        for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] *= f * back;
+      for (int n = 0; n < NT; n++) {
+        top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
+        top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
+        Move by;
+        if (CK != C16) {
+          vtop[n] = fmaxf(vtop[n], __shfl_xor(vtop[n], 16));
+          vtop[n] = fmaxf(vtop[n], __shfl_xor(vtop[n], 32));
+          by = move_products(top[n], vtop[n], m[n], mv[n], g[n]);
+        } else {
+          by = move_powers(top[n], m[n]);
+        }
+        l[n] *= by.sum;
+#pragma unroll
+        for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] *= by.values;
       }
     }
     v4u pf[NT];
-    const float inv = CK != C16 && ref > 0.f ? 1.f / ref : 0.f;
 #pragma unroll
     for (int n = 0; n < NT; n++) {
       const float mu = m[n] == -INFINITY ? 0.f : m[n];
@@ -293,12 +296,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
         l[n] += z[n][e];
       }
       // Rounded to 16 bits for the matrix cores (the sum above is of the unrounded): half an ulp of each
-      // term.  With 8-bit caches V's scale joins here, relative to ref (the largest so far, within a factor
-      // of 8): a product below fp16's range is below 2^-24 of the largest's weight.
+      // term.  With 8-bit caches V's scale joins here, relative to the largest product that the row has seen (within
+      // 2^kSlack): below fp16's normal range a product is off by 2^-25 of that.
 #pragma unroll
       for (int e = 0; e < 4; e++)
         pf[n][e] = CK == C16 ? pack16(z[n][2 * e], z[n][2 * e + 1], BF)
-                             : pack_f16(z[n][2 * e] * (vsc[2 * e] * inv), z[n][2 * e + 1] * (vsc[2 * e + 1] * inv));
+                             : pack_f16(z[n][2 * e] * (vsc[2 * e] * g[n]), z[n][2 * e + 1] * (vsc[2 * e + 1] * g[n]));
     }
 #pragma unroll
     for (int dt = 0; dt < DP / 16; dt++) {
@@ -343,7 +346,9 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
   }
   constexpr int CH = DP / NT;                // columns a turn: NW * 16 NT rows of them take V's room
   constexpr int kP = CH / 4;                 // pieces of four
-  const float unit = CK == C16 ? 1.f : ref;
+  float unit[NT];
+#pragma unroll
+  for (int n = 0; n < NT; n++) unit[n] = CK == C16 ? 1.f : unit_of(m[n], mv[n]);
 #pragma unroll
   for (int turn = 0; turn < NT; turn++) {
     __syncthreads();
@@ -352,7 +357,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
     for (int n = 0; n < NT; n++)
 #pragma unroll
       for (int x = 0; x < CH / 16; x++) {
-        const v4f v = acc[n][turn * (CH / 16) + x] * unit;
+        const v4f v = acc[n][turn * (CH / 16) + x] * unit[n];
         *reinterpret_cast<v4f*>(mine + (16 * n + c) * CH + (((x * 4 + quad) ^ c) & (kP - 1)) * 4) = v;
       }
     __syncthreads();

@@ -12,6 +12,7 @@
 // Pieces of 16 bytes are stored turned by the row's number, so that neither the first product's reads (one piece
 // of 32 rows) nor the second's transposed ones (64 bytes of four rows) meet in a bank.
 #include "paged_attn.h"
+#include "rope.h"
 
 namespace svdq {
 
@@ -45,6 +46,16 @@ __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at)
 }
 #pragma clang diagnostic pop
 
+// The largest of a wave's values, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  v = fmaxf(v, dpp<0x141>(v));
+  v = fmaxf(v, dpp<0x140>(v));
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+
 template <bool BF>
 __device__ __forceinline__ v16f mfma32(const v4u& x, const v4u& y, const v16f& z) {
   if (BF) return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, x), __builtin_bit_cast(v8bf, y), z, 0, 0, 0);
@@ -63,7 +74,9 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   constexpr int kRows = 64 / kPieces;        // rows that a wave's load takes
   constexpr int kLoads = BN / 4 / kRows;     // of a wave, for its share of a tile's K, or V
   __shared__ __attribute__((aligned(16))) uint16_t tiles[4 * BN * DP];     // K, V and the other tile's
-  __shared__ __attribute__((aligned(16))) float s0[2][CK == C16 ? 4 : BN], s1[2][CK == C16 ? 4 : BN];   // scales of K and V
+  constexpr int kScales = CK == C16 ? 4 : BN + 4;
+  // scales of K and V, and the latter's logarithms with the tile's largest behind them
+  __shared__ __attribute__((aligned(16))) float s0[3][kScales], s1[3][kScales];
   __shared__ int sick;                       // some tile of V held an infinity or NaN
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 31, half = lane >> 5;
@@ -97,7 +110,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   for (int d = 0; d < kBlocks; d++)
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[d][i] = 0.f;
-  float m = -INFINITY, l = 0.f, ref = 0.f;   // ref: what V's scales are taken relative to (8-bit caches)
+  float m = -INFINITY, l = 0.f, mv = -INFINITY, scale_by = 0.f;    // scale_by: 2^(m - mv) (8-bit caches)
 
   constexpr int es = CK == C16 ? 2 : 1;
   const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + w.head * a.c.head * es;
@@ -209,7 +222,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     fetch_scales(base, page);
     return __ballot(page >= 0);
   };
-  auto settle = [&](uint16_t* kt, uint16_t* vt, float (*sc)[CK == C16 ? 4 : BN]) {      // codes to LDS
+  auto settle = [&](uint16_t* kt, uint16_t* vt, float (*sc)[kScales]) {      // codes to LDS
     if (CK == C16) return;
 #pragma unroll
     for (int i = 0; i < kLoads; i++) {
@@ -222,13 +235,18 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
         *reinterpret_cast<v4u*>(vt + row * DP + ((p + y) ^ turn_v<DP>(row)) * 8) = widen<CK>(vr[i], y);
       }
     }
-    if (wave == 0 && lane < BN) {
-      sc[0][lane] = ksr;
-      sc[1][lane] = vsr;
+    if (wave == 0) {
+      const float power = __builtin_amdgcn_logf(__builtin_fabsf(vsr)), most = wave_max(power);      // 0 past BN
+      if (lane < BN) {
+        sc[0][lane] = ksr;
+        sc[1][lane] = vsr;
+        sc[2][lane] = power;
+      }
+      if (lane == 0) sc[2][BN] = most;
     }
   };
   // Tiles that some row does not see whole: V without infinities and NaN (rows that see one get it at the end).
-  auto clean = [&](uint16_t* vt, float (*sc)[CK == C16 ? 4 : BN]) {
+  auto clean = [&](uint16_t* vt, float (*sc)[kScales]) {
     bool found = false;
     if (CK != CI8) {
       constexpr int kMine = BN * DP / 8 / 256;
@@ -244,6 +262,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     }
     if (CK != C16 && threadIdx.x < BN && !(__builtin_fabsf(sc[1][CK == C16 ? 0 : threadIdx.x]) < INFINITY)) {
       sc[1][CK == C16 ? 0 : threadIdx.x] = 0.f;
+      sc[2][CK == C16 ? 0 : threadIdx.x] = -INFINITY;
       found = true;
     }
     if (found) sick = 1;
@@ -261,7 +280,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   }
 
   auto compute = [&](int base, uint64_t live, const uint16_t* kt, const uint16_t* vt, bool loads, int then,
-                     const float (*sc)[CK == C16 ? 4 : BN]) {
+                     const float (*sc)[kScales]) {
     v16f st[NB];
 #pragma unroll
     for (int b = 0; b < NB; b++)
@@ -329,36 +348,39 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
 #pragma unroll
       for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = seen >> e & 1 ? st[e >> 4][e & 15] : -INFINITY;
     }
-    auto scale_v = [&](int e) { return sc[1][(e >> 2) * 8 + 4 * half + (e & 3)]; };      // of the lane's e-th key
-    // the row's reference moves only when a logit passes it by kSlack (k_attn_few)
-    float top = -INFINITY, vtop = 0.f;
+    // the references (move_powers)
+    float top = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 16 * NB; e++) top = fmaxf(top, st[e >> 4][e & 15]);
     top *= coef;
     bool move = top > m + kSlack;
-    if (CK != C16) {
-#pragma unroll
-      for (int e = 0; e < 16 * NB; e++) vtop = fmaxf(vtop, __builtin_fabsf(scale_v(e)));
-      move = move || vtop > 8.f * ref;
-    }
+    if (CK != C16) move = move || top + sc[2][CK == C16 ? 0 : BN] > mv + kSlack;        // a bound of the products
     if (__any(move)) {
-      float back = 1.f;
+      float vtop = -INFINITY;
       if (CK != C16) {
-        vtop = fmaxf(vtop, ref);
-        vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
-        back = vtop > 0.f ? ref / vtop : 1.f;
-        ref = vtop;
-      }
-      float mn = fmaxf(top, m);
-      mn = fmaxf(mn, __shfl_xor(mn, 32));
-      const float f = mn == m ? 1.f : __builtin_amdgcn_exp2f(m - mn);
-      m = mn;
-      l *= f;
+#pragma clang fp contract(off)               // rounded as the bound is, which it then never passes
 #pragma unroll
-      for (int d = 0; d < kBlocks; d++) acc[d] *= f * back;
+        for (int b = 0; b < NB; b++)
+#pragma unroll
+          for (int g = 0; g < 4; g++) {
+            const v4f x = *reinterpret_cast<const v4f*>(&sc[2][CK == C16 ? 0 : 32 * b + 8 * g + 4 * half]);
+#pragma unroll
+            for (int i = 0; i < 4; i++) vtop = fmaxf(vtop, st[b][4 * g + i] * coef + x[i]);
+          }
+      }
+      top = fmaxf(top, __shfl_xor(top, 32));
+      Move by;
+      if (CK != C16) {
+        vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
+        by = move_products(top, vtop, m, mv, scale_by);
+      } else {
+        by = move_powers(top, m);
+      }
+      l *= by.sum;
+#pragma unroll
+      for (int d = 0; d < kBlocks; d++) acc[d] *= by.values;
     }
     const float mu = m == -INFINITY ? 0.f : m;
-    const float inv = CK != C16 && ref > 0.f ? 1.f / ref : 0.f;
     float part[4] = {0.f, 0.f, 0.f, 0.f};
     v4f sv[2];                               // scales of V of the lane's half of sixteen keys, read ahead of their powers
     auto read_scales = [&](int u) {
@@ -366,13 +388,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
 #pragma unroll
       for (int x = 0; x < 2; x++) sv[x] = *reinterpret_cast<const v4f*>(&sc[1][CK == C16 ? 0 : (2 * u + x) * 8 + 4 * half]);
     };
-    // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to ref, as in k_attn_few.
+    // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to 2^mv, as in k_attn_few.
     auto power = [&](int u, int x) {
       const int e = 8 * u + 2 * x;
       const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], coef, -mu));
       const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][(e & 15) + 1], coef, -mu));
       part[x] += p + q;
-      pf[u & 1][x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (sv[x >> 1][2 * (x & 1)] * inv), q * (sv[x >> 1][2 * (x & 1) + 1] * inv));
+      pf[u & 1][x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (sv[x >> 1][2 * (x & 1)] * scale_by), q * (sv[x >> 1][2 * (x & 1) + 1] * scale_by));
     };
     read_scales(0);
 #pragma unroll
@@ -436,7 +458,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   }
 
   l += __shfl_xor(l, 32);
-  const float unit = CK == C16 ? 1.f : ref;
+  const float unit = CK == C16 ? 1.f : unit_of(m, mv);
   if (begin < end) {
     __syncthreads();
     if (sick) {                              // rare: key by key, each row those that it sees

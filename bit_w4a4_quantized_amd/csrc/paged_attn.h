@@ -13,7 +13,34 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // range fit it), and so do the queries then.
 enum Kind { C16, CI8, CE4 };
 
-constexpr float kSlack = 8.f;                // powers of two that a row's reference may lag behind
+// A row's powers p_j are taken relative to 2^m, its products with V's scales (8-bit caches) relative to 2^mv, each for
+// the row alone and from the keys that it sees.  A reference moves when a logit (for mv: the product's logarithm) passes
+// it by kSlack, and then only that row's: most tiles need no exchange between lanes and no rescaling, and what other rows
+// see changes no bit of this one.
+constexpr float kSlack = 8.f;
+
+// What a tile moves a row's references by: the factors of its sum and of its values' sums, and the one that V's scales
+// take.  top, vtop: the largest logit of the row in the tile and the largest product's logarithm.
+struct Move {
+  float sum, values;
+};
+__device__ __forceinline__ Move move_powers(float top, float& m) {
+  const float to = top > m + kSlack ? top : m, f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
+  m = to;
+  return {f, f};
+}
+// mv stays near enough to m that 2^(m - mv) is a normal number: products that much smaller or larger than the powers are
+// below or past fp32's range in the output.
+__device__ __forceinline__ Move move_products(float top, float vtop, float& m, float& mv, float& g) {
+  const Move r = move_powers(top, m);
+  const float to = fmaxf(fminf(vtop > mv + kSlack ? vtop : mv, m + 126.f), m - 120.f);
+  const float f = to == mv ? 1.f : __builtin_amdgcn_exp2f(mv - to);
+  mv = to;
+  g = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mv);
+  return {r.sum, f};
+}
+// What a sum of values relative to 2^mv is multiplied by to be relative to 2^m.
+__device__ __forceinline__ float unit_of(float m, float mv) { return m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mv - m); }
 
 template <bool BF>
 __device__ __forceinline__ v4f mfma16(const v4u& x, const v4u& y, const v4f& z) {
