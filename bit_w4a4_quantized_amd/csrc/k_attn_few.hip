@@ -70,17 +70,19 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
       qf[n][s] = v4u{0, 0, 0, 0};
       if (valid[n] && d < dim) __builtin_memcpy(&qf[n][s], q + d, 16);
     }
-    coef[n] = a.scale;
-    if (CK != C16 && a.qbf) coef[n] *= queries_to_f16<kSteps, 16>(qf[n]);
+    // a.scale is in K's scales in LDS with an 8-bit cache
+    coef[n] = CK == C16 ? a.scale : 1.f;
+    if (CK != C16 && a.qbf) coef[n] = queries_to_f16<kSteps, 16>(qf[n]);
   }
 
   v4f acc[NT][DP / 16];
   bool sick = false;                         // the lane has taken an infinity or NaN out of V
-  float m[NT], l[NT], mv[NT], g[NT];         // g: 2^(m - mv) (8-bit caches)
+  float m[NT], l[NT], r[NT], scale_by[NT];   // scale_by: 2^-r (8-bit caches)
 #pragma unroll
   for (int n = 0; n < NT; n++) {
-    m[n] = mv[n] = -INFINITY;
-    l[n] = g[n] = 0.f;
+    m[n] = -INFINITY;
+    l[n] = r[n] = 0.f;
+    scale_by[n] = 1.f;
 #pragma unroll
     for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] = v4f{0.f, 0.f, 0.f, 0.f};
   }
@@ -168,13 +170,15 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();         // the last tile's reads of LDS are done
+    float power = -INFINITY;
     if (CK != C16 && lane < 32) {
-      lds_s[wave][0][lane] = ks;
+      lds_s[wave][0][lane] = ks * a.scale;
       const bool infinite = masked && !(__builtin_fabsf(vs) < INFINITY);
       lds_s[wave][1][lane] = infinite ? 0.f : vs;
-      lds_s[wave][2][lane] = __builtin_amdgcn_logf(infinite ? 0.f : __builtin_fabsf(vs));
+      lds_s[wave][2][lane] = power = __builtin_amdgcn_logf(infinite ? 0.f : __builtin_fabsf(vs));
       sick = sick || infinite;
     }
+    const float most = CK != C16 ? wave_max(power) : 0.f;            // of the tile
 #pragma unroll
     for (int i = 0; i < kLoads; i++)
       *reinterpret_cast<v4u*>(kt + (i * kRows + row_in) * kK + piece * 16) = in ? kr[i] : v4u{0, 0, 0, 0};
@@ -247,43 +251,39 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
         for (int e = 0; e < 8; e++) z[n][e] = seen[n] >> e & 1 ? z[n][e] : -INFINITY;
     }
     // the references (move_powers)
-    float top[NT], vtop[NT];
+    float top[NT];
     bool move = false;
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      top[n] = vtop[n] = -INFINITY;
+      top[n] = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 8; e++) top[n] = fmaxf(top[n], z[n][e]);
-      move = move || top[n] > m[n] + kSlack;
-    }
-    if (CK != C16) {
-#pragma unroll
-      for (int t = 0; t < 2; t++) {
-        const v4f x = *reinterpret_cast<const v4f*>(&lds_s[wave][2][16 * t + 4 * quad]);
-#pragma unroll
-        for (int n = 0; n < NT; n++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) vtop[n] = fmaxf(vtop[n], z[n][4 * t + i] + x[i]);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; n++) move = move || vtop[n] > mv[n] + kSlack;
+      move = move || top[n] - m[n] > kSlack;
+      if (CK != C16) move = move || (top[n] - m[n]) + most > r[n] + kSlack;      // a bound of the products
     }
     if (__any(move)) {
 #pragma unroll
       for (int n = 0; n < NT; n++) {
         top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
         top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
-        Move by;
+        const float old = m[n], sum_by = move_powers(top[n], m[n]);
+        float by = sum_by;
         if (CK != C16) {
-          vtop[n] = fmaxf(vtop[n], __shfl_xor(vtop[n], 16));
-          vtop[n] = fmaxf(vtop[n], __shfl_xor(vtop[n], 32));
-          by = move_products(top[n], vtop[n], m[n], mv[n], g[n]);
-        } else {
-          by = move_powers(top[n], m[n]);
-        }
-        l[n] *= by.sum;
+          float vtop = -INFINITY;
 #pragma unroll
-        for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] *= by.values;
+          for (int t = 0; t < 2; t++) {
+            const v4f x = *reinterpret_cast<const v4f*>(&lds_s[wave][2][16 * t + 4 * quad]);
+#pragma unroll
+            for (int i = 0; i < 4; i++) vtop = fmaxf(vtop, (z[n][4 * t + i] - m[n]) + x[i]);
+          }
+          vtop = fmaxf(vtop, __shfl_xor(vtop, 16));
+          vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
+          by = move_products(vtop, m[n] == old ? 0.f : m[n] - old, r[n]);
+          scale_by[n] = __builtin_amdgcn_exp2f(-r[n]);
+        }
+        l[n] *= sum_by;
+#pragma unroll
+        for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] *= by;
       }
     }
     v4u pf[NT];
@@ -301,7 +301,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
 #pragma unroll
       for (int e = 0; e < 4; e++)
         pf[n][e] = CK == C16 ? pack16(z[n][2 * e], z[n][2 * e + 1], BF)
-                             : pack_f16(z[n][2 * e] * (vsc[2 * e] * g[n]), z[n][2 * e + 1] * (vsc[2 * e + 1] * g[n]));
+                             : pack_f16(z[n][2 * e] * (vsc[2 * e] * scale_by[n]), z[n][2 * e + 1] * (vsc[2 * e + 1] * scale_by[n]));
     }
 #pragma unroll
     for (int dt = 0; dt < DP / 16; dt++) {
@@ -348,7 +348,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
   constexpr int kP = CH / 4;                 // pieces of four
   float unit[NT];
 #pragma unroll
-  for (int n = 0; n < NT; n++) unit[n] = CK == C16 ? 1.f : unit_of(m[n], mv[n]);
+  for (int n = 0; n < NT; n++) unit[n] = CK == C16 ? 1.f : __builtin_amdgcn_exp2f(r[n]);
 #pragma unroll
   for (int turn = 0; turn < NT; turn++) {
     __syncthreads();

@@ -12,7 +12,6 @@
 // Pieces of 16 bytes are stored turned by the row's number, so that neither the first product's reads (one piece
 // of 32 rows) nor the second's transposed ones (64 bytes of four rows) meet in a bank.
 #include "paged_attn.h"
-#include "rope.h"
 
 namespace svdq {
 
@@ -25,6 +24,8 @@ template <int DP>
 __device__ __forceinline__ int turn_k(int row) { return DP == 64 ? (row >> 1) & 7 : DP == 128 ? row & 15 : row & 7; }
 template <int DP>
 __device__ __forceinline__ int turn_v(int row) { return DP == 64 ? (row >> 1 & 1) << 2 : (row & 3) << 2; }
+
+constexpr float kFar = 0x1p20f;              // logits (in powers of two) from here on have steps of an eighth and more
 
 __device__ const uint4 kNothing[1] = {};     // 16 bytes of zeros that loads of absent keys read
 
@@ -45,16 +46,6 @@ __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at)
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(at) : "memory", "m0");
 }
 #pragma clang diagnostic pop
-
-// The largest of a wave's values, in every lane.
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp<0xB1>(v));
-  v = fmaxf(v, dpp<0x4E>(v));
-  v = fmaxf(v, dpp<0x141>(v));
-  v = fmaxf(v, dpp<0x140>(v));
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
-}
 
 template <bool BF>
 __device__ __forceinline__ v16f mfma32(const v4u& x, const v4u& y, const v16f& z) {
@@ -102,15 +93,16 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       if (valid && d < dim) __builtin_memcpy(&qf[s], q + d, 16);
     }
   }
-  float coef = a.scale;
-  if (CK != C16 && a.qbf) coef *= queries_to_f16<kSteps, 32>(qf);
+  // a logit is a sum of products times coef; with an 8-bit cache a power of two, a.scale being in K's scales in LDS
+  float coef = CK == C16 ? a.scale : 1.f;
+  if (CK != C16 && a.qbf) coef = queries_to_f16<kSteps, 32>(qf);
 
   v16f acc[kBlocks];
 #pragma unroll
   for (int d = 0; d < kBlocks; d++)
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[d][i] = 0.f;
-  float m = -INFINITY, l = 0.f, mv = -INFINITY, scale_by = 0.f;    // scale_by: 2^(m - mv) (8-bit caches)
+  float m = -INFINITY, l = 0.f, r_v = 0.f;
 
   constexpr int es = CK == C16 ? 2 : 1;
   const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + w.head * a.c.head * es;
@@ -238,7 +230,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     if (wave == 0) {
       const float power = __builtin_amdgcn_logf(__builtin_fabsf(vsr)), most = wave_max(power);      // 0 past BN
       if (lane < BN) {
-        sc[0][lane] = ksr;
+        sc[0][lane] = ksr * a.scale;
         sc[1][lane] = vsr;
         sc[2][lane] = power;
       }
@@ -353,34 +345,43 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
 #pragma unroll
     for (int e = 0; e < 16 * NB; e++) top = fmaxf(top, st[e >> 4][e & 15]);
     top *= coef;
-    bool move = top > m + kSlack;
-    if (CK != C16) move = move || top + sc[2][CK == C16 ? 0 : BN] > mv + kSlack;        // a bound of the products
-    if (__any(move)) {
-      float vtop = -INFINITY;
+    auto is_far = [](float x) { return CK == C16 && __builtin_fabsf(x) >= kFar && x > -INFINITY; };
+    bool move = top - m > kSlack, far = is_far(top);
+    if (CK != C16) move = move || (top - m) + sc[2][CK == C16 ? 0 : BN] > r_v + kSlack;      // a bound of the products
+    if (__any(move || far)) {
+      // rounded as the bound is, which the products then never pass
+#pragma clang fp contract(off)
+      top = fmaxf(top, __shfl_xor(top, 32));
+      far = is_far(top);
+      const float old = m, sum_by = move_powers(top, m);
+      float by = sum_by;
       if (CK != C16) {
-#pragma clang fp contract(off)               // rounded as the bound is, which it then never passes
+        float vtop = -INFINITY;
 #pragma unroll
         for (int b = 0; b < NB; b++)
 #pragma unroll
           for (int g = 0; g < 4; g++) {
             const v4f x = *reinterpret_cast<const v4f*>(&sc[2][CK == C16 ? 0 : 32 * b + 8 * g + 4 * half]);
 #pragma unroll
-            for (int i = 0; i < 4; i++) vtop = fmaxf(vtop, st[b][4 * g + i] * coef + x[i]);
+            for (int i = 0; i < 4; i++) vtop = fmaxf(vtop, (st[b][4 * g + i] * coef - m) + x[i]);
+            asm volatile("" ::: "memory");   // few at once
           }
-      }
-      top = fmaxf(top, __shfl_xor(top, 32));
-      Move by;
-      if (CK != C16) {
         vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
-        by = move_products(top, vtop, m, mv, scale_by);
-      } else {
-        by = move_powers(top, m);
+        by = move_products(vtop, m == old ? 0.f : m - old, r_v);
       }
-      l *= by.sum;
+      l *= sum_by;
 #pragma unroll
-      for (int d = 0; d < kBlocks; d++) acc[d] *= by.values;
+      for (int d = 0; d < kBlocks; d++) acc[d] *= by;
+      // The powers below take a logit's product and m in one rounding, m the rounded product of the largest: apart by up
+      // to half a step of it, which must stay small.  (Products with a power of two are not rounded.)
+      if (far) {
+        const float back = __builtin_amdgcn_rcpf(coef);
+#pragma unroll
+        for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = (st[e >> 4][e & 15] * coef - m) * back;
+      }
     }
-    const float mu = m == -INFINITY ? 0.f : m;
+    const float mu = m == -INFINITY || far ? 0.f : m;
+    const float scale_by = CK == C16 ? 1.f : __builtin_amdgcn_exp2f(-r_v);
     float part[4] = {0.f, 0.f, 0.f, 0.f};
     v4f sv[2];                               // scales of V of the lane's half of sixteen keys, read ahead of their powers
     auto read_scales = [&](int u) {
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
 #pragma unroll
       for (int x = 0; x < 2; x++) sv[x] = *reinterpret_cast<const v4f*>(&sc[1][CK == C16 ? 0 : (2 * u + x) * 8 + 4 * half]);
     };
-    // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to 2^mv, as in k_attn_few.
+    // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to 2^(m + r), as in k_attn_few.
     auto power = [&](int u, int x) {
       const int e = 8 * u + 2 * x;
       const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], coef, -mu));
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
   }
 
   l += __shfl_xor(l, 32);
-  const float unit = CK == C16 ? 1.f : unit_of(m, mv);
+  const float unit = CK == C16 ? 1.f : __builtin_amdgcn_exp2f(r_v);
   if (begin < end) {
     __syncthreads();
     if (sick) {                              // rare: key by key, each row those that it sees

@@ -1,6 +1,7 @@
 // Shared by the attention kernels over a paged cache (k_attn_few.hip, k_attn_many.hip, k_attn_join.hip).
 #pragma once
 #include "paged.h"
+#include "rope.h"
 
 namespace svdq {
 namespace attn {
@@ -13,34 +14,37 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // range fit it), and so do the queries then.
 enum Kind { C16, CI8, CE4 };
 
-// A row's powers p_j are taken relative to 2^m, its products with V's scales (8-bit caches) relative to 2^mv, each for
-// the row alone and from the keys that it sees.  A reference moves when a logit (for mv: the product's logarithm) passes
-// it by kSlack, and then only that row's: most tiles need no exchange between lanes and no rescaling, and what other rows
-// see changes no bit of this one.
+// A row's powers p_j are taken relative to 2^m, its products with V's scales (8-bit caches) relative to 2^(m + r), each
+// for the row alone and from the keys that it sees.  A reference moves when a logit (for m + r: a product's logarithm)
+// passes it by kSlack, and then only that row's: most tiles need no exchange between lanes and no rescaling, and what
+// other rows see changes no bit of this one.  Logits are only ever subtracted from one another: a sum with a small number
+// could lose it (logits have steps of 16 from 2^27 on).
 constexpr float kSlack = 8.f;
 
-// What a tile moves a row's references by: the factors of its sum and of its values' sums, and the one that V's scales
-// take.  top, vtop: the largest logit of the row in the tile and the largest product's logarithm.
-struct Move {
-  float sum, values;
-};
-__device__ __forceinline__ Move move_powers(float top, float& m) {
-  const float to = top > m + kSlack ? top : m, f = to == m ? 1.f : __builtin_amdgcn_exp2f(m - to);
-  m = to;
-  return {f, f};
+// The row's largest logit of a tile against its reference; the factor of its sums.
+__device__ __forceinline__ float move_powers(float top, float& m) {
+  const float old = m;
+  if (top - old > kSlack) m = top;           // the first tile: from minus infinity
+  return m == old ? 1.f : __builtin_amdgcn_exp2f(old - m);
 }
-// mv stays near enough to m that 2^(m - mv) is a normal number: products that much smaller or larger than the powers are
-// below or past fp32's range in the output.
-__device__ __forceinline__ Move move_products(float top, float vtop, float& m, float& mv, float& g) {
-  const Move r = move_powers(top, m);
-  const float to = fmaxf(fminf(vtop > mv + kSlack ? vtop : mv, m + 126.f), m - 120.f);
-  const float f = to == mv ? 1.f : __builtin_amdgcn_exp2f(mv - to);
-  mv = to;
-  g = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mv);
-  return {r.sum, f};
+// The same for the products, after a move of m by `by`; vtop: the largest product's logarithm, less m.  r stays where
+// 2^r and 2^-r are normal numbers: products so much smaller or larger than the powers are below or past the output's range.
+__device__ __forceinline__ float move_products(float vtop, float by, float& r) {
+  const float kept = r - by;
+  r = fmaxf(kept, -120.f);
+  if (vtop - r > kSlack) r = fminf(vtop, 126.f);
+  return r == kept ? 1.f : __builtin_amdgcn_exp2f(kept - r);
 }
-// What a sum of values relative to 2^mv is multiplied by to be relative to 2^m.
-__device__ __forceinline__ float unit_of(float m, float mv) { return m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mv - m); }
+
+// The largest of a wave's values, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  v = fmaxf(v, dpp<0x141>(v));
+  v = fmaxf(v, dpp<0x140>(v));
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
 
 template <bool BF>
 __device__ __forceinline__ v4f mfma16(const v4u& x, const v4u& y, const v4f& z) {

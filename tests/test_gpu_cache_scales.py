@@ -12,7 +12,8 @@ torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
 
-from test_gpu_cache import (BF16, E4M3, EPS32, F16, F64, I8, QMAX, SMALL, U, Pages, _gpu, attend, check, gen,  # noqa: E402, F401
+from strict import check  # noqa: E402
+from test_gpu_cache import (BF16, E4M3, EPS32, F16, F64, I8, QMAX, SMALL, U, Pages, _gpu, attend, gen,  # noqa: E402, F401
                             randn, random_tree)
 
 INF = math.inf
