@@ -251,6 +251,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
         for (int e = 0; e < 8; e++) z[n][e] = seen[n] >> e & 1 ? z[n][e] : -INFINITY;
     }
     // the references (move_powers)
+    constexpr bool kLands = CK == C16 && !BF;
     float top[NT];
     bool move = false;
 #pragma unroll
@@ -258,15 +259,15 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
       top[n] = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 8; e++) top[n] = fmaxf(top[n], z[n][e]);
-      move = move || top[n] - m[n] > kSlack;
-      if (CK != C16) move = move || (top[n] - m[n]) + most > r[n] + kSlack;      // a bound of the products
+      move = move || top[n] - m[n] > (kLands ? kLand : 0.f) + kSlack;
+      if (CK != C16) move = move || ((top[n] - m[n]) + most) - r[n] > kLand + kSlack;      // a bound of the products
     }
     if (__any(move)) {
 #pragma unroll
       for (int n = 0; n < NT; n++) {
         top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
         top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
-        const float old = m[n], sum_by = move_powers(top[n], m[n]);
+        const float old = m[n], sum_by = move_powers<kLands>(top[n], m[n]);
         float by = sum_by;
         if (CK != C16) {
           float vtop = -INFINITY;
@@ -296,8 +297,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
         l[n] += z[n][e];
       }
       // Rounded to 16 bits for the matrix cores (the sum above is of the unrounded): half an ulp of each
-      // term.  With 8-bit caches V's scale joins here, relative to the largest product that the row has seen (within
-      // 2^kSlack): below fp16's normal range a product is off by 2^-25 of that.
+      // term, or 2^-32 of the largest that the row has seen (move_powers).  With 8-bit caches V's scale joins here.
 #pragma unroll
       for (int e = 0; e < 4; e++)
         pf[n][e] = CK == C16 ? pack16(z[n][2 * e], z[n][2 * e + 1], BF)

@@ -346,14 +346,15 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     for (int e = 0; e < 16 * NB; e++) top = fmaxf(top, st[e >> 4][e & 15]);
     top *= coef;
     auto is_far = [](float x) { return CK == C16 && __builtin_fabsf(x) >= kFar && x > -INFINITY; };
-    bool move = top - m > kSlack, far = is_far(top);
-    if (CK != C16) move = move || (top - m) + sc[2][CK == C16 ? 0 : BN] > r_v + kSlack;      // a bound of the products
+    constexpr bool kLands = CK == C16 && !BF;
+    bool move = top - m > (kLands ? kLand : 0.f) + kSlack, far = is_far(top);
+    if (CK != C16) move = move || ((top - m) + sc[2][CK == C16 ? 0 : BN]) - r_v > kLand + kSlack;      // a bound of the products
     if (__any(move || far)) {
       // rounded as the bound is, which the products then never pass
 #pragma clang fp contract(off)
       top = fmaxf(top, __shfl_xor(top, 32));
       far = is_far(top);
-      const float old = m, sum_by = move_powers(top, m);
+      const float old = m, sum_by = move_powers<kLands>(top, m);
       float by = sum_by;
       if (CK != C16) {
         float vtop = -INFINITY;

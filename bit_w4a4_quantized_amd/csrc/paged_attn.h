@@ -19,12 +19,18 @@ enum Kind { C16, CI8, CE4 };
 // passes it by kSlack, and then only that row's: most tiles need no exchange between lanes and no rescaling, and what
 // other rows see changes no bit of this one.  Logits are only ever subtracted from one another: a sum with a small number
 // could lose it (logits have steps of 16 from 2^27 on).
-constexpr float kSlack = 8.f;
+//
+// What becomes an fp16 operand lies high in its range: a reference is moved to kLand below the largest, which then is at
+// 2^7 and stays below 2^15.  Operands 2^-21 of it keep all bits, smaller ones are off by 2^-32 of it (of 131071 keys 18
+// nats below one other, whose value is 0, nothing was left with the largest at 1).
+constexpr float kSlack = 8.f, kLand = 7.f;
 
 // The row's largest logit of a tile against its reference; the factor of its sums.
+template <bool LAND>
 __device__ __forceinline__ float move_powers(float top, float& m) {
+  constexpr float land = LAND ? kLand : 0.f;
   const float old = m;
-  if (top - old > kSlack) m = top;           // the first tile: from minus infinity
+  if (top - old > land + kSlack) m = top - land;       // the first tile: from minus infinity
   return m == old ? 1.f : __builtin_amdgcn_exp2f(old - m);
 }
 // The same for the products, after a move of m by `by`; vtop: the largest product's logarithm, less m.  r stays where
@@ -32,7 +38,7 @@ __device__ __forceinline__ float move_powers(float top, float& m) {
 __device__ __forceinline__ float move_products(float vtop, float by, float& r) {
   const float kept = r - by;
   r = fmaxf(kept, -120.f);
-  if (vtop - r > kSlack) r = fminf(vtop, 126.f);
+  if (vtop - r > kLand + kSlack) r = fminf(vtop - kLand, 126.f);
   return r == kept ? 1.f : __builtin_amdgcn_exp2f(kept - r);
 }
 

@@ -564,8 +564,10 @@ svdq_status svdq_rope_append(const svdq_paged_cache* cache, const svdq_paged_bat
  *   tree   : bytes [tokens, tree_width], rows tree_stride apart, or NULL.
  * The work is cut by the mean number of rows of a sequence: long chunks and single tokens are best in calls of their own.
  * Logits, the softmax's statistics and sums are fp32; probabilities are rounded to 16 bits for the matrix
- * cores (to fp16 with an 8-bit cache, whose scales of values join them there).  They are taken relative to a
- * maximum that may lag by 2^8: sums of values of a bf16 cache from 2^119 on can leave fp32's range.
+ * cores (to fp16 with an 8-bit cache, whose scales of values join them there).  In fp16 one below 2^-21 of the row's
+ * largest (of probability times scale) is off by up to 2^-32 of that: values of n keys so far below the rest are good to
+ * n 2^-32 of the largest.  Powers are taken relative to a maximum that may lag by 2^8 (2^15 with an fp16 cache): sums of values of a
+ * bf16 cache from 2^119 on can leave fp32's range.
  *   workspace, workspace_bytes : caller-owned device scratch, 16-byte aligned, for the sums of the keys' parts
  *            where rows alone do not fill the chip (svdq_tree_attention_workspace_bytes); rules as for
  *            svdq_gemm_act_residual's.
