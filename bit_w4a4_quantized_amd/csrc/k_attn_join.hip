@@ -135,14 +135,20 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
   } else {
     // The tiles of the last, partial round are cut so that it fills the chip (in rounds of whole tiles: the parts'
     // own, half a part for the workgroups that end early, and the join, whose bytes at 4.5 TB/s stand against 1.7 us
-    // for 64 keys of 128 values).  Few tiles of many keys are cut into one round of workgroups (12 trees of 14 over
-    // 85055: 266 us in 16 parts, 117 in 40; 3 of 48 over 53647 in int8 137 and 38).
-    const int64_t rest = tiles % resident;
+    // for 64 keys of 128 values).  Tiles that are no full round and few of many keys are cut into one round of workgroups (12
+    // trees of 14 over 85055: 266 us in 16 parts, 117 in 40; 3 of 48 over 53647 in int8 137 and 38).
+    //
+    // Empty tiles lie evenly among the numbers: `rest` tiles with rows are in about rest * all / tiles of them.  All parts
+    // together are at most three rounds of workgroups, and so are the sums that they leave (65 trees of 9 over 2000 in
+    // 32 on 8 heads, 520 tiles in 664 numbers: 10 numbers cut 16 ways 152 us, none cut 145; the 152 behind the first 512 cut
+    // 64 ways 261).  `reach` is the table's width, which the contexts may be far below (112 x 9 over 2000: 180 us in a
+    // table for 2048 keys, 215 in one for 32768).
+    const int64_t rest = tiles % resident, cut = tiles < resident ? all : (rest * all + tiles - 1) / tiles;
     const double early = tiles > resident ? 0.5 : 0.0;
     const double join = reach > 0 ? (1.1 * rest + 722.0 / dim) / reach : 0.0;
     double best = 1.0 + early;
     auto weigh = [&](int64_t s) {
-      if (s > most || s > 128) return;
+      if (s > most || s > 128 || cut * s > 3 * resident) return;
       const double t = (double)((rest * s + resident - 1) / resident) / s + early / s + join * s;
       if (t < 0.95 * best) {
         best = t;
@@ -151,12 +157,12 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
     };
     if (rest) {
       for (int s = 2; s <= 16; s++) weigh(s);
-      if (rest * 16 < resident) {
+      if (tiles * 16 < resident) {
         weigh(resident / 2 / rest < 128 ? resident / 2 / rest : 128);
         weigh(resident / rest < 128 ? resident / rest : 128);
       }
     }
-    if (p.parts > 1) p.whole = (int)(tiles - rest);
+    if (p.parts > 1) p.whole = (int)(all - cut);
   }
   if (p.parts < 2) {
     p.parts = 1;
