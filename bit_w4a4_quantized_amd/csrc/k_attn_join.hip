@@ -18,18 +18,17 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
   const int g = threadIdx.x / P, lane = threadIdx.x % P, row_in = g / deep, way = g % deep;
   const int chunks = R / per, tile = a.whole + blockIdx.x / chunks, row = (int)(blockIdx.x % chunks) * per + row_in;
   const int dim = a.c.dim, d = lane * 4;
-  const int parts = a.parts;
-  const int64_t id = (int64_t)(tile - a.whole) * parts;      // of the first part; the others follow
+  const int64_t id = (int64_t)(tile - a.whole) * a.parts;      // of the first part; the others follow
   const float* ml = a.part + a.ids * R * dim + (id * R + row) * 2;
   const float* o = a.part + (id * R + row) * dim + min(d, dim - 4);
-  // the first parts' sums are on their way while the tile's sequence is looked up (what lies there of rows that a
-  // tile has not is not used)
+  // the first parts' sums are on their way while the tile's sequence is looked up (what lies there of rows and parts that
+  // a tile has not is not used)
   constexpr int kFirst = 4;
   float m4[kFirst], l4[kFirst];
   v4f o4[kFirst];
 #pragma unroll
   for (int i = 0; i < kFirst; i++) {
-    const int64_t s = min(way + i * deep, parts - 1) * (int64_t)R;
+    const int64_t s = min(way + i * deep, a.parts - 1) * (int64_t)R;
     m4[i] = ml[2 * s];
     l4[i] = ml[2 * s + 1];
     o4[i] = *reinterpret_cast<const v4f*>(o + s * dim);
@@ -37,6 +36,9 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
   Work w;
   w.id = -1;
   if (!find_tile<R>(a, tile, w)) return;     // the whole workgroup
+  int last, each;
+  share_keys<R>(a, w, a.parts, last, each);
+  const int parts = last > 0 ? (last + each - 1) / each : 0;       // that have keys
   const bool valid = w.row0 + row < w.rows && d < dim;
   float m = -INFINITY, l = 0.f;
   v4f sum{0.f, 0.f, 0.f, 0.f};

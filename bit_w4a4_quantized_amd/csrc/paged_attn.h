@@ -224,7 +224,16 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) 
   return find_rows<R>(a, a.slots - 1 - tile / a.c.heads, w);
 }
 
-// The workgroup's tile, or part of one.
+// How a tile's keys are shared among parts: up to `last`, `each` a part (a table wider than the contexts leaves the
+// last parts without any).
+template <int R>
+__device__ __forceinline__ void share_keys(const AttnArgs& a, const Work& w, int parts, int& last, int& each) {
+  last = a.tree ? w.keys : min(w.keys, w.ctx + min((w.row0 + R - 1) / a.group, w.n - 1) + 1);
+  each = (last + parts - 1) / parts;
+  each = (each + a.unit - 1) / a.unit * a.unit;
+}
+
+// The workgroup's tile, or part of one that has keys.
 template <int R>
 __device__ __forceinline__ bool cut_work(const AttnArgs& a, Work& w) {
   int id = blockIdx.x;
@@ -245,12 +254,11 @@ __device__ __forceinline__ bool cut_work(const AttnArgs& a, Work& w) {
     if (parts > 1) w.id = (int64_t)(tile - a.whole) * parts + split;
   }
   if (!find_tile<R>(a, tile, w)) return false;
-  const int last = a.tree ? w.keys : min(w.keys, w.ctx + min((w.row0 + R - 1) / a.group, w.n - 1) + 1);
-  int each = (last + parts - 1) / parts;
-  each = (each + a.unit - 1) / a.unit * a.unit;
+  int last, each;
+  share_keys<R>(a, w, parts, last, each);
   w.begin = (int)min((int64_t)last, (int64_t)split * each);
   w.end = min(last, w.begin + each);
-  return true;
+  return w.id < 0 || w.begin < w.end;
 }
 
 // A value of V of an existing slot, where it is an infinity or NaN (with its scale), else 0: what make_finite took
