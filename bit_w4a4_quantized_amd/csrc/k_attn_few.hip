@@ -389,8 +389,9 @@ template <bool BF, int CK, int DP, int NT>
 hipError_t launch(const AttnArgs& a, hipStream_t s) {
   constexpr int NW = 4;
   const int64_t blocks = blocks_of(a);
-  if (!launchable(blocks, 64 * NW)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_attn_few<BF, CK, DP, NT, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, s, a);
+  if (blocks > 2 * kGridRow) return hipErrorInvalidConfiguration;
+  const dim3 grid = blocks < 2 * kGridRow ? dim3((unsigned)blocks) : dim3(kGridRow, 2);
+  hipLaunchKernelGGL((k_attn_few<BF, CK, DP, NT, NW>), grid, dim3(64 * NW), 0, s, a);
   return hipGetLastError();
 }
 

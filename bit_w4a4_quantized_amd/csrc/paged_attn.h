@@ -138,6 +138,9 @@ __device__ __forceinline__ v4u transposed(const uint16_t* x, const uint16_t* y) 
 
 constexpr int kManyRows = 128, kFewRows = 32;   // 16 or 32 where there are no more (32 of heads up to 128: registers)
 
+// A launch has fewer than 2^32 threads along x: 2^24 tiles of few rows, the most there are, take two rows of the grid.
+constexpr int kGridRow = 1 << 23;
+
 __host__ __device__ inline int64_t blocks_of(const AttnArgs& a) {
   const int64_t tiles = (int64_t)a.slots * a.c.heads;
   return a.whole + (tiles - a.whole) * a.parts;
@@ -238,6 +241,7 @@ template <int R>
 __device__ __forceinline__ bool cut_work(const AttnArgs& a, Work& w) {
   int id = blockIdx.x;
   if (R <= kFewRows) {
+    id += blockIdx.y * kGridRow;
     // Eight slots' parts at a time, a head after the other: workgroups go round the eight XCDs, so that the heads of a
     // part meet on one of them.  They share the cache lines of scales (and of short rows).
     const int all = (int)blocks_of(a) / a.c.heads, g = id / (8 * a.c.heads), in = id - g * 8 * a.c.heads, m = min(8, all - 8 * g);
