@@ -27,13 +27,13 @@ namespace {
 using namespace attn;
 
 // Waves a SIMD that the registers are kept to.
-constexpr int few_waves(int CK, int DP, int NT) { return DP == 256 ? 1 : NT == 2 ? 2 : DP == 64 ? 3 : CK == C16 ? 2 : 3; }
+constexpr int few_waves(int CK, int DP, int NT) { return DP == 256 ? 1 : DP == 64 ? 3 : NT == 2 || CK == C16 ? 2 : 3; }
 
 template <int CK, int DP, int NT, int NW>
 struct FewLds {
   // V's rows of 2 DP bytes and 32 more: eight of them side by side reach every bank
   __attribute__((aligned(16))) uint16_t v[NW][32 * (DP + 16)];
-  __attribute__((aligned(16))) float s[CK == C16 ? 1 : NW][3][32];   // scales of K and V, the latter's logarithms
+  __attribute__((aligned(16))) float s[CK == C16 ? 1 : NW][2][32];   // scales of K and V
   float ml[NW][16 * NT][2];
 };
 
@@ -77,12 +77,11 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
 
   v4f acc[NT][DP / 16];
   bool sick = false;                         // the lane has taken an infinity or NaN out of V
-  float m[NT], l[NT], r[NT], scale_by[NT];   // scale_by: 2^-r (8-bit caches)
+  float m[NT], l[NT], r[NT];
 #pragma unroll
   for (int n = 0; n < NT; n++) {
     m[n] = -INFINITY;
     l[n] = r[n] = 0.f;
-    scale_by[n] = 1.f;
 #pragma unroll
     for (int dt = 0; dt < DP / 16; dt++) acc[n][dt] = v4f{0.f, 0.f, 0.f, 0.f};
   }
@@ -170,15 +169,12 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();         // the last tile's reads of LDS are done
-    float power = -INFINITY;
     if (CK != C16 && lane < 32) {
       lds_s[wave][0][lane] = ks * a.scale;
       const bool infinite = masked && !(__builtin_fabsf(vs) < INFINITY);
       lds_s[wave][1][lane] = infinite ? 0.f : vs;
-      lds_s[wave][2][lane] = power = __builtin_amdgcn_logf(infinite ? 0.f : __builtin_fabsf(vs));
       sick = sick || infinite;
     }
-    const float most = CK != C16 ? wave_max(power) : 0.f;            // of the tile
 #pragma unroll
     for (int i = 0; i < kLoads; i++)
       *reinterpret_cast<v4u*>(kt + (i * kRows + row_in) * kK + piece * 16) = in ? kr[i] : v4u{0, 0, 0, 0};
@@ -252,15 +248,20 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
     }
     // the references (move_powers)
     constexpr bool kLands = CK == C16 && !BF;
-    float top[NT];
+    float top[NT], most = 0.f;               // most: a bound of the lane's products against its largest logit
     bool move = false;
+    if (CK != C16) {
+#pragma unroll
+      for (int e = 0; e < 8; e++) most = fmaxf(most, __builtin_fabsf(vsc[e]));
+      most = __builtin_amdgcn_logf(most);
+    }
 #pragma unroll
     for (int n = 0; n < NT; n++) {
       top[n] = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 8; e++) top[n] = fmaxf(top[n], z[n][e]);
       move = move || top[n] - m[n] > (kLands ? kLand : 0.f) + kSlack;
-      if (CK != C16) move = move || ((top[n] - m[n]) + most) - r[n] > kLand + kSlack;      // a bound of the products
+      if (CK != C16) move = move || ((top[n] - m[n]) + most) - r[n] > kLand + kSlack - 0.01f;      // less what it rounds
     }
     if (__any(move)) {
 #pragma unroll
@@ -272,15 +273,10 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
         if (CK != C16) {
           float vtop = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < 2; t++) {
-            const v4f x = *reinterpret_cast<const v4f*>(&lds_s[wave][2][16 * t + 4 * quad]);
-#pragma unroll
-            for (int i = 0; i < 4; i++) vtop = fmaxf(vtop, (z[n][4 * t + i] - m[n]) + x[i]);
-          }
+          for (int e = 0; e < 8; e++) vtop = fmaxf(vtop, (z[n][e] - m[n]) + __builtin_amdgcn_logf(__builtin_fabsf(vsc[e])));
           vtop = fmaxf(vtop, __shfl_xor(vtop, 16));
           vtop = fmaxf(vtop, __shfl_xor(vtop, 32));
           by = move_products(vtop, m[n] == old ? 0.f : m[n] - old, r[n]);
-          scale_by[n] = __builtin_amdgcn_exp2f(-r[n]);
         }
         l[n] *= sum_by;
 #pragma unroll
@@ -290,7 +286,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
     v4u pf[NT];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
-      const float mu = m[n] == -INFINITY ? 0.f : m[n];
+      const float mu = m[n] == -INFINITY ? 0.f : m[n], scale_by = CK == C16 ? 1.f : __builtin_amdgcn_exp2f(-r[n]);
 #pragma unroll
       for (int e = 0; e < 8; e++) {
         z[n][e] = __builtin_amdgcn_exp2f(z[n][e] - mu);
@@ -301,7 +297,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
 #pragma unroll
       for (int e = 0; e < 4; e++)
         pf[n][e] = CK == C16 ? pack16(z[n][2 * e], z[n][2 * e + 1], BF)
-                             : pack_f16(z[n][2 * e] * (vsc[2 * e] * scale_by[n]), z[n][2 * e + 1] * (vsc[2 * e + 1] * scale_by[n]));
+                             : pack_f16(z[n][2 * e] * (vsc[2 * e] * scale_by), z[n][2 * e + 1] * (vsc[2 * e + 1] * scale_by));
     }
 #pragma unroll
     for (int dt = 0; dt < DP / 16; dt++) {
