@@ -63,7 +63,6 @@ __device__ __forceinline__ int slot_of(const AppendArgs& a, int seq, int t) {
   return t >= s0 && t < s1 ? context_of(a.b, seq) + (t - s0) : -1;
 }
 
-__device__ __forceinline__ float inv_qmax(int type) { return type == T_INT8 ? 1.f / 127.f : 1.f / 448.f; }
 __device__ __forceinline__ float qmax(int type) { return type == T_INT8 ? 127.f : 448.f; }
 
 enum Form { ADJACENT, PARTIAL, HALVES, HALVES_PARTIAL };     // as in k_rope.hip, and halves of a part of the head
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(256) k_append(AppendArgs a, int lanes, Splits 
       uint8_t* out = static_cast<uint8_t*>(is_v[i] ? a.c.v : a.c.k) + place[i].at + hd[i] * a.c.head;
       if (in0) *reinterpret_cast<uint2*>(out + first_piece * 8) = codes8(y[0], mul, a.c.type);
       if (in1) *reinterpret_cast<uint2*>(out + second_piece * 8) = codes8(y[1], mul, a.c.type);
-      if (j == 0) (is_v[i] ? a.c.vs : a.c.ks)[place[i].sat + hd[i] * a.c.shead] = top * inv_qmax(a.c.type);
+      if (j == 0) (is_v[i] ? a.c.vs : a.c.ks)[place[i].sat + hd[i] * a.c.shead] = top / qmax(a.c.type);
     }
   }
 }
@@ -328,7 +327,7 @@ __global__ void __launch_bounds__(256) k_append_any(AppendArgs a, int64_t units)
   }
   top = fmaxf(group_max(top, 64), kTiny);
   if (have) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) = codes8(y, qmax(a.c.type) / top, a.c.type);
-  if (lane == 0) (is_v ? a.c.vs : a.c.ks)[pl.sat + hd * a.c.shead] = top * inv_qmax(a.c.type);
+  if (lane == 0) (is_v ? a.c.vs : a.c.ks)[pl.sat + hd * a.c.shead] = top / qmax(a.c.type);
 }
 
 bool wide(const AppendArgs& a) {
