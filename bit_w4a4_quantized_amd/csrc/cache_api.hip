@@ -19,6 +19,7 @@ inline bool is8(int t) { return t == SVDQ_TYPE_INT8 || t == SVDQ_TYPE_E4M3; }
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride; }
 inline bool eps_ok(float e) { return isfinite(e) && e > 0.f; }
+inline bool scale_ok(float s) { return s >= 0x1p-126f && s <= 0x1p126f; }     // its product with log2(e) is a normal number
 inline bool power_of_two(int n) { return n > 0 && (n & (n - 1)) == 0; }
 
 // Tiles of at least 16 rows: what 32-bit numbers of tiles and of their parts hold.
@@ -142,7 +143,7 @@ svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_
   svdq_status st = check_sizes(cache, batch, type);
   if (st != SVDQ_OK) return st;
   if (tokens < 0 || tokens > kMaxDim || heads < 1 || heads > kMaxHeads || heads % cache->heads) return SVDQ_ERR_SHAPE;
-  if ((int64_t)tokens * heads >= (int64_t)1 << 31 || !isfinite(scale) || scale <= 0.f) return SVDQ_ERR_SHAPE;
+  if ((int64_t)tokens * heads >= (int64_t)1 << 31 || !scale_ok(scale)) return SVDQ_ERR_SHAPE;
   if (!tiles_ok(tokens, heads, cache->heads, batch->sequences)) return SVDQ_ERR_SHAPE;
   for (const int64_t s : {q_token, q_head, out_token, out_head})
     if (!stride_ok(s)) return SVDQ_ERR_SHAPE;

@@ -560,7 +560,7 @@ svdq_status svdq_rope_append(const svdq_paged_cache* cache, const svdq_paged_bat
  *   q, out : [tokens, heads, dim] of `type` by their strides; heads a multiple of the cache's.  out may be q with
  *            the same strides.  Rows of tokens that belong to no sequence are left as they were.
  *   tokens * heads < 2^31, and (tokens * (heads / cache heads) / 16 + sequences) * cache heads <= 2^24.
- *   scale  : finite, > 0.
+ *   scale  : 2^-126 ... 2^126.
  *   tree   : bytes [tokens, tree_width], rows tree_stride apart, or NULL.
  * The work is cut by the mean number of rows of a sequence: long chunks and single tokens are best in calls of their own.
  * Logits, the softmax's statistics and sums are fp32; probabilities are rounded to 16 bits for the matrix
