@@ -70,9 +70,8 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
       qf[n][s] = v4u{0, 0, 0, 0};
       if (valid[n] && d < dim) __builtin_memcpy(&qf[n][s], q + d, 16);
     }
-    // a.scale is in K's scales in LDS with an 8-bit cache
-    coef[n] = CK == C16 ? a.scale : 1.f;
-    if (CK != C16 && a.qbf) coef[n] = queries_to_f16<kSteps, 16>(qf[n]);
+    coef[n] = a.scale;
+    if (CK != C16) coef[n] = power_of_two(scale_power(a) + (a.qbf ? queries_to_f16<kSteps, 16>(qf[n]) : 0));
   }
 
   v4f acc[NT][DP / 16];
@@ -170,7 +169,7 @@ __device__ __forceinline__ void attend(const AttnArgs& a, const Work& w, FewLds<
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();         // the last tile's reads of LDS are done
     if (CK != C16 && lane < 32) {
-      lds_s[wave][0][lane] = ks * a.scale;
+      lds_s[wave][0][lane] = ks * scale_factor(a);
       const bool infinite = masked && !(__builtin_fabsf(vs) < INFINITY);
       lds_s[wave][1][lane] = infinite ? 0.f : vs;
       sick = sick || infinite;

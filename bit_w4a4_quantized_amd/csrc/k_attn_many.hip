@@ -93,9 +93,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       if (valid && d < dim) __builtin_memcpy(&qf[s], q + d, 16);
     }
   }
-  // a logit is a sum of products times coef; with an 8-bit cache a power of two, a.scale being in K's scales in LDS
-  float coef = CK == C16 ? a.scale : 1.f;
-  if (CK != C16 && a.qbf) coef = queries_to_f16<kSteps, 32>(qf);
+  float coef = a.scale;
+  if (CK != C16) coef = power_of_two(scale_power(a) + (a.qbf ? queries_to_f16<kSteps, 32>(qf) : 0));
 
   v16f acc[kBlocks];
 #pragma unroll
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     if (wave == 0) {
       const float power = __builtin_amdgcn_logf(__builtin_fabsf(vsr)), most = wave_max(power);      // 0 past BN
       if (lane < BN) {
-        sc[0][lane] = ksr * a.scale;
+        sc[0][lane] = ksr * scale_factor(a);
         sc[1][lane] = vsr;
         sc[2][lane] = power;
       }

@@ -105,11 +105,17 @@ __device__ __forceinline__ float one_value(const uint8_t* row, int at) {
   return BF ? bf16_f32(b) : f16_f32(b);
 }
 
+// What a logit's sum of products is multiplied by is a.scale, apart in 8-bit caches: K's scales in LDS take a factor in
+// [1, 2), the sums a power of two, whose products are not rounded.
+__device__ __forceinline__ int scale_power(const AttnArgs& a) { return __builtin_amdgcn_frexp_expf(a.scale) - 1; }
+__device__ __forceinline__ float scale_factor(const AttnArgs& a) { return __builtin_ldexpf(a.scale, -scale_power(a)); }
+__device__ __forceinline__ float power_of_two(int e) { return __builtin_ldexpf(1.f, min(max(e, -126), 126)); }
+
 // A row of bf16 queries (its pieces lie in every NEAR-th lane: 16 or 32) as fp16, divided by
-// a power of two that brings its largest into [1, 2): exact for values down to 2^-14 of the largest and
-// within 2^-25 of it below.  Returns the power.
+// a power of two that brings its largest into [2^14, 2^15): exact for values down to 2^-28 of the largest and
+// within 2^-39 of it below.  Returns the power.
 template <int N, int NEAR>
-__device__ __forceinline__ float queries_to_f16(v4u* q) {
+__device__ __forceinline__ int queries_to_f16(v4u* q) {
   float top = 0.f;
 #pragma unroll
   for (int s = 0; s < N; s++)
@@ -118,13 +124,13 @@ __device__ __forceinline__ float queries_to_f16(v4u* q) {
       top = fmaxf(top, fmaxf(__builtin_fabsf(bf16_f32(q[s][i] & 0xFFFFu)), __builtin_fabsf(bf16_f32(q[s][i] >> 16))));
   if (NEAR == 16) top = fmaxf(top, __shfl_xor(top, 16));
   top = fmaxf(top, __shfl_xor(top, 32));
-  const int e = top > 0.f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 1 : 0;
+  const int e = top > 0.f && top < INFINITY ? __builtin_amdgcn_frexp_expf(top) - 15 : 0;
 #pragma unroll
   for (int s = 0; s < N; s++)
 #pragma unroll
     for (int i = 0; i < 4; i++)
       q[s][i] = pack_f16(__builtin_ldexpf(bf16_f32(q[s][i] & 0xFFFFu), -e), __builtin_ldexpf(bf16_f32(q[s][i] >> 16), -e));
-  return __builtin_ldexpf(1.f, e);
+  return e;
 }
 
 // Four values of each of two blocks of a matrix in LDS, turned: among 16 lanes, lane 4 r + p points at values

@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from strict import check  # noqa: E402
-from test_gpu_cache import (BF16, E4M3, EPS32, F16, F64, I8, QMAX, SMALL, U, Pages, _gpu, attend, gen,  # noqa: E402, F401
+from test_gpu_cache import (BF16, E4M3, EPS32, F16, F64, I8, QMAX, SMALL, U, Pages, _gpu, attend, attention64, gen,  # noqa: E402, F401
                             randn)
 
 KIND = [(F16, F16), (BF16, BF16), (F16, I8), (BF16, I8), (F16, E4M3), (BF16, E4M3)]
@@ -61,3 +61,38 @@ def test_logits_of_any_size(dtype, cache, n, group, dim, size):
     check(attend(p, q, None, scale=2.0 ** (size - 13)), want, tol, f"logits of 2^{size}")
     check(attend(p, -q, None, scale=2.0 ** (size - 13)),
           *mean_of(p, q, see & (mine == torch.where(see, mine, 9.0).amin(1, keepdim=True))), f"logits of -2^{size}")
+
+
+@pytest.mark.parametrize("n,group,dim", ROWS)
+@pytest.mark.parametrize("cache", [I8, E4M3])
+@pytest.mark.parametrize("power", [-130, -100, 0, 100, 126])
+def test_bf16_queries_keep_small_values(power, cache, n, group, dim):
+    """Over codes bf16 queries become fp16: values 2^-20 of a row's largest, which meets keys of zero, carry the logits."""
+    g = gen(171 + n + power)
+    p = Pages(g, [n], [60], 1, dim, cache, 16)
+    k = p.host["k"].float()
+    k[..., 0] = 0
+    put(p, "k", k, 2.0 ** (10 if power < 100 else -90))
+    q = randn(g, n, group, dim)
+    if power == -130:                        # steps of 2^-133
+        q = (8 * q).round() / 8
+    else:
+        q *= 2.0 ** -20
+        q[..., 0] = 1.0
+    q = (q * 2.0 ** power).to(BF16)
+    # logits of size one or so
+    scale = 2.0 ** min(110, max(-110, -power - (7 if cache is I8 else 9) + (20 if power != -130 else 0) - (10 if power < 100 else -90) - 3))
+    want, tol = attention64(p, q, None, scale, U[F16])
+    check(attend(p, q, None, scale=scale), want, tol, f"queries of 2^{power}")
+
+
+@pytest.mark.parametrize("n,group,dim", ROWS)
+@pytest.mark.parametrize("dtype,cache", KIND)
+def test_scales_at_the_ends(dtype, cache, n, group, dim):
+    """The largest and smallest scale with queries of zero."""
+    g = gen(181 + n)
+    p = Pages(g, [n], [60], 1, dim, cache, 16)
+    see = torch.arange(60 + n) <= 60 + torch.arange(n)[:, None]
+    for scale in (2.0 ** -126, 2.0 ** 126):
+        q = torch.zeros(n, group, dim, dtype=dtype)
+        check(attend(p, q, None, scale=scale), *mean_of(p, q, see), f"queries of zero, {scale}")
