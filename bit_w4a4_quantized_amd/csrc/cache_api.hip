@@ -178,6 +178,8 @@ svdq_status svdq_tree_attention(const svdq_paged_cache* cache, const svdq_paged_
   a.ids = p.ids;
   a.whole = p.whole;
   a.parts = p.parts;
+  a.group_inverse = group_inverse(a.group);
+  a.parts_inverse = p.parts > 1 ? parts_inverse(p.parts) : 0;
   a.part = static_cast<float*>(workspace);
   return map_launch(launch_attn(a, static_cast<hipStream_t>(stream)));
 }

@@ -36,9 +36,10 @@ __global__ void __launch_bounds__(256) k_attn_join(AttnArgs a, int deep) {
   Work w;
   w.id = -1;
   if (!find_tile<R>(a, tile, w)) return;     // the whole workgroup
-  int last, each;
-  share_keys<R>(a, w, a.parts, last, each);
-  const int parts = last > 0 ? (last + each - 1) / each : 0;       // that have keys
+  const Shares share = share_keys<R>(a, w, a.parts);
+  // parts that have keys: the quotient to within 2^-15, up
+  int parts = share.units ? (int)((float)share.units * __builtin_amdgcn_rcpf((float)share.each) + 0x1p-10f) : 0;
+  parts = __builtin_amdgcn_readfirstlane(parts + (parts * share.each < share.units));
   const bool valid = w.row0 + row < w.rows && d < dim;
   float m = -INFINITY, l = 0.f;
   v4f sum{0.f, 0.f, 0.f, 0.f};

@@ -1,4 +1,4 @@
-// Shared by the operators around a paged cache of keys and values (k_append.hip, k_attn_few.hip):
+// Shared by the operators around a paged cache of keys and values (cache_api.hip, k_append.hip, paged_attn.h):
 // the argument structs cache_api.hip fills, and how a kernel finds a token's sequence.
 #pragma once
 #include "block_ops.h"
@@ -32,6 +32,7 @@ struct AttnArgs {
   // `whole` tiles take all their keys at once, the others are cut into `parts` each, of whole units of `unit` keys, and
   // joined afterwards.
   int rows, slots, unit, whole, parts;
+  uint32_t group_inverse, parts_inverse;     // of group, and of parts past 1 (slots.h)
   int64_t ids;                               // of parts
   float* part;                               // fp32 [ids][rows][dim] sums, then [ids][rows][2]
 };

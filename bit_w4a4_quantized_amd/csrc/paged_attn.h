@@ -233,13 +233,23 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, Work& w) 
   return find_rows<R>(a, a.slots - 1 - tile / a.c.heads, w);
 }
 
-// How a tile's keys are shared among parts: up to `last`, `each` a part (a table wider than the contexts leaves the
-// last parts without any).
+// How a tile's keys are shared among its parts: keys up to `last`, `units` of a.unit, `each` of them a part (a table
+// wider than the contexts leaves the last parts without any).  The quotients by numbers from the host: k_attn_join waits for
+// them (by division 0.4 to 2 us a call).
+struct Shares {
+  int last, units, each;
+};
 template <int R>
-__device__ __forceinline__ void share_keys(const AttnArgs& a, const Work& w, int parts, int& last, int& each) {
-  last = a.tree ? w.keys : min(w.keys, w.ctx + min((w.row0 + R - 1) / a.group, w.n - 1) + 1);
-  each = (last + parts - 1) / parts;
-  each = (each + a.unit - 1) / a.unit * a.unit;
+__device__ __forceinline__ Shares share_keys(const AttnArgs& a, const Work& w, int parts) {
+  Shares s;
+  s.last = w.keys;
+  if (!a.tree) {
+    const int token = (int)group_quotient(w.row0 + R - 1, a.group, a.group_inverse);
+    s.last = min(w.keys, w.ctx + min(token, w.n - 1) + 1);
+  }
+  s.units = a.unit == 32 ? (s.last + 31) >> 5 : (s.last + 63) >> 6;
+  s.each = parts == 1 ? s.units : (int)high_product(s.units + parts - 1, a.parts_inverse);
+  return s;
 }
 
 // The workgroup's tile, or part of one that has keys.
@@ -264,10 +274,9 @@ __device__ __forceinline__ bool cut_work(const AttnArgs& a, Work& w) {
     if (parts > 1) w.id = (int64_t)(tile - a.whole) * parts + split;
   }
   if (!find_tile<R>(a, tile, w)) return false;
-  int last, each;
-  share_keys<R>(a, w, parts, last, each);
-  w.begin = (int)min((int64_t)last, (int64_t)split * each);
-  w.end = min(last, w.begin + each);
+  const Shares s = share_keys<R>(a, w, parts);
+  w.begin = min(s.last, split * s.each * a.unit);
+  w.end = min(s.last, w.begin + s.each * a.unit);
   return w.id < 0 || w.begin < w.end;
 }
 

@@ -51,4 +51,15 @@ SVDQ_BOTH inline int first_row_of(int64_t first, int slot, int R, int rows) {
   return row < 0 || row >= rows ? -1 : (int)row;
 }
 
+// Quotients by a number d that the host knows, without a division.  group_inverse: of any x below 2^31 + 2^8 by d up to
+// 2^16; the product is the quotient or one less.  parts_inverse: of x up to 2^25 + 127 by d in 2 ... 128; the excess
+// of the inverse, below d, adds less than one d-th.
+SVDQ_BOTH inline uint32_t high_product(uint32_t x, uint32_t y) { return (uint32_t)((uint64_t)x * y >> 32); }
+inline uint32_t group_inverse(int d) { return d == 1 ? 0xFFFFFFFFu : (uint32_t)(((uint64_t)1 << 32) / d); }
+inline uint32_t parts_inverse(int d) { return (uint32_t)((((uint64_t)1 << 32) + d - 1) / d); }
+SVDQ_BOTH inline uint32_t group_quotient(uint32_t x, uint32_t d, uint32_t inverse) {
+  const uint32_t q = high_product(x, inverse);
+  return x - q * d >= d ? q + 1 : q;
+}
+
 }  // namespace svdq

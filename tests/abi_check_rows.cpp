@@ -1,5 +1,6 @@
-// Which rows of attention a slot takes (bit_w4a4_quantized_amd/csrc/slots.h), for starts that hold anything: whatever
-// sequence is found for a slot, its rows are tokens and heads that there are.  Without a GPU.
+// Which rows of attention a slot takes, for starts that hold anything: whatever sequence is found for a slot, its rows are
+// tokens and heads that there are.  And the quotients that the kernels take without dividing.  Both from
+// bit_w4a4_quantized_amd/csrc/slots.h, without a GPU.
 #include <cstdint>
 #include <cstdio>
 #include <initializer_list>
@@ -49,6 +50,21 @@ int main() {
                   }
                 }
             }
+  // quotients by numbers from the host
+  uint32_t x = 1;
+  auto any = [&](uint32_t below) { return (x = x * 1664525u + 1013904223u) % below; };
+  for (int i = 0; i < 40000; i++) {
+    const uint32_t d = i < 300 ? i + 1 : i < 400 ? 65536 - (i - 300) : 1 + any(65536), most = (1u << 31) + 255;
+    const uint32_t q = any(most / d + 1) * d;
+    for (const uint32_t n : {0u, d - 1, d, q, q - (q > 0), q + d - 1 < most ? q + d - 1 : q, most, any(most)})
+      if (group_quotient(n, d, group_inverse((int)d)) != n / d) failures++;
+  }
+  for (uint32_t d = 2; d <= 128; d++)
+    for (int i = 0; i < 2000; i++) {
+      const uint32_t most = (1u << 25) + 127, q = any(most / d) * d;
+      for (const uint32_t n : {0u, d - 1, d, q, q + d - 1, q - (q > 0), most, most - 127, any(most)})
+        if (high_product(n, parts_inverse((int)d)) != n / d) failures++;
+    }
   std::printf("%s: %d failure(s), %d of %d tiles with rows\n", failures ? "FAILED" : "OK", failures, owned, tiles);
   return failures ? 1 : 0;
 }
