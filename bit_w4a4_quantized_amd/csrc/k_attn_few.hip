@@ -8,7 +8,7 @@
 //
 // The cache's bytes bound it (64 sequences over up to 8000 int8 keys of 8 heads of 128, 812 MB: 168 us, 4.8 TB/s, the
 // rate of a large copy; one over 131072 E4M3 keys, 277 MB: 64 us), the loads' latency where it is short (1000 bf16 keys:
-// 8.6 us).  A row is a token and one of the `group` query heads that share a cache head;
+// 8.4 us).  A row is a token and one of the `group` query heads that share a cache head;
 // a workgroup has 16 NT rows of one sequence and cache head and a part of the keys, its waves take turns at
 // tiles of 32 keys, each with sums of its own, joined at the end through LDS and over the parts by
 // k_attn_join.  Nothing is shared between the waves in between, so there is no barrier in the loop and the

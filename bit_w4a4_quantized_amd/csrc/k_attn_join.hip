@@ -144,8 +144,8 @@ AttnPlan attn_plan(int sequences, int tokens, int heads, int kv_heads, int dim, 
     // Empty tiles lie evenly among the numbers: `rest` tiles with rows are in about rest * all / tiles of them.  All parts
     // together are at most three rounds of workgroups, and so are the sums that they leave (65 trees of 9 over 2000 in
     // 32 on 8 heads, 520 tiles in 664 numbers: 10 numbers cut 16 ways 152 us, none cut 145; the 152 behind the first 512 cut
-    // 64 ways 261).  `reach` is the table's width, which the contexts may be far below (112 x 9 over 2000: 180 us in a
-    // table for 2048 keys, 215 in one for 32768).
+    // 64 ways 261).  `reach` is the table's width, which the contexts may be far below (112 x 9 over 2000: 179 us in a
+    // table for 2048 keys, 213 in one for 32768).
     const int64_t rest = tiles % resident, cut = tiles < resident ? all : (rest * all + tiles - 1) / tiles;
     const double early = tiles > resident ? 0.5 : 0.0;
     const double join = reach > 0 ? (1.1 * rest + 722.0 / dim) / reach : 0.0;

@@ -1,7 +1,7 @@
 // Attention of a step's tokens over a paged cache (svdq_tree_attention), for many rows a cache head: large trees
 // and chunks of prompts.  The mathematics is k_attn_few's; here the matrix cores bound it
-// (with the exponentials: a chunk of 4096 over 12288 bf16 keys of 24 heads of 128, 722 GFLOP: 740 to 795 us, 910 to
-// 975 TFLOP/s, matrix cores busy for half of it; over an E4M3 cache 1250), and the loads of few keys' tiles.
+// (with the exponentials: a chunk of 4096 over 12288 bf16 keys of 24 heads of 128, 722 GFLOP: 730 to 790 us, 915 to
+// 990 TFLOP/s, matrix cores busy for half of it; over an E4M3 cache 990 to 1030), and the loads of few keys' tiles.
 //
 // A workgroup has 128 rows of one sequence and cache head (and a part of the keys), each of its four waves 32 of
 // them; all four share tiles of 64 keys (32 of heads past 128), which come to LDS by loads of their own while the tile before is in work
