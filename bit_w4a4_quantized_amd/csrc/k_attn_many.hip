@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       }
     }
     if (wave == 0) {
-      const float power = __builtin_amdgcn_logf(__builtin_fabsf(vsr)), most = wave_max(power);      // 0 past BN
+      const float power = __builtin_amdgcn_logf(__builtin_fabsf(vsr)), most = wave_max(power);      // (of zero past BN)
       if (lane < BN) {
         sc[0][lane] = ksr * scale_factor(a);
         sc[1][lane] = vsr;
@@ -375,12 +375,11 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       // The powers below take a logit's product and m in one rounding, m the rounded product of the largest: apart by up
       // to half a step of it, which must stay small.  (Products with a power of two are not rounded.)
       if (far) {
-        const float back = __builtin_amdgcn_rcpf(coef);
 #pragma unroll
-        for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = (st[e >> 4][e & 15] * coef - m) * back;
+        for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = st[e >> 4][e & 15] * coef - m;
       }
     }
-    const float mu = m == -INFINITY || far ? 0.f : m;
+    const float mu = m == -INFINITY || far ? 0.f : m, times = far ? 1.f : coef;
     const float scale_by = CK == C16 ? 1.f : __builtin_amdgcn_exp2f(-r_v);
     float part[4] = {0.f, 0.f, 0.f, 0.f};
     v4f sv[2];                               // scales of V of the lane's half of sixteen keys, read ahead of their powers
@@ -392,8 +391,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to 2^(m + r), as in k_attn_few.
     auto power = [&](int u, int x) {
       const int e = 8 * u + 2 * x;
-      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], coef, -mu));
-      const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][(e & 15) + 1], coef, -mu));
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], times, -mu));
+      const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][(e & 15) + 1], times, -mu));
       part[x] += p + q;
       pf[u & 1][x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (sv[x >> 1][2 * (x & 1)] * scale_by), q * (sv[x >> 1][2 * (x & 1) + 1] * scale_by));
     };

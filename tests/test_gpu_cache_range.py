@@ -96,3 +96,22 @@ def test_scales_at_the_ends(dtype, cache, n, group, dim):
     for scale in (2.0 ** -126, 2.0 ** 126):
         q = torch.zeros(n, group, dim, dtype=dtype)
         check(attend(p, q, None, scale=scale), *mean_of(p, q, see), f"queries of zero, {scale}")
+
+
+@pytest.mark.parametrize("n,group,dim", ROWS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_far_logits_by_the_largest_scale(dtype, n, group, dim):
+    """Logits of 0 to 3 times 2^115 from queries of 2^-14 and a scale of 2^126."""
+    g = gen(191 + n)
+    p = Pages(g, [n], [150], 1, dim, dtype, 16)
+    k = torch.zeros(p.pages, 16, 1, dim)
+    level = torch.randint(0, 4, (p.pages, 16, 1), generator=g).float()
+    k[..., 0] = 8 * level
+    put(p, "k", k)
+    q = torch.zeros(n, group, dim, dtype=dtype)
+    q[..., 0] = 2.0 ** -14
+    keys = torch.arange(150 + n)
+    mine = level[p.table[0][keys // 16].long(), keys % 16, 0]
+    see = keys <= 150 + torch.arange(n)[:, None]
+    top = torch.where(see, mine, -1.0).amax(1, keepdim=True)
+    check(attend(p, q, None, scale=2.0 ** 126), *mean_of(p, q, see & (mine == top)), "far logits")
