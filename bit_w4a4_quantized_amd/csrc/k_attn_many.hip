@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
 #pragma unroll
     for (int i = 0; i < 16; i++) acc[d][i] = 0.f;
   float m = -INFINITY, l = 0.f, r_v = 0.f;
+  bool far_rows = false;                     // some row of the wave has its reference at kFar or beyond (16-bit caches)
 
   constexpr int es = CK == C16 ? 2 : 1;
   const uint8_t* kbase = static_cast<const uint8_t*>(a.c.k) + w.head * a.c.head * es;
@@ -344,15 +345,13 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
 #pragma unroll
     for (int e = 0; e < 16 * NB; e++) top = fmaxf(top, st[e >> 4][e & 15]);
     top *= coef;
-    auto is_far = [](float x) { return CK == C16 && __builtin_fabsf(x) >= kFar && x > -INFINITY; };
     constexpr bool kLands = CK == C16 && !BF;
-    bool move = top - m > (kLands ? kLand : 0.f) + kSlack, far = is_far(top);
+    bool move = top - m > (kLands ? kLand : 0.f) + kSlack, far = false;
     if (CK != C16) move = move || ((top - m) + sc[2][CK == C16 ? 0 : BN]) - r_v > kLand + kSlack;      // a bound of the products
-    if (__any(move || far)) {
+    if (__any(move) || far_rows) {
       // rounded as the bound is, which the products then never pass
 #pragma clang fp contract(off)
       top = fmaxf(top, __shfl_xor(top, 32));
-      far = is_far(top);
       const float old = m, sum_by = move_powers<kLands>(top, m);
       float by = sum_by;
       if (CK != C16) {
@@ -374,12 +373,18 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
       for (int d = 0; d < kBlocks; d++) acc[d] *= by;
       // The powers below take a logit's product and m in one rounding, m the rounded product of the largest: apart by up
       // to half a step of it, which must stay small.  (Products with a power of two are not rounded.)
-      if (far) {
+      if (CK == C16) {
+        far = __builtin_fabsf(m) >= kFar && m > -INFINITY;
+        far_rows = __any(far);
+        if (far) {
+          // (1 / coef may lie below the normal numbers)
+          const float back = __builtin_ldexpf(__builtin_amdgcn_rcpf(__builtin_ldexpf(coef, -64)), -64);
 #pragma unroll
-        for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = st[e >> 4][e & 15] * coef - m;
+          for (int e = 0; e < 16 * NB; e++) st[e >> 4][e & 15] = (st[e >> 4][e & 15] * coef - m) * back;
+        }
       }
     }
-    const float mu = m == -INFINITY || far ? 0.f : m, times = far ? 1.f : coef;
+    const float mu = m == -INFINITY || far ? 0.f : m;
     const float scale_by = CK == C16 ? 1.f : __builtin_amdgcn_exp2f(-r_v);
     float part[4] = {0.f, 0.f, 0.f, 0.f};
     v4f sv[2];                               // scales of V of the lane's half of sixteen keys, read ahead of their powers
@@ -391,8 +396,8 @@ __global__ void __launch_bounds__(256, DP == 256 ? 1 : 2) k_attn_many(AttnArgs a
     // Two of sixteen keys' powers: rounded to 16 bits, with V's scales relative to 2^(m + r), as in k_attn_few.
     auto power = [&](int u, int x) {
       const int e = 8 * u + 2 * x;
-      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], times, -mu));
-      const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][(e & 15) + 1], times, -mu));
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][e & 15], coef, -mu));
+      const float q = __builtin_amdgcn_exp2f(__builtin_fmaf(st[e >> 4][(e & 15) + 1], coef, -mu));
       part[x] += p + q;
       pf[u & 1][x] = CK == C16 ? pack16(p, q, BF) : pack_f16(p * (sv[x >> 1][2 * (x & 1)] * scale_by), q * (sv[x >> 1][2 * (x & 1) + 1] * scale_by));
     };
